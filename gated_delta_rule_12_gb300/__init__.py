@@ -17,6 +17,13 @@ Entry points (same names as the C ABI, without the ``gdn_`` prefix):
     chunk_fwd_workspace_size(...)         -> bytes
     chunk_fwd_kernel_count(...)           -> kernels one chunk_fwd call launches
     chunk_bwd(q, k, v, g, beta, dout, ...) -> (dq, dk, dv, dg, dbeta, dinit_state)
+    gated_scan_fwd(x, g, ...)             -> (out, final_state)   per-channel gated linear recurrence
+    gated_scan_bwd(x, g, out, dout, ...)  -> (dx, dg, dinit_state)
+    gated_scan_step(state, x, g)          -> out            (state updated in place)
+    layer_norm_fwd(x, weight, bias, eps)  -> (out, mean, rstd)
+    layer_norm_bwd(dout, x, mean, rstd, weight) -> (dx, dweight, dbias)
+    linear_cross_entropy_fwd(h, weight, targets) -> (loss, lse)   no logits array
+    linear_cross_entropy_bwd(h, weight, targets, lse, dloss) -> (dh, dweight)
     check_device_error(workspace)         -> None or raises
 """
 from __future__ import annotations
@@ -39,7 +46,10 @@ CHUNK = 64
 EXPORTS = ["gdn_status_string", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd_kernel_count", "gdn_chunk_fwd",
            "gdn_chunk_bwd_workspace_size", "gdn_chunk_bwd", "gdn_decode_step", "gdn_decode_multi", "gdn_prologue",
            "gdn_check_device_error", "gdn_chunk_fwd_noalloc", "gdn_prologue_chunk_fwd_workspace_size",
-           "gdn_prologue_chunk_fwd"]
+           "gdn_prologue_chunk_fwd", "gdn_gated_scan_fwd", "gdn_gated_scan_bwd", "gdn_gated_scan_step",
+           "gdn_layer_norm_fwd", "gdn_layer_norm_bwd_workspace_size", "gdn_layer_norm_bwd",
+           "gdn_linear_cross_entropy_workspace_size", "gdn_linear_cross_entropy_fwd",
+           "gdn_linear_cross_entropy_bwd"]
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -107,6 +117,21 @@ def load_library(path: str = LIB_PATH, build_if_missing: bool = False) -> ctypes
         lib.gdn_prologue_chunk_fwd.argtypes = [_vp] * 13 + [_vp, _i32, _vp, _vp] + [_i32] * 6 + \
             [ctypes.c_int, _f32, _i32, _i32, _vp, _sz, _vp]
         lib.gdn_prologue_chunk_fwd.restype = ctypes.c_int
+        _ci = ctypes.c_int
+        lib.gdn_gated_scan_fwd.argtypes = [_vp] * 4 + [_i32, _vp, _vp] + [_i32] * 3 + [_ci, _i32, _vp]
+        lib.gdn_gated_scan_bwd.argtypes = [_vp] * 7 + [_i32] + [_vp] * 3 + [_i32] * 3 + [_ci, _i32, _vp]
+        lib.gdn_gated_scan_step.argtypes = [_vp] * 4 + [_i32] * 2 + [_ci, _i32, _vp]
+        lib.gdn_layer_norm_fwd.argtypes = [_vp] * 6 + [ctypes.c_int64, _i32, _ci, _f32, _vp]
+        lib.gdn_layer_norm_bwd_workspace_size.argtypes = [ctypes.c_int64, _i32, _ci]
+        lib.gdn_layer_norm_bwd_workspace_size.restype = _sz
+        lib.gdn_layer_norm_bwd.argtypes = [_vp] * 8 + [ctypes.c_int64, _i32, _ci, _vp, _sz, _vp]
+        lib.gdn_linear_cross_entropy_workspace_size.argtypes = [_i32] * 3 + [_ci, _i32]
+        lib.gdn_linear_cross_entropy_workspace_size.restype = _sz
+        lib.gdn_linear_cross_entropy_fwd.argtypes = [_vp] * 5 + [_i32] * 3 + [_ci, _vp, _sz, _vp]
+        lib.gdn_linear_cross_entropy_bwd.argtypes = [_vp] * 7 + [_i32] * 3 + [_ci, _vp, _sz, _vp]
+        for name in ("gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "layer_norm_fwd", "layer_norm_bwd",
+                     "linear_cross_entropy_fwd", "linear_cross_entropy_bwd"):
+            getattr(lib, "gdn_" + name).restype = _ci
         _lib = lib
         return lib
 
@@ -390,6 +415,236 @@ def prologue_chunk_fwd(xq, xk, xv, wq, wk, wv, a, b, A_log, dt_bias, conv_state_
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_prologue_chunk_fwd")
     return out, final_state
+
+
+def _check_scan_args(x, g, cu_seqlens, dtype, states, same):
+    """Shapes, dtypes, placement and contiguity of a gated-scan call; returns (B, T, D, N).  ``states`` are the
+    [N,D] fp32 tensors, ``same`` further tensors that must match g."""
+    if g.dim() != 3:
+        raise ValueError("x and g must be [B,T,D]")
+    B, T, D = g.shape
+    N = B
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32:
+            raise TypeError("cu_seqlens must be int32")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or B != 1:
+            raise ValueError("cu_seqlens must be [N+1] with N >= 1, and B = 1")
+        N = cu_seqlens.numel() - 1
+    for t in (x, g, *same):
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError("x, g and the other token tensors must share one dtype")
+        if t.shape != g.shape:
+            raise ValueError("x, g and the other token tensors must share one shape")
+    for t in states:
+        if t is None:
+            continue
+        if t.dtype != torch.float32:
+            raise TypeError("states must be float32")
+        if tuple(t.shape) != (N, D):
+            raise ValueError(f"states must be [N,D] = {(N, D)}")
+    _need_cuda(x, g, cu_seqlens, *states, *same)
+    return B, T, D, N
+
+
+def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, input_gate=False, out=None, final_state=None,
+                   output_final_state=True, stream=None):
+    """Per-channel gated linear recurrence (``gdn_gated_scan_fwd``): h_t = a_t h_{t-1} + c_t x_t with a = exp(g)
+    and c = 1, or 1 - a with ``input_gate``.
+
+    x, g [B,T,D] (fp32 or bf16, one dtype); init_state [N,D] fp32 or None; cu_seqlens int32 [N+1] (device) or
+    None.  Returns ``(out, final_state)``; final_state is None if not requested.
+    """
+    lib = _lib or load_library()
+    B, T, D, N = _check_scan_args(x, g, cu_seqlens, x.dtype, (init_state, final_state), (x, out))
+    if out is None:
+        out = torch.empty_like(x)
+    if final_state is None and output_final_state:
+        final_state = torch.empty((N, D), dtype=torch.float32, device=x.device)
+    rc = lib.gdn_gated_scan_fwd(x.data_ptr(), g.data_ptr(), _ptr(init_state), _ptr(cu_seqlens),
+                                N if cu_seqlens is not None else 0, out.data_ptr(), _ptr(final_state), B, T, D,
+                                _dt(x), int(bool(input_gate)), _stream(stream))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_gated_scan_fwd")
+    return out, final_state
+
+
+def gated_scan_bwd(x, g, out, dout, init_state=None, dfinal_state=None, cu_seqlens=None, input_gate=False,
+                   want_dinit=True, stream=None):
+    """Backward of ``gated_scan_fwd`` (``gdn_gated_scan_bwd``): returns ``(dx, dg, dinit_state)`` for the loss
+    gradients ``dout`` [B,T,D] and ``dfinal_state`` [N,D] (or None).  ``out`` is the forward's output; ``x`` may be
+    None without ``input_gate``."""
+    lib = _lib or load_library()
+    if input_gate and x is None:
+        raise ValueError("gated_scan_bwd: x is needed with the input gate")
+    B, T, D, N = _check_scan_args(x, g, cu_seqlens, g.dtype, (init_state, dfinal_state), (out, dout))
+    dx, dg = torch.empty_like(g), torch.empty_like(g)
+    dinit = torch.empty((N, D), dtype=torch.float32, device=g.device) if want_dinit else None
+    rc = lib.gdn_gated_scan_bwd(_ptr(x), g.data_ptr(), out.data_ptr(), dout.data_ptr(), _ptr(init_state),
+                                _ptr(dfinal_state), _ptr(cu_seqlens), N if cu_seqlens is not None else 0,
+                                dx.data_ptr(), dg.data_ptr(), _ptr(dinit), B, T, D, _dt(g), int(bool(input_gate)),
+                                _stream(stream))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_gated_scan_bwd")
+    return dx, dg, dinit
+
+
+def gated_scan_step(state, x, g, input_gate=False, out=None, stream=None):
+    """One token of the gated scan per sequence (``gdn_gated_scan_step``); ``state`` [N,D] fp32 is updated in
+    place.  x, g [N,D] (fp32 or bf16).  Returns out [N,D]."""
+    lib = _lib or load_library()
+    if state.dim() != 2 or x.shape != state.shape or g.shape != state.shape or (out is not None and
+                                                                                out.shape != state.shape):
+        raise ValueError("gated_scan_step: state, x, g and out must be [N,D]")
+    if state.dtype != torch.float32:
+        raise TypeError("state must be float32")
+    if out is None:
+        out = torch.empty_like(x)
+    if g.dtype != x.dtype or out.dtype != x.dtype:
+        raise TypeError("x, g and out must share one dtype")
+    _need_cuda(state, x, g, out)
+    N, D = state.shape
+    rc = lib.gdn_gated_scan_step(state.data_ptr(), x.data_ptr(), g.data_ptr(), out.data_ptr(), N, D, _dt(x),
+                                 int(bool(input_gate)), _stream(stream))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_gated_scan_step")
+    return out
+
+
+def _check_norm_args(x, params, stats, same):
+    """Shapes, dtypes, placement and contiguity of a layer-norm call; returns (rows, D)."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., D] with D >= 1")
+    D = x.shape[-1]
+    rows = x.numel() // D
+    for t in params:
+        if t is not None and t.dtype != torch.float32:
+            raise TypeError("weight and bias must be float32")
+        if t is not None and tuple(t.shape) != (D,):
+            raise ValueError("weight and bias must be [D]")
+    for t in stats:
+        if t.dtype != torch.float32:
+            raise TypeError("mean and rstd must be float32")
+        if t.numel() != rows:
+            raise ValueError("mean and rstd must hold one value a row")
+    for t in same:
+        if t is not None and t.dtype != x.dtype:
+            raise TypeError("x and the other row tensors must share one dtype")
+        if t is not None and t.shape != x.shape:
+            raise ValueError("x and the other row tensors must share one shape")
+    _need_cuda(x, *params, *stats, *same)
+    return rows, D
+
+
+def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
+    """Layer norm over the last axis (``gdn_layer_norm_fwd``).  x [..., D] (fp32 or bf16); weight, bias [D] fp32 or
+    None.  Returns ``(out, mean, rstd)``, the statistics fp32 of shape ``x.shape[:-1]``."""
+    lib = _lib or load_library()
+    rows, D = _check_norm_args(x, (weight, bias), (), (out,))
+    dt = _dt(x)
+    if out is None:
+        out = torch.empty_like(x)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    rc = lib.gdn_layer_norm_fwd(x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), mean.data_ptr(),
+                                rstd.data_ptr(), rows, D, dt, float(eps), _stream(stream))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_layer_norm_fwd")
+    return out, mean, rstd
+
+
+def layer_norm_bwd_workspace_size(rows, D, dtype=torch.bfloat16) -> int:
+    dt = GDN_BF16 if dtype == torch.bfloat16 else GDN_F32
+    return int(load_library().gdn_layer_norm_bwd_workspace_size(rows, D, dt))
+
+
+def layer_norm_bwd(dout, x, mean, rstd, weight=None, workspace=None, stream=None):
+    """Backward of ``layer_norm_fwd`` (``gdn_layer_norm_bwd``): returns ``(dx, dweight, dbias)``, the last two [D]
+    fp32.  ``mean`` and ``rstd`` are the forward's."""
+    lib = _lib or load_library()
+    rows, D = _check_norm_args(x, (weight,), (mean, rstd), (dout,))
+    dt = _dt(x)
+    dx = torch.empty_like(x)
+    dw = torch.empty(D, dtype=torch.float32, device=x.device)
+    db = torch.empty_like(dw)
+    if workspace is None:
+        workspace = torch.empty(max(256, lib.gdn_layer_norm_bwd_workspace_size(rows, D, dt)), dtype=torch.uint8,
+                                device=x.device)
+    _need_cuda(workspace)
+    rc = lib.gdn_layer_norm_bwd(dout.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
+                                dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, D, dt, workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_layer_norm_bwd")
+    return dx, dw, db
+
+
+def _check_ce_args(h, weight, targets, rows):
+    if h.dim() != 2 or weight.dim() != 2 or h.shape[1] != weight.shape[1]:
+        raise ValueError("h must be [N,D] and weight [V,D]")
+    if weight.dtype != h.dtype:
+        raise TypeError("h and weight must share one dtype")
+    if targets.dtype != torch.int32:
+        raise TypeError("targets must be int32")
+    if tuple(targets.shape) != (h.shape[0],):
+        raise ValueError("targets must be [N]")
+    for t in rows:
+        if t.dtype != torch.float32:
+            raise TypeError("lse and dloss must be float32")
+        if tuple(t.shape) != (h.shape[0],):
+            raise ValueError("lse and dloss must be [N]")
+    _need_cuda(h, weight, targets, *rows)
+    return h.shape[0], h.shape[1], weight.shape[0]
+
+
+def linear_cross_entropy_workspace_size(N, D, V, dtype=torch.bfloat16, backward=False) -> int:
+    dt = GDN_BF16 if dtype == torch.bfloat16 else GDN_F32
+    return int(load_library().gdn_linear_cross_entropy_workspace_size(N, D, V, dt, int(bool(backward))))
+
+
+def linear_cross_entropy_fwd(h, weight, targets, workspace=None, stream=None):
+    """Softmax cross entropy of the logits ``h @ weight.T`` without forming them
+    (``gdn_linear_cross_entropy_fwd``).
+
+    h [N,D], weight [V,D] (fp32 or bf16); targets int32 [N], rows with a target outside [0,V) are ignored.
+    Returns ``(loss, lse)``, both [N] fp32 and 0 in ignored rows.
+    """
+    lib = _lib or load_library()
+    N, D, V = _check_ce_args(h, weight, targets, ())
+    dt = _dt(h)
+    loss = torch.empty(N, dtype=torch.float32, device=h.device)
+    lse = torch.empty_like(loss)
+    if workspace is None:
+        workspace = torch.empty(max(256, lib.gdn_linear_cross_entropy_workspace_size(N, D, V, dt, 0)),
+                                dtype=torch.uint8, device=h.device)
+    _need_cuda(workspace)
+    rc = lib.gdn_linear_cross_entropy_fwd(h.data_ptr(), weight.data_ptr(), targets.data_ptr(), loss.data_ptr(),
+                                          lse.data_ptr(), N, D, V, dt, workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_linear_cross_entropy_fwd")
+    return loss, lse
+
+
+def linear_cross_entropy_bwd(h, weight, targets, lse, dloss, workspace=None, stream=None):
+    """Gradient of ``linear_cross_entropy_fwd`` (``gdn_linear_cross_entropy_bwd``) for the gradient ``dloss`` [N]
+    fp32 of each row's loss: returns ``(dh, dweight)`` in the dtype of h.  ``lse`` is the forward's."""
+    lib = _lib or load_library()
+    N, D, V = _check_ce_args(h, weight, targets, (lse, dloss))
+    dt = _dt(h)
+    dh, dw = torch.empty_like(h), torch.empty_like(weight)
+    if workspace is None:
+        workspace = torch.empty(max(256, lib.gdn_linear_cross_entropy_workspace_size(N, D, V, dt, 1)),
+                                dtype=torch.uint8, device=h.device)
+    _need_cuda(workspace)
+    rc = lib.gdn_linear_cross_entropy_bwd(h.data_ptr(), weight.data_ptr(), targets.data_ptr(), lse.data_ptr(),
+                                          dloss.data_ptr(), dh.data_ptr(), dw.data_ptr(), N, D, V, dt,
+                                          workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                          _stream(stream))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_linear_cross_entropy_bwd")
+    return dh, dw
 
 
 def check_device_error(workspace, stream=None):

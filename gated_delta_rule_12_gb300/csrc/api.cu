@@ -353,6 +353,181 @@ gdn_status gdn_prologue_chunk_fwd(const void *xq, const void *xk, const void *xv
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+static gdn_status scan_geometry(GatedScanArgs &a, const int32_t *cu_seqlens, int32_t num_seqs, int32_t B, int32_t T,
+                                int32_t D, gdn_dtype dt, int32_t input_gate)
+{
+    if (B < 1 || T < 0 || D < 1) return GDN_ERR_INVALID_ARG;
+    if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (cu_seqlens ? (B != 1 || num_seqs < 1) : (num_seqs != 0 && num_seqs != B)) return GDN_ERR_INVALID_ARG;
+    if (!aligned_to(cu_seqlens, 4)) return GDN_ERR_INVALID_ARG;
+    a = GatedScanArgs();
+    a.cu = cu_seqlens;
+    a.N = cu_seqlens ? num_seqs : B;
+    a.T = T; a.D = D;
+    a.dt = (dt == GDN_BF16) ? 1 : 0;
+    a.input_gate = input_gate ? 1 : 0;
+    return GDN_OK;
+}
+
+gdn_status gdn_gated_scan_fwd(const void *x, const void *g, const float *init_state, const int32_t *cu_seqlens,
+                              int32_t num_seqs, void *out, float *final_state, int32_t B, int32_t T, int32_t D,
+                              gdn_dtype dt, int32_t input_gate, void *stream)
+{
+    GatedScanArgs a;
+    const gdn_status s = scan_geometry(a, cu_seqlens, num_seqs, B, T, D, dt, input_gate);
+    if (s != GDN_OK) return s;
+    const bool have_tokens = (int64_t)B * T > 0;
+    if (have_tokens && (!x || !g || !out)) return GDN_ERR_INVALID_ARG;
+    const unsigned esz = (dt == GDN_BF16) ? 2u : 4u;
+    if (!aligned_to(x, esz) || !aligned_to(g, esz) || !aligned_to(out, esz) || !aligned_to(init_state, 4) ||
+        !aligned_to(final_state, 4))
+        return GDN_ERR_INVALID_ARG;
+    if (!have_tokens && !final_state) return GDN_OK;
+    a.x = x; a.g = g; a.init_state = init_state; a.out = out; a.final_state = final_state;
+    return launch_gated_scan_fwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_gated_scan_bwd(const void *x, const void *g, const void *out, const void *dout,
+                              const float *init_state, const float *dfinal_state, const int32_t *cu_seqlens,
+                              int32_t num_seqs, void *dx, void *dg, float *dinit_state, int32_t B, int32_t T,
+                              int32_t D, gdn_dtype dt, int32_t input_gate, void *stream)
+{
+    GatedScanArgs a;
+    const gdn_status s = scan_geometry(a, cu_seqlens, num_seqs, B, T, D, dt, input_gate);
+    if (s != GDN_OK) return s;
+    const bool have_tokens = (int64_t)B * T > 0;
+    if (have_tokens && ((input_gate && !x) || !g || !out || !dout || !dx || !dg)) return GDN_ERR_INVALID_ARG;
+    const unsigned esz = (dt == GDN_BF16) ? 2u : 4u;
+    const void *elems[] = {x, g, out, dout, dx, dg};
+    for (const void *p : elems)
+        if (!aligned_to(p, esz)) return GDN_ERR_INVALID_ARG;
+    if (!aligned_to(init_state, 4) || !aligned_to(dfinal_state, 4) || !aligned_to(dinit_state, 4))
+        return GDN_ERR_INVALID_ARG;
+    if (!have_tokens && !dinit_state) return GDN_OK;
+    a.x = x; a.g = g; a.h = out; a.dout = dout; a.init_state = init_state; a.dfinal = dfinal_state;
+    a.dx = dx; a.dg = dg; a.dinit = dinit_state;
+    return launch_gated_scan_bwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_gated_scan_step(float *state, const void *x, const void *g, void *out, int32_t N, int32_t D,
+                               gdn_dtype dt, int32_t input_gate, void *stream)
+{
+    if (N < 0 || D < 1) return GDN_ERR_INVALID_ARG;
+    if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (N == 0) return GDN_OK;
+    const unsigned esz = (dt == GDN_BF16) ? 2u : 4u;
+    if (!state || !x || !g || !out || !aligned_to(state, 4) || !aligned_to(x, esz) || !aligned_to(g, esz) ||
+        !aligned_to(out, esz))
+        return GDN_ERR_INVALID_ARG;
+    const cudaError_t e = launch_gated_scan_step(state, x, g, out, (int64_t)N * D, (dt == GDN_BF16) ? 1 : 0,
+                                                 input_gate ? 1 : 0, (cudaStream_t)stream);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_layer_norm_fwd(const void *x, const float *weight, const float *bias, void *out, float *mean,
+                              float *rstd, int64_t rows, int32_t D, gdn_dtype dt, float eps, void *stream)
+{
+    if (rows < 0 || D < 1 || !(eps >= 0.f)) return GDN_ERR_INVALID_ARG;
+    if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (rows > ((int64_t)1 << 48) / D) return GDN_ERR_INVALID_ARG;
+    if (rows == 0) return GDN_OK;
+    const unsigned esz = (dt == GDN_BF16) ? 2u : 4u;
+    if (!x || !out || !aligned_to(x, esz) || !aligned_to(out, esz)) return GDN_ERR_INVALID_ARG;
+    const void *ptrs4[] = {weight, bias, mean, rstd};
+    for (const void *p : ptrs4)
+        if (!aligned_to(p, 4)) return GDN_ERR_INVALID_ARG;
+    LayerNormArgs a = LayerNormArgs();
+    a.x = x; a.weight = weight; a.bias = bias; a.out = out; a.mean = mean; a.rstd = rstd;
+    a.rows = rows; a.D = D; a.dt = (dt == GDN_BF16) ? 1 : 0; a.eps = eps;
+    return launch_layer_norm_fwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_layer_norm_bwd_workspace_size(int64_t rows, int32_t D, gdn_dtype dt)
+{
+    if (rows < 0 || D < 1 || (dt != GDN_F32 && dt != GDN_BF16) || rows > ((int64_t)1 << 48) / D) return 0;
+    return layer_norm_bwd_workspace_bytes(rows, D, (dt == GDN_BF16) ? 1 : 0);
+}
+
+gdn_status gdn_layer_norm_bwd(const void *dout, const void *x, const float *mean, const float *rstd,
+                              const float *weight, void *dx, float *dweight, float *dbias, int64_t rows, int32_t D,
+                              gdn_dtype dt, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (rows < 0 || D < 1) return GDN_ERR_INVALID_ARG;
+    if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (rows > ((int64_t)1 << 48) / D) return GDN_ERR_INVALID_ARG;
+    const unsigned esz = (dt == GDN_BF16) ? 2u : 4u;
+    if (rows > 0 && (!dout || !x || !mean || !rstd)) return GDN_ERR_INVALID_ARG;
+    if (!aligned_to(dout, esz) || !aligned_to(x, esz) || !aligned_to(dx, esz)) return GDN_ERR_INVALID_ARG;
+    const void *ptrs4[] = {mean, rstd, weight, dweight, dbias};
+    for (const void *p : ptrs4)
+        if (!aligned_to(p, 4)) return GDN_ERR_INVALID_ARG;
+    if (!workspace || ((uintptr_t)workspace & 255u) != 0) return GDN_ERR_WORKSPACE;
+    if (workspace_bytes < gdn_layer_norm_bwd_workspace_size(rows, D, dt)) return GDN_ERR_WORKSPACE;
+    LayerNormArgs a = LayerNormArgs();
+    a.dout = dout; a.x = x; a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd);
+    a.weight = weight; a.dx = dx; a.dweight = dweight; a.dbias = dbias;
+    a.rows = rows; a.D = D; a.dt = (dt == GDN_BF16) ? 1 : 0;
+    a.workspace = workspace;
+    return launch_layer_norm_bwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_linear_cross_entropy_workspace_size(int32_t N, int32_t D, int32_t V, gdn_dtype dt, int32_t backward)
+{
+    if (N < 0 || N > (1 << 23) || D < 1 || V < 1 || (dt != GDN_F32 && dt != GDN_BF16)) return 0;
+    return linear_ce_workspace_bytes(N, D, V, (dt == GDN_BF16) ? 1 : 0, backward != 0);
+}
+
+static gdn_status ce_args(LinearCeArgs &a, const void *h, const void *weight, const int32_t *targets, int32_t N,
+                          int32_t D, int32_t V, gdn_dtype dt, bool backward, void *workspace, size_t workspace_bytes)
+{
+    if (N < 0 || D < 1 || V < 1) return GDN_ERR_INVALID_ARG;
+    if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (N > 0 && (!h || !targets)) return GDN_ERR_INVALID_ARG;
+    if (N > (1 << 23)) return GDN_ERR_UNSUPPORTED;
+    if (!weight) return GDN_ERR_INVALID_ARG;
+    if (!aligned16(h) || !aligned16(weight) || !aligned_to(targets, 4)) return GDN_ERR_INVALID_ARG;
+    if (!workspace || ((uintptr_t)workspace & 255u) != 0) return GDN_ERR_WORKSPACE;
+    if (workspace_bytes < gdn_linear_cross_entropy_workspace_size(N, D, V, dt, backward)) return GDN_ERR_WORKSPACE;
+    a = LinearCeArgs();
+    a.h = h; a.w = weight; a.targets = targets;
+    a.N = N; a.D = D; a.V = V; a.dt = (dt == GDN_BF16) ? 1 : 0;
+    a.workspace = workspace;
+    return GDN_OK;
+}
+
+gdn_status gdn_linear_cross_entropy_fwd(const void *h, const void *weight, const int32_t *targets, float *loss,
+                                        float *lse, int32_t N, int32_t D, int32_t V, gdn_dtype dt, void *workspace,
+                                        size_t workspace_bytes, void *stream)
+{
+    LinearCeArgs a;
+    const gdn_status s = ce_args(a, h, weight, targets, N, D, V, dt, false, workspace, workspace_bytes);
+    if (s != GDN_OK) return s;
+    if ((N > 0 && !loss) || !aligned_to(loss, 4) || !aligned_to(lse, 4)) return GDN_ERR_INVALID_ARG;
+    if (N == 0) return GDN_OK;
+    a.loss = loss; a.lse = lse;
+    return launch_linear_ce_fwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_linear_cross_entropy_bwd(const void *h, const void *weight, const int32_t *targets, const float *lse,
+                                        const float *dloss, void *dh, void *dweight, int32_t N, int32_t D, int32_t V,
+                                        gdn_dtype dt, void *workspace, size_t workspace_bytes, void *stream)
+{
+    LinearCeArgs a;
+    const gdn_status s = ce_args(a, h, weight, targets, N, D, V, dt, true, workspace, workspace_bytes);
+    if (s != GDN_OK) return s;
+    if ((N > 0 && (!lse || !dloss)) || !aligned_to(lse, 4) || !aligned_to(dloss, 4) || !aligned16(dh) ||
+        !aligned16(dweight))
+        return GDN_ERR_INVALID_ARG;
+    if (!dh && !dweight) return GDN_OK;
+    if (N == 0) {
+        if (!dweight) return GDN_OK;
+        const size_t bytes = (size_t)V * D * (dt == GDN_BF16 ? 2 : 4);
+        return cudaMemsetAsync(dweight, 0, bytes, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    }
+    a.lse_in = lse; a.dloss = dloss; a.dh = dh; a.dw = dweight;
+    return launch_linear_ce_bwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 gdn_status gdn_check_device_error(void *workspace, void *stream)
 {
     if (!workspace || ((uintptr_t)workspace & 255u) != 0) return GDN_ERR_INVALID_ARG;

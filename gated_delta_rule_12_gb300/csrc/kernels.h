@@ -67,6 +67,49 @@ struct BwdArgs {
     void *workspace;
 };
 
+struct GatedScanArgs {
+    const void *x, *g;                        // [B, T, D], dtype dt (x may be null in a backward without input gate)
+    const void *h, *dout;                     // backward only: the forward's output and its gradient
+    const float *init_state, *dfinal;         // [N, D] fp32 or null
+    const int32_t *cu;                        // [N + 1] or null
+    void *out, *dx, *dg;                      // forward: out; backward: dx, dg; dtype dt
+    float *final_state, *dinit;               // [N, D] fp32 or null
+    int N, T, D, dt, input_gate;
+};
+
+struct LayerNormArgs {
+    const void *x, *dout;                     // [rows, D], dtype dt
+    const float *weight, *bias;               // [D] fp32 or null
+    void *out, *dx;                           // [rows, D], dtype dt
+    float *mean, *rstd;                       // [rows] fp32: written by the forward, read by the backward
+    float *dweight, *dbias;                   // [D] fp32 or null
+    int64_t rows;
+    int D, dt;
+    float eps;
+    void *workspace;
+};
+
+struct LinearCeArgs {
+    const void *h, *w;                        // [N, D], [V, D], dtype dt
+    const int32_t *targets;                   // [N]
+    const float *lse_in, *dloss;              // backward only: [N] fp32
+    float *loss, *lse;                        // forward only: [N] fp32
+    void *dh, *dw;                            // backward only: [N, D], [V, D], dtype dt
+    int N, D, V, dt;
+    void *workspace;
+};
+
+cudaError_t launch_gated_scan_fwd(const GatedScanArgs &a, cudaStream_t st);
+cudaError_t launch_gated_scan_bwd(const GatedScanArgs &a, cudaStream_t st);
+cudaError_t launch_gated_scan_step(float *state, const void *x, const void *g, void *out, int64_t n, int dt,
+                                   int input_gate, cudaStream_t st);
+cudaError_t launch_layer_norm_fwd(const LayerNormArgs &a, cudaStream_t st);
+cudaError_t launch_layer_norm_bwd(const LayerNormArgs &a, cudaStream_t st);
+size_t layer_norm_bwd_workspace_bytes(int64_t rows, int D, int dt);
+cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st);
+cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st);
+size_t linear_ce_workspace_bytes(int N, int D, int V, int dt, bool backward);
+
 cudaError_t launch_chunk_simt(const ChunkArgs &a, cudaStream_t st);
 cudaError_t launch_chunk_bwd(const BwdArgs &a, cudaStream_t st);
 size_t chunk_bwd_workspace_bytes(int64_t slots, int H, int dk, int dv);

@@ -312,6 +312,115 @@ gdn_status gdn_prologue_chunk_fwd(const void *xq, const void *xk, const void *xv
                                   void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Gated linear recurrence per channel ("gated scan"), the recurrence with a vector state that hybrid stacks place
+ * between matrix-state layers.  No counterpart on the pages; it is eq. 10 with a diagonal state and no key:
+ *     h_t = a_t h_{t-1} + c_t x_t,   a = exp(g),
+ *     c = 1 (input_gate = 0) or c = 1 - a (input_gate != 0: h stays a weighted mean of what it has seen).
+ *   x, g, out     [B, T, D] dtype dt, contiguous; g = log a per channel (<= 0 for a decay; -inf resets the channel).
+ *   init_state    [N, D] fp32 or NULL for zeros; final_state [N, D] fp32 or NULL to skip (may alias init_state);
+ *                 a sequence without tokens passes its initial state on.
+ *   cu_seqlens    as gdn_chunk_fwd (NULL: N = B sequences of T tokens; else packed, B = 1, N = num_seqs).
+ *   T >= 0, D >= 1, no other limit on either; every pointer aligned to its element size (16-byte aligned rows take
+ *   the fast path).  out must not overlap x or g.  The recurrence runs in fp32; out is rounded to dt once.
+ * No workspace.  Results do not depend on timing.
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
+ */
+gdn_status gdn_gated_scan_fwd(const void *x, const void *g, const float *init_state,
+                              const int32_t *cu_seqlens, int32_t num_seqs,
+                              void *out, float *final_state,
+                              int32_t B, int32_t T, int32_t D, gdn_dtype dt, int32_t input_gate, void *stream);
+
+/*
+ * Backward pass of gdn_gated_scan_fwd.  With e_t = dL/dh_{t-1} through h_t, scanned from the end:
+ *     dH_t = dout_t + e_{t+1},  e_t = a_t dH_t   (e behind the last token = dfinal_state),
+ *     dx_t = c_t dH_t,   dg_t = a_t dH_t (h_{t-1} - [input_gate] x_t),   dinit_state = e of the first token.
+ *   out           the forward's output h (dtype dt); x may be NULL without the input gate.
+ *   dout, dx, dg  [B, T, D] dtype dt; dx and dg must not overlap any input.
+ *   dfinal_state  [N, D] fp32 or NULL for zeros; dinit_state [N, D] fp32 or NULL to skip.
+ * Other arguments and errors as gdn_gated_scan_fwd.
+ */
+gdn_status gdn_gated_scan_bwd(const void *x, const void *g, const void *out, const void *dout,
+                              const float *init_state, const float *dfinal_state,
+                              const int32_t *cu_seqlens, int32_t num_seqs,
+                              void *dx, void *dg, float *dinit_state,
+                              int32_t B, int32_t T, int32_t D, gdn_dtype dt, int32_t input_gate, void *stream);
+
+/*
+ * One token per sequence of gdn_gated_scan_fwd: state [N, D] fp32 is updated in place, out [N, D] dtype dt receives
+ * it rounded; x, g [N, D] dtype dt.  N = 0: nothing is enqueued.
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
+ */
+gdn_status gdn_gated_scan_step(float *state, const void *x, const void *g, void *out,
+                               int32_t N, int32_t D, gdn_dtype dt, int32_t input_gate, void *stream);
+
+/*
+ * Layer norm over the last axis: the norm in front of a token mixing block, or per head behind it ("Gated Delta
+ * Networks: Improving Mamba2 with Delta Rule", §3.4 normalises the block's output; the norm itself is the textbook
+ * one):  out = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps).
+ *   x, out        [rows, D] dtype dt, contiguous; out may alias x.
+ *   weight, bias  [D] fp32, or NULL for 1 and 0.
+ *   mean, rstd    [rows] fp32, or NULL to skip; the backward pass needs them.
+ *   rows >= 0, D >= 1, rows * D <= 2^48, eps >= 0; pointers aligned to their element size (x and out 16-byte
+ *   aligned with D a multiple of 8 take the fast path).
+ * Statistics are fp32, the variance from the deviations from the mean.
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
+ */
+gdn_status gdn_layer_norm_fwd(const void *x, const float *weight, const float *bias,
+                              void *out, float *mean, float *rstd,
+                              int64_t rows, int32_t D, gdn_dtype dt, float eps, void *stream);
+
+/*
+ * Backward pass of gdn_layer_norm_fwd, with xhat = (x - mean) rstd and u = dout weight:
+ *     dx = rstd (u - mean(u) - xhat mean(u xhat)),  dweight = sum_rows dout xhat,  dbias = sum_rows dout.
+ *   dout, x, dx   [rows, D] dtype dt (dx may alias dout; NULL skips it).
+ *   dweight, dbias  [D] fp32, overwritten (NULL skips either); rows = 0 leaves zeros in them.
+ *   workspace     at least gdn_layer_norm_bwd_workspace_size() bytes, 256-byte aligned.
+ * The sums over rows are joined in a fixed order: the same inputs give the same bits.
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_WORKSPACE, GDN_ERR_CUDA.
+ */
+size_t gdn_layer_norm_bwd_workspace_size(int64_t rows, int32_t D, gdn_dtype dt);
+
+gdn_status gdn_layer_norm_bwd(const void *dout, const void *x, const float *mean, const float *rstd,
+                              const float *weight, void *dx, float *dweight, float *dbias,
+                              int64_t rows, int32_t D, gdn_dtype dt,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Softmax cross entropy of a linear head, without an [N, V] array of logits:
+ *     lse_i = log sum_v exp(h_i . w_v),   loss_i = lse_i - h_i . w_{targets_i}.
+ *   h             [N, D] dtype dt;  weight [V, D] dtype dt;  both 16-byte aligned and contiguous.
+ *   targets       [N] int32.  A row whose target lies outside [0, V) is ignored: its loss and lse are 0.
+ *   loss          [N] fp32;  lse [N] fp32 or NULL to skip (the backward pass needs it).
+ *   0 <= N <= 2^23, D >= 1, V >= 1 (larger N: GDN_ERR_UNSUPPORTED).
+ *   workspace     at least gdn_linear_cross_entropy_workspace_size(..., backward = 0) bytes, 256-byte aligned; its
+ *                 first 256 bytes hold the device error word read by gdn_check_device_error.
+ * Logits and sums are fp32.
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_CUDA.
+ */
+size_t gdn_linear_cross_entropy_workspace_size(int32_t N, int32_t D, int32_t V, gdn_dtype dt, int32_t backward);
+
+gdn_status gdn_linear_cross_entropy_fwd(const void *h, const void *weight, const int32_t *targets,
+                                        float *loss, float *lse,
+                                        int32_t N, int32_t D, int32_t V, gdn_dtype dt,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of gdn_linear_cross_entropy_fwd: G_iv = (exp(h_i . w_v - lse_i) - [v = targets_i]) dloss_i, taken in
+ * pieces of the vocabulary;  dh = G weight,  dweight = G^T h.
+ *   lse           [N] fp32 of the forward call;  dloss [N] fp32, the gradient of each row's loss.
+ *   dh            [N, D] dtype dt or NULL to skip;  dweight [V, D] dtype dt or NULL to skip.  Overwritten; both
+ *                 16-byte aligned.
+ * Ignored rows get a zero dh and add nothing to dweight, whatever their h and dloss hold.
+ *   workspace     as the forward call, with backward = 1.
+ * Errors as the forward call.
+ */
+gdn_status gdn_linear_cross_entropy_bwd(const void *h, const void *weight, const int32_t *targets,
+                                        const float *lse, const float *dloss,
+                                        void *dh, void *dweight,
+                                        int32_t N, int32_t D, int32_t V, gdn_dtype dt,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * gdn_chunk_fwd_noalloc -- gdn_chunk_fwd for callers that cannot allocate.
  * The pages have no counterpart of this call: it exists for callers that may
  * not call cudaMalloc or any allocating routine where they run the operator
