@@ -240,10 +240,15 @@ cudaError_t bwd(const LinearCeArgs &a, cudaStream_t st)
 
 }  // namespace
 
-size_t linear_ce_workspace_bytes(int N, int D, int V, int, bool backward) { return 256 + layout(N, D, V, backward).total; }
+size_t linear_ce_workspace_bytes(int N, int D, int V, int dt, bool backward)
+{
+    if (linear_ce_tc_supported(dt, D)) return linear_ce_tc_workspace_bytes(N, D, V, backward);
+    return 256 + layout(N, D, V, backward).total;
+}
 
 cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a0, cudaStream_t st)
 {
+    if (linear_ce_tc_supported(a0.dt, a0.D)) return launch_linear_ce_tc_fwd(a0, st);
     LinearCeArgs a = a0;
     a.workspace = (char *)a0.workspace + 256;
     return a.dt ? fwd<__nv_bfloat16>(a, st) : fwd<float>(a, st);
@@ -251,6 +256,7 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a0, cudaStream_t st)
 
 cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a0, cudaStream_t st)
 {
+    if (linear_ce_tc_supported(a0.dt, a0.D)) return launch_linear_ce_tc_bwd(a0, st);
     LinearCeArgs a = a0;
     a.workspace = (char *)a0.workspace + 256;
     return a.dt ? bwd<__nv_bfloat16>(a, st) : bwd<float>(a, st);

@@ -138,7 +138,8 @@ def ce_fwd(h, w, targets):
 
 
 def ce_bwd(h, w, targets, lse, dloss, low_bits):
-    """(dh, dweight) and bounds.  ``low_bits``: G enters the products rounded to bfloat16."""
+    """(dh, dweight) and bounds.  ``low_bits``: softmax - onehot enters the products rounded to bfloat16, and dweight's
+    other factor, dloss h in units of the largest dloss, is rounded too."""
     h, w, t, lse, dl = f64(h), f64(w), targets.cpu().long(), f64(lse), f64(dloss)
     N, V, D = h.shape[0], w.shape[0], h.shape[1]
     keep = (t >= 0) & (t < V)
@@ -154,7 +155,7 @@ def ce_bwd(h, w, targets, lse, dloss, low_bits):
     if low_bits:
         eG = eG + BF16 * G.abs()
     edh = eG @ w.abs() + 2 * U * (V + 64) * (G.abs() @ w.abs())
-    edw = eG.T @ h.abs() + 2 * U * (N + 64) * (G.abs().T @ h.abs())
+    edw = (eG + (BF16 if low_bits else 0.0) * G.abs()).T @ h.abs() + 2 * U * (N + 64) * (G.abs().T @ h.abs())
     return (G @ w, G.T @ h), (edh, edw)
 
 
