@@ -5,6 +5,10 @@
 // Backward, with e_t = dL/dh_{t-1} (through h_t), a scan from the end of the same form:
 //     dH_t = dout_t + e_{t+1},   e_t = a_t dH_t,   e_{len} = dfinal,
 //     dx_t = c_t dH_t,           dg_t = a_t dH_t (h_{t-1} [- x_t with the input gate]),   dinit = e_0.
+//
+// Bound by memory: three tensors forward, five backward (six with the gate), at 3 and 6 operations an element.  What
+// keeps the kernel from that bound is the number of instructions an element and the latency of the joins along time,
+// hence pairs of channels in one instruction and few, long iterations.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -23,83 +27,689 @@ __device__ __forceinline__ void span(const GatedScanArgs &a, int n, int64_t &tok
     }
 }
 
-// One thread per (sequence, channel), one step after the other.
-template <typename T, bool GATE>
-__global__ void __launch_bounds__(128) scan_fwd_kernel(GatedScanArgs a)
+// Arithmetic on two channels at once (fp32 pairs in a 64-bit register).
+using Pair = unsigned long long;
+
+__device__ __forceinline__ Pair pair(float lo, float hi)
 {
-    const int ch = blockIdx.x * blockDim.x + threadIdx.x;
-    if (ch >= a.D) return;
-    for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
-        int64_t tok0;
-        int len;
-        span(a, n, tok0, len);
-        float h = a.init_state ? a.init_state[(int64_t)n * a.D + ch] : 0.f;
-        for (int t = 0; t < len; ++t) {
-            const int64_t i = (tok0 + t) * a.D + ch;
-            const float g = to_f32(((const T *)a.g)[i]), x = to_f32(((const T *)a.x)[i]);
-            h = fmaf(expf(g), h, GATE ? -expm1f(g) * x : x);
-            ((T *)a.out)[i] = from_f32<T>(h);
-        }
-        if (a.final_state) a.final_state[(int64_t)n * a.D + ch] = h;
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(Pair p, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
+{
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b)
+{
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// exp(g) as 2^(g log2 e) by the hardware's exponential.  In fp32 the rounding of the product g log2 e, |g| / 2 ulp of
+// the result, is put back to first order (log2 e as a sum of two floats); for bf16 it stays below the gate's own
+// rounding.
+template <typename T>
+__device__ __forceinline__ Pair decay(Pair g)
+{
+    const Pair t = mul2(g, pair(1.44269502f, 1.44269502f));
+    float t0, t1;
+    split(t, t0, t1);
+    const float r0 = exp2_approx(t0), r1 = exp2_approx(t1);
+    if constexpr (sizeof(T) == 4) {
+        const Pair down = mul2(g, pair(-1.44269502f, -1.44269502f));
+        const Pair lost = fma2(g, pair(1.92596299e-8f, 1.92596299e-8f), fma2(g, pair(1.44269502f, 1.44269502f), down));
+        const Pair r = pair(r0, r1);
+        float f0, f1;
+        split(fma2(r, mul2(lost, pair(0.693147181f, 0.693147181f)), r), f0, f1);
+        // where r is 0 or infinite, or about to be, lost may be NaN
+        return pair(fabsf(t0) < 126.f ? f0 : r0, fabsf(t1) < 126.f ? f1 : r1);
+    } else {
+        return pair(r0, r1);
     }
 }
 
-template <typename T, bool GATE>
-__global__ void __launch_bounds__(128) scan_bwd_kernel(GatedScanArgs a)
+// A lane owns 8 bytes of a row, 4 bf16 or 2 float channels; L lanes (4, 8 or 16) take a row of a CTA's block of
+// channels, and the 32 / L groups of a warp take successive runs of R rows.
+template <typename T> constexpr int kVec = 8 / sizeof(T);
+template <typename T> constexpr int kPairs = kVec<T> / 2;
+
+template <typename T>
+__device__ __forceinline__ void unpack(uint2 w, Pair (&v)[kPairs<T>])
 {
-    const int ch = blockIdx.x * blockDim.x + threadIdx.x;
-    if (ch >= a.D) return;
-    for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
-        int64_t tok0;
-        int len;
-        span(a, n, tok0, len);
-        const int64_t s = (int64_t)n * a.D + ch;
-        float e = a.dfinal ? a.dfinal[s] : 0.f;
-        for (int t = len - 1; t >= 0; --t) {
-            const int64_t i = (tok0 + t) * a.D + ch;
-            const float g = to_f32(((const T *)a.g)[i]), al = expf(g);
-            float prev = t > 0 ? to_f32(((const T *)a.h)[i - a.D]) : (a.init_state ? a.init_state[s] : 0.f);
-            const float dh = to_f32(((const T *)a.dout)[i]) + e;
-            e = al * dh;
-            if (GATE) prev -= to_f32(((const T *)a.x)[i]);
-            ((T *)a.dx)[i] = from_f32<T>(GATE ? -expm1f(g) * dh : dh);
-            ((T *)a.dg)[i] = from_f32<T>(e * prev);
-        }
-        if (a.dinit) a.dinit[s] = e;
+    if constexpr (sizeof(T) == 4) {
+        v[0] = pair(__uint_as_float(w.x), __uint_as_float(w.y));
+    } else {
+        v[0] = pair(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
+        v[1] = pair(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
     }
 }
 
-template <typename T, bool GATE>
+template <typename T>
+__device__ __forceinline__ uint2 pack(const Pair (&v)[kPairs<T>])
+{
+    float a, b;
+    split(v[0], a, b);
+    if constexpr (sizeof(T) == 4) {
+        return make_uint2(__float_as_uint(a), __float_as_uint(b));
+    } else {
+        uint2 r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.x) : "f"(b), "f"(a));
+        split(v[1], a, b);
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.y) : "f"(b), "f"(a));
+        return r;
+    }
+}
+
+// One stretch of the recurrence maps a carry c to H + A c.  A = exp(S), S the sum of the stretch's g, is kept finite,
+// so that growth beyond fp32's range leaves a carry of 0 at 0.
+template <typename T> struct Map { Pair A[kPairs<T>], H[kPairs<T>]; };
+
+template <typename T>
+__device__ __forceinline__ void set_decay(Map<T> &m, const Pair (&sum)[kPairs<T>])
+{
+#pragma unroll
+    for (int v = 0; v < kPairs<T>; ++v) {
+        float a, b;
+        split(decay<T>(sum[v]), a, b);
+        m.A[v] = pair(fminf(a, 3.402823466e38f), fminf(b, 3.402823466e38f));
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void apply(const Map<T> &m, Pair (&c)[kPairs<T>])
+{
+#pragma unroll
+    for (int v = 0; v < kPairs<T>; ++v) c[v] = fma2(m.A[v], c[v], m.H[v]);
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t shared_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+// The maps of an iteration in shared memory, by turns, so that one barrier an iteration is enough.
+template <typename T, int L>
+struct Exchange {
+    static constexpr int NP = kPairs<T>;
+    Map<T> *maps;                   // [2][nwarps][L]: of each warp
+    Pair *sums;                     // [2][nwarps][L][pairs]: S of each warp      (cluster only)
+    Map<T> *ctas;                   // [2][csize][L]: of each CTA                 (cluster only)
+    int nwarps, csize, rank;
+    static __host__ __device__ int bytes(int nwarps, int csize)
+    {
+        return 2 * L * (nwarps * (int)sizeof(Map<T>) + (csize > 1 ? nwarps * NP * 8 + csize * (int)sizeof(Map<T>) : 0));
+    }
+    __device__ __forceinline__ Exchange(unsigned char *p, int nw, int cs, int rk)
+        : maps((Map<T> *)p), sums((Pair *)(maps + 2 * nw * L)), ctas((Map<T> *)(sums + 2 * nw * L * NP)),
+          nwarps(nw), csize(cs), rank(rk) {}
+
+    // The work of a cluster's extra warp: joins its CTA's maps and hands the result to the other CTAs.  It stores
+    // nothing to global memory: the release that makes the maps visible waits for all earlier stores of its thread,
+    // and with the rows' own stores among them that wait took a quarter of the kernel.
+    __device__ __forceinline__ void hand_over(int turn)
+    {
+        const int lane = threadIdx.x & (L - 1);
+        __syncthreads();
+        Map<T> all;
+        Pair s[NP];
+#pragma unroll
+        for (int v = 0; v < NP; ++v) s[v] = all.H[v] = 0;
+        for (int w = 0; w < nwarps; ++w) {
+            apply(maps[(turn * nwarps + w) * L + lane], all.H);
+#pragma unroll
+            for (int v = 0; v < NP; ++v) s[v] = add2(s[v], sums[((turn * nwarps + w) * L + lane) * NP + v]);
+        }
+        set_decay<T>(all, s);
+        // the groups of the warp share the CTAs out
+        const uint32_t mine = shared_addr(&ctas[(turn * csize + rank) * L + lane]);
+        for (int r = (threadIdx.x & 31) / L; r < csize; r += 32 / L) {
+            uint32_t to;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(mine), "r"(r));
+#pragma unroll
+            for (int v = 0; v < NP; ++v) {
+                asm volatile("st.shared::cluster.b64 [%0], %1;" :: "r"(to + 8 * v), "l"(all.A[v]) : "memory");
+                asm volatile("st.shared::cluster.b64 [%0], %1;" :: "r"(to + 8 * (NP + v)), "l"(all.H[v]) : "memory");
+            }
+        }
+        __syncwarp();
+        cluster_sync();
+    }
+
+    // On entry a group holds the sum S and the map's H of its rows, and every thread the carry into the iteration's
+    // first row; returns the carry into the group's rows and moves `carry` behind the iteration's last row.  The order
+    // is fixed: groups, warps, CTAs.
+    template <bool CLUSTER>
+    __device__ __forceinline__ void join(int turn, Pair (&s)[NP], Pair (&h)[NP], Pair (&carry)[NP], Pair (&in)[NP])
+    {
+        const int lane = threadIdx.x & (L - 1), group = (threadIdx.x & 31) / L, warp = threadIdx.x >> 5;
+        Map<T> m;
+        // scan over the warp's groups: each takes in the ones before it, 1, 2, 4 at a time
+#pragma unroll
+        for (int o = 1; o < 32 / L; o *= 2) {
+            set_decay<T>(m, s);
+#pragma unroll
+            for (int v = 0; v < NP; ++v) {
+                const Pair so = __shfl_up_sync(0xffffffffu, s[v], o * L), ho = __shfl_up_sync(0xffffffffu, h[v], o * L);
+                if (group >= o) {
+                    h[v] = fma2(m.A[v], ho, h[v]);
+                    s[v] = add2(s[v], so);
+                }
+            }
+        }
+        if (group == 32 / L - 1) {
+            set_decay<T>(m, s);
+#pragma unroll
+            for (int v = 0; v < NP; ++v) m.H[v] = h[v];
+            maps[(turn * nwarps + warp) * L + lane] = m;
+            if (CLUSTER)
+#pragma unroll
+                for (int v = 0; v < NP; ++v) sums[((turn * nwarps + warp) * L + lane) * NP + v] = s[v];
+        }
+        // the map of the groups before this one
+        Map<T> before;
+#pragma unroll
+        for (int v = 0; v < NP; ++v) {
+            s[v] = __shfl_up_sync(0xffffffffu, s[v], L & 31);
+            before.H[v] = __shfl_up_sync(0xffffffffu, h[v], L & 31);
+        }
+        set_decay<T>(before, s);
+        __syncthreads();
+        const Map<T> *all = maps + turn * nwarps * L + lane;
+        if (CLUSTER) {
+            asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            for (int r = 0; r < csize; ++r) {
+#pragma unroll
+                for (int v = 0; v < NP; ++v) in[v] = r == rank ? carry[v] : in[v];
+                apply(ctas[(turn * csize + r) * L + lane], carry);
+            }
+#pragma unroll 4
+            for (int w = 0; w < warp; ++w) apply(all[w * L], in);
+        } else {
+#pragma unroll 4
+            for (int w = 0; w < warp; ++w) apply(all[w * L], carry);
+#pragma unroll
+            for (int v = 0; v < NP; ++v) in[v] = carry[v];
+#pragma unroll 4
+            for (int w = warp; w < nwarps; ++w) apply(all[w * L], carry);
+        }
+        if (group > 0) apply(before, in);
+    }
+};
+
+// ROWS rows of 8 L bytes into a warp's slot; row i at src + i * step elements, rows from `rows` on and channels behind
+// D as zeros.  CW: bytes that a copy may move at once, by the alignment of the rows; 2 (a row of an odd number of bf16)
+// has no asynchronous copy and goes through registers.
+template <typename T, int L, int ROWS, int CW>
+__device__ __forceinline__ void fetch(uint32_t slot, const T *src, int step, int rows, int channels)
+{
+    const int lane = threadIdx.x & 31;
+    if constexpr (CW == 16) {
+        constexpr int across = L / 2, down = 32 / across;   // copies a row; rows a step
+        const int col = (lane % across) * (16 / (int)sizeof(T)), r0 = lane / across;
+        const T *p = src + ((int64_t)step * r0 + col);
+        const bool live = col < channels;
+#pragma unroll
+        for (int i = 0; i < ROWS / down; ++i) {
+            const bool in = live && r0 + down * i < rows;
+            asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;"
+                         :: "r"(slot + lane * 16 + i * 512), "l"(in ? p + (int64_t)step * (down * i) : src),
+                            "r"(in ? 16 : 0) : "memory");
+        }
+    } else if constexpr (CW == 4) {
+        constexpr int across = L * 2 < 32 ? L * 2 : 32, down = 32 / across, per = 4 / sizeof(T);
+        const int col = (lane % across) * per, r0 = lane / across;
+        const T *p = src + ((int64_t)step * r0 + col);
+        const bool live = col < channels;
+#pragma unroll
+        for (int i = 0; i < ROWS / down; ++i) {
+            const bool in = live && r0 + down * i < rows;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                         :: "r"(slot + lane * 4 + i * 128), "l"(in ? p + (int64_t)step * (down * i) : src),
+                            "r"(in ? 4 : 0) : "memory");
+        }
+    } else {
+        constexpr int across = L * 2 < 32 ? L * 2 : 32, down = 32 / across;
+        const int col = (lane % across) * 2, r0 = lane / across;
+        uint32_t w[ROWS / down];
+#pragma unroll
+        for (int i = 0; i < ROWS / down; ++i) {
+            const unsigned short *p = reinterpret_cast<const unsigned short *>(src + (int64_t)step * (r0 + down * i)) + col;
+            const bool in = r0 + down * i < rows;
+            w[i] = in && col < channels ? __ldg(p) : 0u;
+            if (in && col + 1 < channels) w[i] |= (uint32_t)__ldg(p + 1) << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS / down; ++i)
+            asm volatile("st.shared.b32 [%0], %1;" :: "r"(slot + lane * 4 + i * 128), "r"(w[i]) : "memory");
+    }
+}
+
+// The lane's channels of one row; `mine` = how many of them lie before D.
+template <typename T, int CW>
+__device__ __forceinline__ void put(T *dst, const Pair (&v)[kPairs<T>], int mine)
+{
+    const uint2 w = pack<T>(v);
+    if constexpr (CW == 16) {
+        if (mine > 0) *reinterpret_cast<uint2 *>(dst) = w;
+    } else if constexpr (CW == 4) {
+        constexpr int per = 4 / sizeof(T);
+        if (mine > 0) *reinterpret_cast<uint32_t *>(dst) = w.x;
+        if (mine > per) *reinterpret_cast<uint32_t *>(dst + per) = w.y;
+    } else {
+        unsigned short *p = reinterpret_cast<unsigned short *>(dst);
+        if (mine > 0) p[0] = (unsigned short)w.x;
+        if (mine > 1) p[1] = (unsigned short)(w.x >> 16);
+        if (mine > 2) p[2] = (unsigned short)w.y;
+        if (mine > 3) p[3] = (unsigned short)(w.y >> 16);
+    }
+}
+
+__device__ __forceinline__ uint2 words(uint32_t at)
+{
+    uint2 w;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(at));
+    return w;
+}
+
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+// What a CTA works on: one sequence (with the cluster's other CTAs, along time) and one block of L kVec channels.
+template <typename T, int L>
+struct Work {
+    int n, ch0, channels, rank, len, mine;
+    int64_t tok0;
+    __device__ __forceinline__ Work(const GatedScanArgs &a, int nblocks, int csize)
+    {
+        rank = blockIdx.x % csize;
+        const int unit = blockIdx.x / csize;
+        n = unit / nblocks;
+        ch0 = (unit % nblocks) * (L * kVec<T>);
+        channels = min(a.D - ch0, (L * kVec<T>));
+        mine = channels - (threadIdx.x & (L - 1)) * kVec<T>;
+        span(a, n, tok0, len);
+    }
+    __device__ __forceinline__ void get(const float *s, const GatedScanArgs &a, Pair (&p)[kPairs<T>]) const
+    {
+        const float *at = s + (int64_t)n * a.D + ch0 + (threadIdx.x & (L - 1)) * kVec<T>;
+#pragma unroll
+        for (int v = 0; v < kPairs<T>; ++v)
+            p[v] = pair(s && 2 * v < mine ? at[2 * v] : 0.f, s && 2 * v + 1 < mine ? at[2 * v + 1] : 0.f);
+    }
+    __device__ __forceinline__ void set(float *s, const GatedScanArgs &a, const Pair (&p)[kPairs<T>]) const
+    {
+        float *at = s + (int64_t)n * a.D + ch0 + (threadIdx.x & (L - 1)) * kVec<T>;
+#pragma unroll
+        for (int v = 0; v < kPairs<T>; ++v) {
+            float x, y;
+            split(p[v], x, y);
+            if (s && 2 * v < mine) at[2 * v] = x;
+            if (s && 2 * v + 1 < mine) at[2 * v + 1] = y;
+        }
+    }
+};
+
+__device__ __forceinline__ int rows_left(int64_t from, int len, int most)
+{
+    return (int)max((int64_t)0, min((int64_t)most, len - from));
+}
+
+// -expm1(g) on a pair
+__device__ __forceinline__ Pair gate_of(Pair g)
+{
+    float a, b;
+    split(g, a, b);
+    return pair(-expm1f(a), -expm1f(b));
+}
+
+// An iteration takes csize * nwarps * R * 32 / L rows.  Rows pass through a ring of each warp's own slots by asynchronous
+// copies, so only the joins need barriers.  A group scans its R rows from 0 (S and H), the joined carry comes in,
+// and the rows are run again from it out of registers: memory is read once and written once.
+template <typename T, bool GATE, int CW, int L, int R, int STAGES, int WARPS, bool CLUSTER>
+__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), WARPS > 8 ? 1 : 2)
+scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
+{
+    constexpr int NP = kPairs<T>, ROWS = R * 32 / L, SLOT = R * 256;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int warp = threadIdx.x >> 5, nwarps = (blockDim.x >> 5) - (CLUSTER ? 1 : 0);
+    const Work<T, L> w(a, nblocks, csize);
+    Exchange<T, L> ex(smem + nwarps * STAGES * 2 * SLOT, nwarps, csize, w.rank);
+    const int64_t per = (int64_t)csize * nwarps * ROWS;
+    int turn = 0, stage = 0;
+    if (CLUSTER) {
+        cluster_sync();   // the others' shared memory may be written once they run
+        if (warp == nwarps) {
+            for (int64_t first = 0; first < w.len; first += per, turn ^= 1) ex.hand_over(turn);
+            return;
+        }
+    }
+
+    const uint32_t slots = shared_addr(smem) + warp * STAGES * 2 * SLOT;
+    const int group = (threadIdx.x & 31) / L;
+    const uint32_t own = group * R * L * 8 + (threadIdx.x & (L - 1)) * 8;
+    const int64_t base = w.tok0 * a.D + w.ch0;
+    Pair carry[NP];
+    w.get(a.init_state, a, carry);
+    int64_t t0 = (int64_t)(w.rank * nwarps + warp) * ROWS;   // the warp's first row of the iteration
+    auto load = [&](int64_t t, int st) {
+        const int rows = rows_left(t, w.len, ROWS);
+        const int64_t at = base + (rows > 0 ? t * a.D : 0);
+        fetch<T, L, ROWS, CW>(slots + st * 2 * SLOT, (const T *)a.g + at, a.D, rows, w.channels);
+        fetch<T, L, ROWS, CW>(slots + (st * 2 + 1) * SLOT, (const T *)a.x + at, a.D, rows, w.channels);
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+        load(t0 + s * per, s);
+        commit_copies();
+    }
+    for (int64_t first = 0; first < w.len; first += per, t0 += per, turn ^= 1) {
+        wait_copies<STAGES - 1>();
+        __syncwarp();
+        const uint32_t sg = slots + stage * 2 * SLOT + own, sx = sg + SLOT;
+        Pair al[R][NP], u[R][NP], sum[NP], h[NP], in[NP];
+#pragma unroll
+        for (int v = 0; v < NP; ++v) sum[v] = h[v] = 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            unpack<T>(words(sg + i * (8 * L)), al[i]);   // rows behind the end: g = x = 0, the identity
+            unpack<T>(words(sx + i * (8 * L)), u[i]);
+#pragma unroll
+            for (int v = 0; v < NP; ++v) {
+                sum[v] = add2(sum[v], al[i][v]);
+                if (GATE) u[i][v] = mul2(u[i][v], gate_of(al[i][v]));
+                al[i][v] = decay<T>(al[i][v]);
+                h[v] = fma2(al[i][v], h[v], u[i][v]);
+            }
+        }
+        __syncwarp();
+        load(t0 + STAGES * per, stage);
+        commit_copies();
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        ex.template join<CLUSTER>(turn, sum, h, carry, in);
+        const int rows = rows_left(t0 + group * R, w.len, R);
+        T *out = (T *)a.out + (base + (t0 + group * R) * a.D + (threadIdx.x & (L - 1)) * kVec<T>);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+#pragma unroll
+            for (int v = 0; v < NP; ++v) in[v] = fma2(al[i][v], in[v], u[i][v]);
+            if (i < rows) put<T, CW>(out + (int64_t)a.D * i, in, w.mine);
+        }
+    }
+    wait_copies<0>();
+    if (w.rank == 0 && warp == 0 && group == 0) w.set(a.final_state, a, carry);
+}
+
+// The same from the end: row i of a warp's slot is token len - 1 - (r0 + i), its h the one before.
+template <typename T, bool GATE, int CW, int L, int R, int STAGES, int WARPS, bool CLUSTER>
+__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), WARPS > 8 ? 1 : 2)
+scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
+{
+    constexpr int NP = kPairs<T>, NT = GATE ? 4 : 3, ROWS = R * 32 / L, SLOT = R * 256;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int warp = threadIdx.x >> 5, nwarps = (blockDim.x >> 5) - (CLUSTER ? 1 : 0);
+    const Work<T, L> w(a, nblocks, csize);
+    Exchange<T, L> ex(smem + nwarps * STAGES * NT * SLOT, nwarps, csize, w.rank);
+    const int64_t per = (int64_t)csize * nwarps * ROWS;
+    int turn = 0, stage = 0;
+    if (CLUSTER) {
+        cluster_sync();
+        if (warp == nwarps) {
+            for (int64_t first = 0; first < w.len; first += per, turn ^= 1) ex.hand_over(turn);
+            return;
+        }
+    }
+
+    const uint32_t slots = shared_addr(smem) + warp * STAGES * NT * SLOT;
+    const int group = (threadIdx.x & 31) / L;
+    const uint32_t own = group * R * L * 8 + (threadIdx.x & (L - 1)) * 8;
+    const int64_t last = (w.tok0 + w.len - 1) * a.D + w.ch0;
+    Pair carry[NP];
+    w.get(a.dfinal, a, carry);
+    int64_t r0 = (int64_t)(w.rank * nwarps + warp) * ROWS;
+    auto load = [&](int64_t r, int st) {
+        const int rows = rows_left(r, w.len, ROWS), before = rows_left(r, w.len - 1, ROWS);   // the first token has none
+        const int64_t at = rows > 0 ? last - r * a.D : 0;
+        const uint32_t s = slots + st * NT * SLOT;
+        fetch<T, L, ROWS, CW>(s, (const T *)a.g + at, -a.D, rows, w.channels);
+        fetch<T, L, ROWS, CW>(s + SLOT, (const T *)a.dout + at, -a.D, rows, w.channels);
+        fetch<T, L, ROWS, CW>(s + 2 * SLOT, (const T *)a.h + (before > 0 ? at - a.D : 0), -a.D, before, w.channels);
+        if (GATE) fetch<T, L, ROWS, CW>(s + 3 * SLOT, (const T *)a.x + at, -a.D, rows, w.channels);
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+        load(r0 + s * per, s);
+        commit_copies();
+    }
+    for (int64_t first = 0; first < w.len; first += per, r0 += per, turn ^= 1) {
+        wait_copies<STAGES - 1>();
+        __syncwarp();
+        const uint32_t sg = slots + stage * NT * SLOT + own, sd = sg + SLOT, shh = sd + SLOT, sx = shh + SLOT;
+        Pair al[R][NP], d[R][NP], sum[NP], h[NP], e[NP];
+#pragma unroll
+        for (int v = 0; v < NP; ++v) sum[v] = h[v] = 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            unpack<T>(words(sg + i * (8 * L)), al[i]);
+            unpack<T>(words(sd + i * (8 * L)), d[i]);
+#pragma unroll
+            for (int v = 0; v < NP; ++v) {
+                sum[v] = add2(sum[v], al[i][v]);
+                al[i][v] = decay<T>(al[i][v]);
+                h[v] = mul2(al[i][v], add2(h[v], d[i][v]));
+            }
+        }
+        ex.template join<CLUSTER>(turn, sum, h, carry, e);
+        const int64_t rh = r0 + group * R;
+        const int rows = rows_left(rh, w.len, R);
+        const int64_t start = w.len - 1 - rh;   // the row of the sequence's first token
+        const int64_t at = last - rh * a.D + (threadIdx.x & (L - 1)) * kVec<T>;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            Pair prev[NP], x[NP], g[NP], vx[NP], vg[NP];
+            unpack<T>(words(shh + i * (8 * L)), prev);
+            if (i == start) w.get(a.init_state, a, prev);
+            if (GATE) {
+                unpack<T>(words(sx + i * (8 * L)), x);
+                unpack<T>(words(sg + i * (8 * L)), g);
+            }
+#pragma unroll
+            for (int v = 0; v < NP; ++v) {
+                const Pair dh = add2(d[i][v], e[v]);
+                e[v] = mul2(al[i][v], dh);
+                vx[v] = GATE ? mul2(gate_of(g[v]), dh) : dh;
+                vg[v] = mul2(e[v], GATE ? fma2(x[v], pair(-1.f, -1.f), prev[v]) : prev[v]);
+            }
+            if (i < rows) {
+                put<T, CW>((T *)a.dx + at - (int64_t)a.D * i, vx, w.mine);
+                put<T, CW>((T *)a.dg + at - (int64_t)a.D * i, vg, w.mine);
+            }
+        }
+        __syncwarp();
+        load(r0 + STAGES * per, stage);
+        commit_copies();
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+    wait_copies<0>();
+    if (w.rank == 0 && warp == 0 && group == 0) w.set(a.dinit, a, carry);
+}
+
+// Eight elements a thread where the arrays allow 16-byte accesses of the element type, else one.
+template <typename T, bool GATE, int E>
 __global__ void __launch_bounds__(256) scan_step_kernel(float *state, const T *x, const T *g, T *out, int64_t n)
 {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const float gv = to_f32(g[i]), xv = to_f32(x[i]);
-        const float h = fmaf(expf(gv), state[i], GATE ? -expm1f(gv) * xv : xv);
-        state[i] = h;
-        out[i] = from_f32<T>(h);
+    const int64_t stride = (int64_t)gridDim.x * 256 * E;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * E; i < n; i += stride) {
+        T xv[E], gv[E], ov[E];
+        float h[E];
+        if constexpr (E == 8) {
+            constexpr int Q = E * sizeof(T) / 16;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                reinterpret_cast<uint4 *>(xv)[q] = __ldcs(reinterpret_cast<const uint4 *>(x + i) + q);
+                reinterpret_cast<uint4 *>(gv)[q] = __ldcs(reinterpret_cast<const uint4 *>(g + i) + q);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                reinterpret_cast<float4 *>(h)[q] = *(reinterpret_cast<const float4 *>(state + i) + q);
+        } else {
+            xv[0] = x[i];
+            gv[0] = g[i];
+            h[0] = state[i];
+        }
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const float gg = to_f32(gv[j]), xx = to_f32(xv[j]);
+            h[j] = fmaf(expf(gg), h[j], GATE ? -expm1f(gg) * xx : xx);
+            ov[j] = from_f32<T>(h[j]);
+        }
+        if constexpr (E == 8) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                *(reinterpret_cast<float4 *>(state + i) + q) = reinterpret_cast<float4 *>(h)[q];
+#pragma unroll
+            for (int q = 0; q < (int)(E * sizeof(T) / 16); ++q)
+                *(reinterpret_cast<uint4 *>(out + i) + q) = reinterpret_cast<uint4 *>(ov)[q];
+        } else {
+            state[i] = h[0];
+            out[i] = ov[0];
+        }
     }
+}
+
+// How the work is cut: lanes a row, warps a CTA, CTAs a cluster.
+//
+// One CTA of 8 warps takes some 2 us an iteration however few rows that is, so what is needed is enough CTAs, two on
+// each of 152 SMs, with many rows each.  Blocks of 128-byte rows come first (19 x 2048 x 1024 bf16, 304 CTAs: 42 us,
+// 5.6 TB/s).  Where they are fewer than 228, narrower rows, whose neighbours in the warp go along time instead, make
+// more CTAs of more rows (4 x 2048 x 2048: 16 lanes 27.8 us, 8 lanes 24.7, 4 lanes 34.8, forward).  Packed sequences
+// of unequal lengths are held up by the longest, so they take more CTAs (8 sequences, 32768 x 2048: 189, 126, 129 us).
+// A cluster's join costs about 2 us more an iteration (4 x 2048 x 2048 in clusters of two: 45 us), so it serves only
+// where 32-byte rows leave most SMs idle (1 x 32768 x 64, clusters of 16: 60 us with 128-byte rows, 19 us with 32-byte
+// rows; 438 us in one CTA).
+struct Cut { int lanes, warps, csize; };
+
+Cut cut(const GatedScanArgs &a, int vec, int R)
+{
+    Cut c = {16, 8, 1};
+    const int T = a.T;
+    auto units = [&] { return (int64_t)a.N * ceil_div(a.D, c.lanes * vec); };
+    auto rows = [&] { return (int64_t)c.csize * c.warps * R * 32 / c.lanes; };
+    while (c.lanes > 4 && units() < (a.cu ? 912 : 228) && rows() < T) c.lanes /= 2;
+    if (c.lanes > 4 || units() >= 228 || rows() >= T) return c;
+    c.warps = 16;
+    if (units() >= 76 || rows() >= T) return c;
+    c.warps = 15;
+    while (c.csize < 16 && units() * c.csize * 2 <= 152 && rows() < T) c.csize *= 2;
+    return c;
+}
+
+template <typename T, int L, int R, class Kernel>
+cudaError_t launch(Kernel kernel, const GatedScanArgs &a, int slot_bytes, Cut c, cudaStream_t st)
+{
+    const int nblocks = ceil_div(a.D, L * kVec<T>);
+    const int64_t units = (int64_t)a.N * nblocks;
+    const int most = ceil_div(a.T > 0 ? a.T : 1, R * 32 / L);
+    const int nwarps = most < c.warps ? most : c.warps;
+    if (units * c.csize > 0x7fffffffll) return cudaErrorInvalidValue;
+    const int smem = nwarps * slot_bytes + Exchange<T, L>::bytes(nwarps, c.csize);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && c.csize > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * c.csize));
+    cfg.blockDim = dim3(32 * (nwarps + (c.csize > 1)));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = c.csize;
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = c.csize > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a, nblocks, c.csize);
+}
+
+// Bytes that one copy may move: every row of every tensor has to start on a multiple of them.
+template <typename T>
+int copy_width(const GatedScanArgs &a)
+{
+    const uintptr_t all = (uintptr_t)a.x | (uintptr_t)a.g | (uintptr_t)a.out | (uintptr_t)a.h | (uintptr_t)a.dout |
+                          (uintptr_t)a.dx | (uintptr_t)a.dg | (uintptr_t)a.D * sizeof(T);
+    return (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 2;
+}
+
+template <typename T, bool GATE, int CW>
+cudaError_t fwd_cw(const GatedScanArgs &a, cudaStream_t st)
+{
+    constexpr int R = 8, S = 2, SLOTS = S * 2 * R * 256;
+    const Cut c = cut(a, kVec<T>, R);
+    if (c.csize > 1) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 15, true>, a, SLOTS, c, st);
+    if (c.warps > 8) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 16, false>, a, SLOTS, c, st);
+    if (c.lanes == 4) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 8, false>, a, SLOTS, c, st);
+    if (c.lanes == 8) return launch<T, 8, R>(scan_fwd_kernel<T, GATE, CW, 8, R, S, 8, false>, a, SLOTS, c, st);
+    return launch<T, 16, R>(scan_fwd_kernel<T, GATE, CW, 16, R, S, 8, false>, a, SLOTS, c, st);
+}
+
+template <typename T, bool GATE, int CW>
+cudaError_t bwd_cw(const GatedScanArgs &a, cudaStream_t st)
+{
+    constexpr int R = GATE ? 4 : 8, S = 2, SLOTS = S * (GATE ? 4 : 3) * R * 256;
+    const Cut c = cut(a, kVec<T>, R);
+    if (c.csize > 1) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 15, true>, a, SLOTS, c, st);
+    if (c.warps > 8) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 16, false>, a, SLOTS, c, st);
+    if (c.lanes == 4) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 8, false>, a, SLOTS, c, st);
+    if (c.lanes == 8) return launch<T, 8, R>(scan_bwd_kernel<T, GATE, CW, 8, R, S, 8, false>, a, SLOTS, c, st);
+    return launch<T, 16, R>(scan_bwd_kernel<T, GATE, CW, 16, R, S, 8, false>, a, SLOTS, c, st);
 }
 
 template <typename T, bool GATE>
 cudaError_t fwd(const GatedScanArgs &a, cudaStream_t st)
 {
-    scan_fwd_kernel<T, GATE><<<dim3(ceil_div(a.D, 128), a.N < 65535 ? a.N : 65535), 128, 0, st>>>(a);
-    return cudaGetLastError();
+    const int cw = copy_width<T>(a);
+    if constexpr (sizeof(T) == 2)
+        if (cw == 2) return fwd_cw<T, GATE, 2>(a, st);
+    return cw == 16 ? fwd_cw<T, GATE, 16>(a, st) : fwd_cw<T, GATE, 4>(a, st);
 }
 
 template <typename T, bool GATE>
 cudaError_t bwd(const GatedScanArgs &a, cudaStream_t st)
 {
-    scan_bwd_kernel<T, GATE><<<dim3(ceil_div(a.D, 128), a.N < 65535 ? a.N : 65535), 128, 0, st>>>(a);
-    return cudaGetLastError();
+    const int cw = copy_width<T>(a);
+    if constexpr (sizeof(T) == 2)
+        if (cw == 2) return bwd_cw<T, GATE, 2>(a, st);
+    return cw == 16 ? bwd_cw<T, GATE, 16>(a, st) : bwd_cw<T, GATE, 4>(a, st);
 }
 
 template <typename T, bool GATE>
 cudaError_t step(float *state, const void *x, const void *g, void *out, int64_t n, cudaStream_t st)
 {
-    const int64_t blocks = (n + 255) / 256;
-    scan_step_kernel<T, GATE><<<(unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), 256, 0, st>>>(
-        state, (const T *)x, (const T *)g, (T *)out, n);
+    const bool wide = n % 8 == 0 && (((uintptr_t)state | (uintptr_t)x | (uintptr_t)g | (uintptr_t)out) & 15) == 0;
+    const int64_t blocks = (n + (wide ? 2047 : 255)) / (wide ? 2048 : 256);
+    const unsigned grid = (unsigned)(blocks < 152 * 8 ? blocks : 152 * 8);
+    if (wide) scan_step_kernel<T, GATE, 8><<<grid, 256, 0, st>>>(state, (const T *)x, (const T *)g, (T *)out, n);
+    else scan_step_kernel<T, GATE, 1><<<grid, 256, 0, st>>>(state, (const T *)x, (const T *)g, (T *)out, n);
     return cudaGetLastError();
 }
 
