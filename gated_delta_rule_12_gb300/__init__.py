@@ -417,6 +417,30 @@ def prologue_chunk_fwd(xq, xk, xv, wq, wk, wv, a, b, A_log, dt_bias, conv_state_
     return out, final_state
 
 
+# Calls of a few microseconds are held up by what surrounds them, so the wrappers below look torch's attributes up once
+# and take the current stream as the raw handle (0.1 us; the stream object takes 3).
+_F32, _BF16 = torch.float32, torch.bfloat16
+_empty, _empty_like = torch.empty, torch.empty_like
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_of(t, stream):
+    if stream is None:
+        return _raw_stream(t.get_device())
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _made_here(stream, *ts):
+    """Tensors that a wrapper allocated (from the current stream's memory) are used by a kernel on ``stream``: the
+    allocator keeps them until that work is done."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream)
+        for t in ts:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _check_scan_args(x, g, cu_seqlens, dtype, states, same):
     """Shapes, dtypes, placement and contiguity of a gated-scan call; returns (B, T, D, N).  ``states`` are the
     [N,D] fp32 tensors, ``same`` further tensors that must match g."""
@@ -440,7 +464,7 @@ def _check_scan_args(x, g, cu_seqlens, dtype, states, same):
     for t in states:
         if t is None:
             continue
-        if t.dtype != torch.float32:
+        if t.dtype != _F32:
             raise TypeError("states must be float32")
         if tuple(t.shape) != (N, D):
             raise ValueError(f"states must be [N,D] = {(N, D)}")
@@ -459,14 +483,15 @@ def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, input_gate=False, out
     lib = _lib or load_library()
     B, T, D, N = _check_scan_args(x, g, cu_seqlens, x.dtype, (init_state, final_state), (x, out))
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty_like(x)
     if final_state is None and output_final_state:
-        final_state = torch.empty((N, D), dtype=torch.float32, device=x.device)
+        final_state = _empty((N, D), dtype=_F32, device=x.device)
     rc = lib.gdn_gated_scan_fwd(x.data_ptr(), g.data_ptr(), _ptr(init_state), _ptr(cu_seqlens),
                                 N if cu_seqlens is not None else 0, out.data_ptr(), _ptr(final_state), B, T, D,
-                                _dt(x), int(bool(input_gate)), _stream(stream))
+                                _dt(x), int(bool(input_gate)), _stream_of(g, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_gated_scan_fwd")
+    _made_here(stream, out, final_state)
     return out, final_state
 
 
@@ -479,14 +504,15 @@ def gated_scan_bwd(x, g, out, dout, init_state=None, dfinal_state=None, cu_seqle
     if input_gate and x is None:
         raise ValueError("gated_scan_bwd: x is needed with the input gate")
     B, T, D, N = _check_scan_args(x, g, cu_seqlens, g.dtype, (init_state, dfinal_state), (out, dout))
-    dx, dg = torch.empty_like(g), torch.empty_like(g)
-    dinit = torch.empty((N, D), dtype=torch.float32, device=g.device) if want_dinit else None
+    dx, dg = _empty_like(g), _empty_like(g)
+    dinit = _empty((N, D), dtype=_F32, device=g.device) if want_dinit else None
     rc = lib.gdn_gated_scan_bwd(_ptr(x), g.data_ptr(), out.data_ptr(), dout.data_ptr(), _ptr(init_state),
                                 _ptr(dfinal_state), _ptr(cu_seqlens), N if cu_seqlens is not None else 0,
                                 dx.data_ptr(), dg.data_ptr(), _ptr(dinit), B, T, D, _dt(g), int(bool(input_gate)),
-                                _stream(stream))
+                                _stream_of(g, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_gated_scan_bwd")
+    _made_here(stream, dx, dg, dinit)
     return dx, dg, dinit
 
 
@@ -497,18 +523,19 @@ def gated_scan_step(state, x, g, input_gate=False, out=None, stream=None):
     if state.dim() != 2 or x.shape != state.shape or g.shape != state.shape or (out is not None and
                                                                                 out.shape != state.shape):
         raise ValueError("gated_scan_step: state, x, g and out must be [N,D]")
-    if state.dtype != torch.float32:
+    if state.dtype != _F32:
         raise TypeError("state must be float32")
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty_like(x)
     if g.dtype != x.dtype or out.dtype != x.dtype:
         raise TypeError("x, g and out must share one dtype")
     _need_cuda(state, x, g, out)
     N, D = state.shape
     rc = lib.gdn_gated_scan_step(state.data_ptr(), x.data_ptr(), g.data_ptr(), out.data_ptr(), N, D, _dt(x),
-                                 int(bool(input_gate)), _stream(stream))
+                                 int(bool(input_gate)), _stream_of(g, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_gated_scan_step")
+    _made_here(stream, out)
     return out
 
 
@@ -519,12 +546,12 @@ def _check_norm_args(x, params, stats, same):
     D = x.shape[-1]
     rows = x.numel() // D
     for t in params:
-        if t is not None and t.dtype != torch.float32:
+        if t is not None and t.dtype != _F32:
             raise TypeError("weight and bias must be float32")
-        if t is not None and tuple(t.shape) != (D,):
+        if t is not None and (t.dim() != 1 or t.numel() != D):
             raise ValueError("weight and bias must be [D]")
     for t in stats:
-        if t.dtype != torch.float32:
+        if t.dtype != _F32:
             raise TypeError("mean and rstd must be float32")
         if t.numel() != rows:
             raise ValueError("mean and rstd must hold one value a row")
@@ -544,18 +571,19 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     rows, D = _check_norm_args(x, (weight, bias), (), (out,))
     dt = _dt(x)
     if out is None:
-        out = torch.empty_like(x)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty_like(mean)
+        out = _empty_like(x)
+    mean = _empty(x.shape[:-1], dtype=_F32, device=x.device)
+    rstd = _empty_like(mean)
     rc = lib.gdn_layer_norm_fwd(x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), mean.data_ptr(),
-                                rstd.data_ptr(), rows, D, dt, float(eps), _stream(stream))
+                                rstd.data_ptr(), rows, D, dt, float(eps), _stream_of(x, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_layer_norm_fwd")
+    _made_here(stream, out, mean, rstd)
     return out, mean, rstd
 
 
 def layer_norm_bwd_workspace_size(rows, D, dtype=torch.bfloat16) -> int:
-    dt = GDN_BF16 if dtype == torch.bfloat16 else GDN_F32
+    dt = GDN_BF16 if dtype == _BF16 else GDN_F32
     return int(load_library().gdn_layer_norm_bwd_workspace_size(rows, D, dt))
 
 
@@ -565,18 +593,19 @@ def layer_norm_bwd(dout, x, mean, rstd, weight=None, workspace=None, stream=None
     lib = _lib or load_library()
     rows, D = _check_norm_args(x, (weight,), (mean, rstd), (dout,))
     dt = _dt(x)
-    dx = torch.empty_like(x)
-    dw = torch.empty(D, dtype=torch.float32, device=x.device)
-    db = torch.empty_like(dw)
+    dx = _empty_like(x)
+    dw = _empty(D, dtype=_F32, device=x.device)
+    db = _empty_like(dw)
     if workspace is None:
-        workspace = torch.empty(max(256, lib.gdn_layer_norm_bwd_workspace_size(rows, D, dt)), dtype=torch.uint8,
+        workspace = _empty(max(256, lib.gdn_layer_norm_bwd_workspace_size(rows, D, dt)), dtype=torch.uint8,
                                 device=x.device)
     _need_cuda(workspace)
     rc = lib.gdn_layer_norm_bwd(dout.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
                                 dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, D, dt, workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream(stream))
+                                workspace.numel() * workspace.element_size(), _stream_of(x, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_layer_norm_bwd")
+    _made_here(stream, dx, dw, db, workspace)
     return dx, dw, db
 
 
@@ -590,7 +619,7 @@ def _check_ce_args(h, weight, targets, rows):
     if tuple(targets.shape) != (h.shape[0],):
         raise ValueError("targets must be [N]")
     for t in rows:
-        if t.dtype != torch.float32:
+        if t.dtype != _F32:
             raise TypeError("lse and dloss must be float32")
         if tuple(t.shape) != (h.shape[0],):
             raise ValueError("lse and dloss must be [N]")
@@ -599,7 +628,7 @@ def _check_ce_args(h, weight, targets, rows):
 
 
 def linear_cross_entropy_workspace_size(N, D, V, dtype=torch.bfloat16, backward=False) -> int:
-    dt = GDN_BF16 if dtype == torch.bfloat16 else GDN_F32
+    dt = GDN_BF16 if dtype == _BF16 else GDN_F32
     return int(load_library().gdn_linear_cross_entropy_workspace_size(N, D, V, dt, int(bool(backward))))
 
 
@@ -613,17 +642,18 @@ def linear_cross_entropy_fwd(h, weight, targets, workspace=None, stream=None):
     lib = _lib or load_library()
     N, D, V = _check_ce_args(h, weight, targets, ())
     dt = _dt(h)
-    loss = torch.empty(N, dtype=torch.float32, device=h.device)
-    lse = torch.empty_like(loss)
+    loss = _empty(N, dtype=_F32, device=h.device)
+    lse = _empty_like(loss)
     if workspace is None:
-        workspace = torch.empty(max(256, lib.gdn_linear_cross_entropy_workspace_size(N, D, V, dt, 0)),
+        workspace = _empty(max(256, lib.gdn_linear_cross_entropy_workspace_size(N, D, V, dt, 0)),
                                 dtype=torch.uint8, device=h.device)
     _need_cuda(workspace)
     rc = lib.gdn_linear_cross_entropy_fwd(h.data_ptr(), weight.data_ptr(), targets.data_ptr(), loss.data_ptr(),
                                           lse.data_ptr(), N, D, V, dt, workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(), _stream(stream))
+                                          workspace.numel() * workspace.element_size(), _stream_of(h, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_linear_cross_entropy_fwd")
+    _made_here(stream, loss, lse, workspace)
     return loss, lse
 
 
@@ -633,17 +663,18 @@ def linear_cross_entropy_bwd(h, weight, targets, lse, dloss, workspace=None, str
     lib = _lib or load_library()
     N, D, V = _check_ce_args(h, weight, targets, (lse, dloss))
     dt = _dt(h)
-    dh, dw = torch.empty_like(h), torch.empty_like(weight)
+    dh, dw = _empty_like(h), _empty_like(weight)
     if workspace is None:
-        workspace = torch.empty(max(256, lib.gdn_linear_cross_entropy_workspace_size(N, D, V, dt, 1)),
+        workspace = _empty(max(256, lib.gdn_linear_cross_entropy_workspace_size(N, D, V, dt, 1)),
                                 dtype=torch.uint8, device=h.device)
     _need_cuda(workspace)
     rc = lib.gdn_linear_cross_entropy_bwd(h.data_ptr(), weight.data_ptr(), targets.data_ptr(), lse.data_ptr(),
                                           dloss.data_ptr(), dh.data_ptr(), dw.data_ptr(), N, D, V, dt,
                                           workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                          _stream(stream))
+                                          _stream_of(h, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_linear_cross_entropy_bwd")
+    _made_here(stream, dh, dw, workspace)
     return dh, dw
 
 

@@ -11,6 +11,7 @@
 // hence pairs of channels in one instruction and few, long iterations.
 #include "common.cuh"
 #include "kernels.h"
+#include "pairs.cuh"
 
 namespace gdn {
 namespace {
@@ -25,35 +26,6 @@ __device__ __forceinline__ void span(const GatedScanArgs &a, int n, int64_t &tok
         tok0 = (int64_t)n * a.T;
         len = a.T;
     }
-}
-
-// Arithmetic on two channels at once (fp32 pairs in a 64-bit register).
-using Pair = unsigned long long;
-
-__device__ __forceinline__ Pair pair(float lo, float hi)
-{
-    Pair r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void split(Pair p, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
-{
-    Pair r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b)
-{
-    Pair r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b)
-{
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 __device__ __forceinline__ float exp2_approx(float x)

@@ -3,15 +3,433 @@
 //     y = (x - mean) rstd w + b,   rstd = 1 / sqrt(mean((x - mean)^2) + eps)
 // Backward, with xhat = (x - mean) rstd and u = dy w:
 //     dx = rstd (u - mean(u) - xhat mean(u xhat)),   dw = sum_rows dy xhat,   db = sum_rows dy.
+//
+// Bound by memory: x and y forward; dy, x and dx backward.  A team of threads holds a row in registers, so each row is
+// read once; the variance comes from the deviations in registers.  A thread keeps the same columns for every row of
+// its team: w and b are read once a thread, and dw and db gather in registers, join over the CTA's teams in shared
+// memory and leave one partial row a CTA, which a second kernel adds up.  Rows come four ahead through asynchronous
+// copies: 32 KB of them in flight on an SM, as registers one row ahead allow, held the backward pass to 3.9 TB/s and
+// the norm over heads (131072 x 128) to 2.6.  Rows of more than 16384 elements go through kernels that read them again.
+//
+// Measured (GB300, bf16, device time): forward 8192 x 2048 14.8 us (4.6 TB/s); backward 25.2 us, 131072 x 128 backward
+// 24.1 us (4.0 and 4.2 TB/s), of which about 3 us are the second kernel and the gap before it.
 #include "common.cuh"
 #include "kernels.h"
+#include "pairs.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
+// ---------------------------------------------------------------------------
+// rows in registers
+// ---------------------------------------------------------------------------
 
-// Sum over the block, the same bits in every thread.
+constexpr int kSMs = 152;
+
+// VW elements as one access: 16 bytes, or one element where rows are not aligned for more.
+template <typename T, int VW>
+struct Raw {
+    static constexpr int kWords = VW * sizeof(T) / 4 > 0 ? VW * sizeof(T) / 4 : 1;
+    uint32_t w[kWords];
+    __device__ __forceinline__ float get(int j) const
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+        else return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    }
+};
+
+// Rows on their way: every thread copies its own accesses into its own slots, kStages rows ahead, and reads them back
+// itself, so the ring needs no barrier and no registers.  A missing access reads as zeros.  Single bf16 elements have
+// no asynchronous copy and go through a register.  MAX threads' slots take up to 128 KB.
+template <typename T, int VW, int NV, int TENSORS, int MAX>
+struct Ring {
+    static constexpr int kBytes = Raw<T, VW>::kWords * 4;
+    static constexpr int kFit = 128 * 1024 / (TENSORS * NV * kBytes * (MAX < 512 ? 512 : MAX));
+    static constexpr int kStages = kFit >= 4 ? 4 : kFit >= 2 ? 2 : 1;
+    uint32_t base;
+    static __host__ __device__ int bytes(int threads) { return kStages * TENSORS * NV * kBytes * threads; }
+    __device__ __forceinline__ explicit Ring(const void *smem)
+        : base(static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * kBytes) {}
+    __device__ __forceinline__ uint32_t slot(int stage, int tensor, int v) const
+    {
+        return base + ((stage * TENSORS + tensor) * NV + v) * (blockDim.x * kBytes);
+    }
+    __device__ __forceinline__ void load(int stage, int tensor, int v, const T *p, bool in) const   // p is read if `in`
+    {
+        if constexpr (kBytes == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                         :: "r"(slot(stage, tensor, v)), "l"(p), "r"(in ? 16 : 0) : "memory");
+        else if constexpr (sizeof(T) == 4)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                         :: "r"(slot(stage, tensor, v)), "l"(p), "r"(in ? 4 : 0) : "memory");
+        else
+            asm volatile("st.shared.b32 [%0], %1;"
+                         :: "r"(slot(stage, tensor, v)),
+                            "r"(in ? (uint32_t)__ldcs(reinterpret_cast<const unsigned short *>(p)) : 0u) : "memory");
+    }
+    __device__ __forceinline__ void read(int stage, int tensor, Raw<T, VW> (&r)[NV]) const
+    {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if constexpr (kBytes == 16)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(r[v].w[0]), "=r"(r[v].w[1]), "=r"(r[v].w[2]), "=r"(r[v].w[3])
+                             : "r"(slot(stage, tensor, v)) : "memory");
+            else
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[v].w[0]) : "r"(slot(stage, tensor, v)) : "memory");
+    }
+};
+
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+// A thread's NV accesses as pairs: pair i holds elements 2 i and 2 i + 1 of the NV * VW.
+template <typename T, int VW, int NV>
+__device__ __forceinline__ Pair get_pair(const Raw<T, VW> (&raw)[NV], int i)
+{
+    if constexpr (VW == 1) return pair(raw[2 * i].get(0), raw[2 * i + 1].get(0));
+    else return pair(raw[2 * i / VW].get(2 * i % VW), raw[2 * i / VW].get(2 * i % VW + 1));
+}
+
+// Access v of the row at `row`, at column c.
+template <typename T, int VW, int N>
+__device__ __forceinline__ void put(T *p, const Pair (&y)[N], int v)
+{
+    if constexpr (VW == 1) {
+        float a, b;
+        split(y[v / 2], a, b);
+        *p = from_f32<T>(v & 1 ? b : a);
+    } else if constexpr (sizeof(T) == 4) {
+        float4 r;
+        split(y[2 * v], r.x, r.y);
+        split(y[2 * v + 1], r.z, r.w);
+        *reinterpret_cast<float4 *>(p) = r;
+    } else {
+        uint4 r;
+        uint32_t *w = reinterpret_cast<uint32_t *>(&r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            split(y[4 * v + i], a, b);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
+        }
+        *reinterpret_cast<uint4 *>(p) = r;
+    }
+}
+
+__device__ __forceinline__ float total(Pair p)
+{
+    float a, b;
+    split(p, a, b);
+    return a + b;
+}
+
+__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
+
+// Sums of N values over a team, the same bits in every thread of it: shuffles within a warp, then, for teams of
+// several warps, their sums in order through `sh` behind a barrier of the team's own.
+template <int TEAM, int N>
+struct TeamSum {
+    float *mine, *all;   // where the warp's sums go, where the team's start
+    int size, warps, barrier, other;
+    __device__ __forceinline__ TeamSum(float *sh, int team_size)   // sh: [2][N][warps of the CTA]
+    {
+        size = team_size;
+        warps = team_size / 32;
+        barrier = 1 + threadIdx.x / team_size;
+        mine = sh + (threadIdx.x >> 5);
+        all = sh + (threadIdx.x / team_size) * warps;
+        other = N * (blockDim.x >> 5);      // by turns, so that one barrier a sum is enough
+    }
+    __device__ __forceinline__ void operator()(float (&v)[N])
+    {
+#pragma unroll
+        for (int o = (TEAM ? TEAM : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if constexpr (TEAM == 0) {
+            const int row = blockDim.x >> 5;
+            if ((threadIdx.x & 31) == 0)
+#pragma unroll
+                for (int i = 0; i < N; ++i) mine[i * row] = v[i];
+            asm volatile("bar.sync %0, %1;" :: "r"(barrier), "r"(size) : "memory");
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = 0.f;
+            if (warps == 2) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float2 p = *reinterpret_cast<const float2 *>(all + i * row);
+                    v[i] = p.x + p.y;
+                }
+            } else {
+                for (int w = 0; w < warps; w += 4)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const float4 p = *reinterpret_cast<const float4 *>(all + i * row + w);
+                        v[i] += (p.x + p.y) + (p.z + p.w);
+                    }
+            }
+            mine += other;
+            all += other;
+            other = -other;
+        }
+    }
+};
+
+// 1 / sqrt(v): the hardware's approximation and one step of Newton's iteration (1 ulp; the division and square root
+// of IEEE rounding take 30 instructions a row more).
+__device__ __forceinline__ float inv_sqrt(float v)
+{
+    const float r = rsqrtf(v);
+    const float e = fmaf(v * r, -r, 1.f);
+    return r < 1e18f ? fmaf(0.5f * r, e, r) : r;   // v = 0 has no step: infinite as it is
+}
+
+// TEAM: threads of a row's team where they are a part of a warp or a warp, 0 for `team` threads of several warps.
+// MAX: most threads a CTA.  FULL: the row fills the team, no access is missing.
+template <typename T, int VW, int NV, int TEAM, int MAX, bool FULL>
+__global__ void __launch_bounds__(MAX, MAX == 256 ? (NV * VW <= 8 ? 4 : NV * VW <= 16 ? 3 : 2) : 1)
+rows_fwd_kernel(const LayerNormArgs a, int team)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ __align__(16) float sh[2 * 32];
+    using Rows = Ring<T, VW, NV, 1, MAX>;
+    constexpr int kStages = Rows::kStages;
+    const Rows ring(smem);
+    if (TEAM) team = TEAM;
+    TeamSum<TEAM, 1> sum(sh, team);
+    constexpr int NP = NV * VW / 2;
+    const int lane = threadIdx.x % team, teams = blockDim.x / team;
+    const int64_t step = (int64_t)gridDim.x * teams;
+    const float inv = 1.f / (float)a.D;
+    bool live[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) live[v] = FULL || (v * team + lane) * VW < a.D;
+    // every team of a CTA goes through the same number of rows: the shuffles take whole warps
+    int64_t r = (int64_t)blockIdx.x * teams + threadIdx.x / team;
+    const T *next = (const T *)a.x + r * a.D + lane * VW;
+    T *y = (T *)a.out + r * a.D + lane * VW;
+    const int64_t step_d = step * a.D;
+    auto load = [&](int stage, bool in) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) ring.load(stage, 0, v, next + v * team * VW, in && live[v]);
+        commit_copies();
+        next += step_d;
+    };
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) load(k, r + k * step < a.rows);
+    Pair w[NP], b[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        float wv[2], bv[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int v = (2 * i + k) / VW, c = (v * team + lane) * VW + (2 * i + k) % VW;
+            wv[k] = live[v] && a.weight ? a.weight[c] : 1.f;
+            bv[k] = live[v] && a.bias ? a.bias[c] : 0.f;
+        }
+        w[i] = pair(wv[0], wv[1]);
+        b[i] = pair(bv[0], bv[1]);
+    }
+    const int64_t rows_ahead = a.rows - kStages * step;
+    int stage = 0;
+    for (int64_t first = (int64_t)blockIdx.x * teams; first < a.rows; first += step, r += step, y += step_d) {
+        Raw<T, VW> raw[NV];
+        wait_copies<kStages - 1>();
+        ring.read(stage, 0, raw);
+        Pair x[NP], p = 0, q = 0;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            x[i] = get_pair<T, VW, NV>(raw, i);
+            if (i & 1) q = add2(q, x[i]);
+            else p = add2(p, x[i]);
+        }
+        load(stage, r < rows_ahead);
+        stage = (stage + 1) & (kStages - 1);
+        float s[1] = {total(add2(p, q))};
+        sum(s);
+        const float mean = s[0] * inv;
+        p = q = 0;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            x[i] = add2(x[i], both(-mean));
+            if constexpr (VW == 1) {   // columns behind D take no part
+                if (!live[2 * i + 1]) {
+                    float lo, hi;
+                    split(x[i], lo, hi);
+                    x[i] = pair(live[2 * i] ? lo : 0.f, 0.f);
+                }
+            } else {
+                if (!live[2 * i / VW]) x[i] = 0;
+            }
+            if (i & 1) q = fma2(x[i], x[i], q);
+            else p = fma2(x[i], x[i], p);
+        }
+        s[0] = total(add2(p, q));
+        sum(s);
+        const float rstd = inv_sqrt(fmaf(s[0], inv, a.eps));
+        if (r < a.rows) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) x[i] = fma2(mul2(x[i], both(rstd)), w[i], b[i]);
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (live[v]) put<T, VW>(y + v * team * VW, x, v);
+            if (lane == 0) {
+                if (a.mean) a.mean[r] = mean;
+                if (a.rstd) a.rstd[r] = rstd;
+            }
+        }
+    }
+    wait_copies<0>();
+}
+
+template <typename T, int VW, int NV, int TEAM, int MAX, bool FULL>
+__global__ void __launch_bounds__(MAX, MAX == 512 && NV * VW <= 8 ? 2 : 1) rows_bwd_kernel(const LayerNormArgs a, int team)
+{
+    extern __shared__ __align__(16) unsigned char smem[];   // the ring; at the end the sums
+    __shared__ __align__(16) float sh[2 * 32 * 2];
+    using Rows = Ring<T, VW, NV, 2, MAX>;
+    constexpr int kStages = Rows::kStages;
+    const Rows ring(smem);
+    if (TEAM) team = TEAM;
+    TeamSum<TEAM, 2> sum(sh, team);
+    constexpr int NP = NV * VW / 2;
+    const int lane = threadIdx.x % team, teams = blockDim.x / team;
+    const int64_t step = (int64_t)gridDim.x * teams;
+    const float inv = 1.f / (float)a.D;
+    bool live[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) live[v] = FULL || (v * team + lane) * VW < a.D;
+    int64_t r = (int64_t)blockIdx.x * teams + threadIdx.x / team;
+    int64_t at = r * a.D + lane * VW;
+    T *dx = (T *)a.dx + at;
+    const int64_t step_d = step * a.D;
+    auto load = [&](int stage, bool in) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            ring.load(stage, 0, v, (const T *)a.x + at + v * team * VW, in && live[v]);
+            ring.load(stage, 1, v, (const T *)a.dout + at + v * team * VW, in && live[v]);
+        }
+        commit_copies();
+        at += step_d;
+    };
+    // the statistics come two rows ahead, in registers
+    float2 stat[2];
+    auto load_stat = [&](int64_t r) { return r < a.rows ? make_float2(__ldg(a.mean + r), __ldg(a.rstd + r)) : make_float2(0.f, 0.f); };
+    stat[0] = load_stat(r);
+    stat[1] = load_stat(r + step);
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) load(k, r + k * step < a.rows);
+    Pair w[NP], dw[NP], db[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        float wv[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int v = (2 * i + k) / VW, c = (v * team + lane) * VW + (2 * i + k) % VW;
+            wv[k] = live[v] && a.weight ? a.weight[c] : 1.f;
+        }
+        w[i] = pair(wv[0], wv[1]);
+        dw[i] = db[i] = 0;
+    }
+    const int64_t rows_ahead = a.rows - kStages * step;
+    int stage = 0;
+    for (int64_t first = (int64_t)blockIdx.x * teams; first < a.rows; first += step, r += step, dx += step_d) {
+        const float mean = stat[0].x, rstd = stat[0].y;
+        stat[0] = stat[1];
+        stat[1] = load_stat(r + 2 * step);
+        Raw<T, VW> rx[NV], rd[NV];
+        wait_copies<kStages - 1>();
+        ring.read(stage, 0, rx);
+        ring.read(stage, 1, rd);
+        Pair xh[NP], u[NP], p = 0, q = 0;
+        // columns behind D: dy = 0, so u, its sums and the gradients' stay 0
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const Pair dy = get_pair<T, VW, NV>(rd, i);
+            xh[i] = mul2(add2(get_pair<T, VW, NV>(rx, i), both(-mean)), both(rstd));
+            u[i] = mul2(dy, w[i]);
+            p = add2(p, u[i]);
+            q = fma2(u[i], xh[i], q);
+            dw[i] = fma2(dy, xh[i], dw[i]);
+            db[i] = add2(db[i], dy);
+        }
+        load(stage, r < rows_ahead);
+        stage = (stage + 1) & (kStages - 1);
+        float s[2] = {total(p), total(q)};
+        sum(s);
+        const float c1 = s[0] * inv, c2 = s[1] * inv;
+        if (a.dx && r < a.rows) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                u[i] = mul2(both(rstd), add2(u[i], fma2(xh[i], both(-c2), both(-c1))));
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (live[v]) put<T, VW>(dx + v * team * VW, u, v);
+        }
+    }
+    // the CTA's teams: those of a warp by shuffles, then one row [dw | db] a warp or team in shared memory, in order
+    wait_copies<0>();
+    if (!a.dweight && !a.dbias) return;
+    __syncthreads();
+    float *joined = reinterpret_cast<float *>(smem);
+    const int own = TEAM && TEAM < 32 ? 32 : team, rows = blockDim.x / own;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        float g[4];
+        split(dw[i], g[0], g[1]);
+        split(db[i], g[2], g[3]);
+#pragma unroll
+        for (int o = TEAM ? TEAM : 32; o < 32; o *= 2)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) g[k] += __shfl_xor_sync(0xffffffffu, g[k], o);
+        if (threadIdx.x % own == lane)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int v = (2 * i + (k & 1)) / VW, c = (v * team + lane) * VW + (2 * i + (k & 1)) % VW;
+                if (live[v]) joined[((threadIdx.x / own) * 2 + (k >> 1)) * a.D + c] = g[k];
+            }
+    }
+    __syncthreads();
+    float *part = (float *)a.workspace + (int64_t)blockIdx.x * 2 * a.D;
+    for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) {
+        float t = joined[i];
+        for (int k = 1; k < rows; ++k) t += joined[k * 2 * a.D + i];
+        part[i] = t;
+    }
+}
+
+// Adds up `parts` partial rows [dw | db]: 32 columns a block, every eighth row a warp, in order.
+__global__ void __launch_bounds__(256) join_kernel(const LayerNormArgs a, int parts)
+{
+    __shared__ float sh[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane, n = 2 * (int64_t)a.D;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched beside the kernel that writes the partial rows
+    float s = 0.f;
+    if (c < n)
+        for (int p = warp; p < parts; p += 8) s += ((const float *)a.workspace)[p * n + c];
+    sh[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < n) {
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += sh[i][lane];
+        if (c < a.D) {
+            if (a.dweight) a.dweight[c] = s;
+        } else if (a.dbias) {
+            a.dbias[c - a.D] = s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// longer rows: a CTA a row, read again for every pass
+// ---------------------------------------------------------------------------
+
+constexpr int kThreads = 256;
+constexpr int kRowSplits = 32;    // row ranges whose partial sums dw and db are joined from
+
 __device__ __forceinline__ float block_sum(float v, float *sh)
 {
     v = warp_sum(v);
@@ -23,9 +441,8 @@ __device__ __forceinline__ float block_sum(float v, float *sh)
     return s;
 }
 
-// One block per row; the variance from a second pass over the row's deviations.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_fwd_kernel(LayerNormArgs a)
+__global__ void __launch_bounds__(kThreads) long_fwd_kernel(const LayerNormArgs a)
 {
     __shared__ float sh[kThreads / 32];
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
@@ -52,7 +469,7 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_kernel(LayerNormArgs a)
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_dx_kernel(LayerNormArgs a)
+__global__ void __launch_bounds__(kThreads) long_dx_kernel(const LayerNormArgs a)
 {
     __shared__ float sh[kThreads / 32];
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
@@ -73,11 +490,9 @@ __global__ void __launch_bounds__(kThreads) norm_dx_kernel(LayerNormArgs a)
     }
 }
 
-constexpr int kRowSplits = 128;   // row ranges whose partial sums dw and db are joined from
-
 // Partial sums of dw and db over one of kRowSplits row ranges, a thread per channel.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_dw_partial_kernel(LayerNormArgs a)
+__global__ void __launch_bounds__(kThreads) long_dw_kernel(const LayerNormArgs a)
 {
     const int ch = blockIdx.x * kThreads + threadIdx.x;
     if (ch >= a.D) return;
@@ -94,41 +509,138 @@ __global__ void __launch_bounds__(kThreads) norm_dw_partial_kernel(LayerNormArgs
     part[a.D + ch] = sb;
 }
 
-__global__ void __launch_bounds__(kThreads) norm_dw_join_kernel(LayerNormArgs a)
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+constexpr int kMost = 16384;   // elements of a row that 1024 threads hold
+
+struct Shape { int team, wide; };   // threads a row; whether a thread takes 16 elements or fewer
+
+// The smallest team, a power of two from 8 to 1024, whose threads can take the row at `many` accesses each; a part of
+// a warp, or a warp, at `few` where that is enough.  8192 x 2048 bf16: forward 32 elements a thread 14.8 us, 16
+// elements 15.5, 8 elements 19.8; backward, whose dw and db take twice as many registers, 16 elements 25.2 us,
+// 8 elements 29.4, 32 elements (spilling) 51.
+Shape shape(int D, int vw, int few, int many)
 {
-    const int ch = blockIdx.x * kThreads + threadIdx.x;
-    if (ch >= a.D) return;
-    float sw = 0.f, sb = 0.f;
-    for (int s = 0; s < kRowSplits; ++s) {
-        sw += ((const float *)a.workspace)[(int64_t)s * 2 * a.D + ch];
-        sb += ((const float *)a.workspace)[(int64_t)s * 2 * a.D + a.D + ch];
+    const int nvec = ceil_div(D, vw);
+    for (int g = 8; g <= 32; g *= 2)
+        if (nvec <= g * few) return {g, 0};
+    for (int g = 32; g <= 1024; g *= 2)
+        if (nvec <= g * many) return {g, 1};
+    return {0, 0};
+}
+
+template <typename T, int VW, int NV, int TEAM, int MAX, bool FULL>
+cudaError_t run_fwd(const LayerNormArgs &a, int team, cudaStream_t st)
+{
+    const int threads = team > 256 ? team : 256, smem = Ring<T, VW, NV, 1, MAX>::bytes(threads);
+    const int64_t ctas = (a.rows + threads / team - 1) / (threads / team);
+    const int most = kSMs * (threads > 256 ? 1 : NV * VW <= 8 ? 4 : NV * VW <= 16 ? 3 : 2);
+    if (smem > 32 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(rows_fwd_kernel<T, VW, NV, TEAM, MAX, FULL>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
     }
-    if (a.dweight) a.dweight[ch] = sw;
-    if (a.dbias) a.dbias[ch] = sb;
+    rows_fwd_kernel<T, VW, NV, TEAM, MAX, FULL><<<(unsigned)(ctas < most ? ctas : most), threads, smem, st>>>(a, team);
+    return cudaGetLastError();
+}
+
+// CTAs of 512 threads that an SM holds in the backward kernel: two where a thread has 8 elements or fewer.
+int bwd_ctas(int D) { return D <= 256 ? 2 * kSMs : kSMs; }
+
+cudaError_t launch_join(const LayerNormArgs &a, int parts, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((2 * (int64_t)a.D + 31) / 32));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel, a, parts);
+}
+
+template <typename T, int VW, int NV, int TEAM, int MAX, bool FULL>
+cudaError_t run_bwd(const LayerNormArgs &a, int team, cudaStream_t st)
+{
+    const int threads = team > MAX ? team : MAX;
+    const int64_t ctas = (a.rows + threads / team - 1) / (threads / team);
+    const int most = bwd_ctas(a.D), grid = (int)(ctas < most ? (ctas > 0 ? ctas : 1) : most);
+    const bool sums = a.dweight || a.dbias;
+    const int own = team < 32 ? 32 : team, joined = sums ? threads / own * 2 * a.D * 4 : 0;
+    const int ring = Ring<T, VW, NV, 2, MAX>::bytes(threads), smem = joined > ring ? joined : ring;
+    if (smem > 32 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(rows_bwd_kernel<T, VW, NV, TEAM, MAX, FULL>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    rows_bwd_kernel<T, VW, NV, TEAM, MAX, FULL><<<grid, threads, smem, st>>>(a, team);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess || !sums ? e : launch_join(a, grid, st);
+}
+
+template <typename T, int VW, bool BWD>
+cudaError_t run(const LayerNormArgs &a, cudaStream_t st)
+{
+    constexpr int few = VW == 1 ? 4 : 8 / VW, many = VW == 1 ? 16 : (BWD ? 16 : 32) / VW;
+    const Shape s = shape(a.D, VW, few, many);
+    const bool full = VW > 1 && a.D == s.team * VW * (s.wide ? many : few);
+#define GDN_NORM1(NV, TEAM, MAX, FULL) \
+    (BWD ? run_bwd<T, VW, NV, TEAM, MAX, FULL>(a, s.team, st) : run_fwd<T, VW, NV, TEAM, MAX, FULL>(a, s.team, st))
+#define GDN_NORM(NV, TEAM, FMAX, BMAX) \
+    (full ? GDN_NORM1(NV, TEAM, (BWD ? BMAX : FMAX), (VW > 1)) : GDN_NORM1(NV, TEAM, (BWD ? BMAX : FMAX), false))
+    if (s.team == 8) return GDN_NORM(few, 8, 256, 512);
+    if (s.team == 16) return GDN_NORM(few, 16, 256, 512);
+    if (s.team == 32) return s.wide ? GDN_NORM(many, 32, 256, 512) : GDN_NORM(few, 32, 256, 512);
+    if (s.team == 1024) return GDN_NORM(many, 0, 1024, 1024);
+    return s.team <= 256 ? GDN_NORM(many, 0, 256, 512) : GDN_NORM(many, 0, 512, 512);
+#undef GDN_NORM
+#undef GDN_NORM1
+}
+
+bool vectors_fit(const LayerNormArgs &a)
+{
+    const uintptr_t all = (uintptr_t)a.x | (uintptr_t)a.out | (uintptr_t)a.dout | (uintptr_t)a.dx |
+                          (uintptr_t)a.D * (a.dt ? 2 : 4);
+    return (all & 15) == 0;
+}
+
+template <typename T>
+cudaError_t fwd(const LayerNormArgs &a, cudaStream_t st)
+{
+    if (a.D > kMost) {
+        long_fwd_kernel<T><<<(unsigned)(a.rows < kSMs * 8 ? a.rows : kSMs * 8), kThreads, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    return vectors_fit(a) ? run<T, 16 / sizeof(T), false>(a, st) : run<T, 1, false>(a, st);
 }
 
 template <typename T>
 cudaError_t bwd(const LayerNormArgs &a, cudaStream_t st)
 {
-    const unsigned blocks = (unsigned)(a.rows < 152 * 8 ? a.rows : 152 * 8);
-    if (a.dx && blocks) norm_dx_kernel<T><<<blocks, kThreads, 0, st>>>(a);
-    if (a.dweight || a.dbias) {
-        norm_dw_partial_kernel<T><<<dim3(ceil_div(a.D, kThreads), kRowSplits), kThreads, 0, st>>>(a);
-        norm_dw_join_kernel<<<ceil_div(a.D, kThreads), kThreads, 0, st>>>(a);
-    }
-    return cudaGetLastError();
+    if (a.D <= kMost) return vectors_fit(a) ? run<T, 16 / sizeof(T), true>(a, st) : run<T, 1, true>(a, st);
+    const unsigned blocks = (unsigned)(a.rows < kSMs * 8 ? a.rows : kSMs * 8);
+    if (a.dx && blocks) long_dx_kernel<T><<<blocks, kThreads, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || (!a.dweight && !a.dbias)) return e;
+    long_dw_kernel<T><<<dim3(ceil_div(a.D, kThreads), kRowSplits), kThreads, 0, st>>>(a);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join(a, kRowSplits, st);
 }
 
 }  // namespace
 
-size_t layer_norm_bwd_workspace_bytes(int64_t, int D, int) { return align256((size_t)kRowSplits * 2 * D * 4); }
+size_t layer_norm_bwd_workspace_bytes(int64_t, int D, int)
+{
+    return align256((size_t)(D > kMost ? kRowSplits : bwd_ctas(D)) * 2 * D * 4);
+}
 
 cudaError_t launch_layer_norm_fwd(const LayerNormArgs &a, cudaStream_t st)
 {
-    const unsigned blocks = (unsigned)(a.rows < 152 * 8 ? a.rows : 152 * 8);
-    if (a.dt) norm_fwd_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a);
-    else norm_fwd_kernel<float><<<blocks, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return a.dt ? fwd<__nv_bfloat16>(a, st) : fwd<float>(a, st);
 }
 
 cudaError_t launch_layer_norm_bwd(const LayerNormArgs &a, cudaStream_t st)
