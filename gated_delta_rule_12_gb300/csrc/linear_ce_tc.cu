@@ -1,7 +1,7 @@
 // linear_ce_tc.cu -- the linear cross entropy's products on the tensor cores (bf16, D a multiple of 8).
 //
 // One persistent kernel form serves the three products, each over 256 x 256 tiles of a pair of CTAs:
-//   logits   [h | w]     A = h  (K = D contiguous),     B = w (K contiguous):    a row's (max, sum) per 256 words
+//   logits   [h | w]     A = h  (K = D contiguous),     B = w (K contiguous):    a row's (max, sum) per tile
 //   E        same operands, recomputed for one piece of the vocabulary:          E = softmax - onehot, bf16
 //   gradients            dW: A = E^T, B = dloss h (both with K = tokens as rows),  dW of the piece
 //                        dh: A = E (K = words contiguous), B = w (K as rows),    fp32 sums over the pieces
@@ -10,7 +10,8 @@
 // them, so that one tile's epilogue runs under the next one's products.  A pair reads half of B per CTA, which
 // brings shared-memory traffic under the 128 B a clock that one-CTA tiles of this size exceed.
 // Roles: warp 0 issues the TMA loads of its CTA, warp 1 of the even CTA the MMAs, warps 2-5 the epilogue (a thread a
-// row; 32 tensor-memory lanes a warp).
+// row; 32 tensor-memory lanes a warp).  Eight epilogue warps, half of the columns each, measured slower (255 tokens,
+// 50257 words: 35 us against 31).
 //
 // Precision: operands are bf16, sums fp32.  E is rounded to bf16 (relative 2^-8, independent from entry to entry, as
 // exact as the inputs that it meets).  It is kept free of dloss: a target's entry is mostly close to -1, where bf16 is
@@ -19,11 +20,17 @@
 // rounding).  dh takes dloss in fp32 at its end.  dW takes it through its other operand, h dloss / s with s = max
 // |dloss| over the kept rows, which is h itself where all rows weigh the same, and multiplies by s in fp32 at its end.
 //
+// Bound by the tensor cores, or by reading w where tokens are few.  Measured on the device: loss of 8192 x 2048 x 32768
+// 0.54 ms (2.0 PFLOP/s), gradient with 65536 words 3.55 ms (1.86 PFLOP/s); both run into the power limit when repeated
+// (0.62 and 4.04 ms).  Loss of 255 x 1024 x 50257 31 us, half of the copy rate: three rounds of tiles and what
+// surrounds them.
+//
 // Every wait on an mbarrier is bounded (1 s); a timeout records kDevErrTimeout in the workspace's error word, and the
 // CTA's roles unwind to the common exit, where both CTAs meet before tensor memory is freed.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <stdint.h>
 #include <string.h>
 
 #include "common.cuh"
@@ -40,9 +47,10 @@ constexpr int kHalf = 128;                 // a CTA's rows of A and of B
 constexpr int kDepth = 64;                 // K of one stage: 128 B, the swizzle's width
 constexpr int kStages = 6;
 constexpr int kStageBytes = 2 * kHalf * kDepth * 2;
-constexpr int kStore = 4096;               // a warp's store buffer: 32 rows of 128 B; two a warp
-constexpr int kThreads = 192;
-constexpr int kSmem = 1024 + kStages * kStageBytes + 4 * 2 * kStore + 256;
+constexpr int kStore = 4096;               // a warp's store buffer: 32 rows of 128 B
+constexpr int kEpilogueWarps = 4;
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kStore + 256;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr int kPairs = 76;                 // CTA pairs the GPU holds at once (152 SMs)
 
@@ -59,13 +67,14 @@ struct Product {
 struct CeParams {
     Product p[2];             // kGrads: dW, dh; else p[0]
     int tiles0, tiles;        // tiles of p[0]; of both
+    int width;                // columns of a tile; kTile but for kLogits
     int N, V, D;
     int v0, cols;             // the piece (kProb), the whole vocabulary (kLogits)
     int accumulate;           // kGrads: dh adds to the earlier pieces' sums
     const int32_t *targets;
     const float *lse_in;
     const float *scale;       // kGrads: s
-    float2 *part;             // kLogits: [tiles of 256 words][N]
+    float2 *part;             // kLogits: [tiles of `width` words][N]
     float *at;                // kLogits: [N]
     unsigned *err;
     int clear_err;            // the call's first kernel
@@ -197,10 +206,8 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-__device__ __forceinline__ void wait_store_read1()   // all but the latest store group have read their source
-{
-    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
+__device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Which product, tile and K range a tile index stands for.
 struct Tile {
@@ -243,7 +250,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t stores = base + kStages * kStageBytes;
-    const uint32_t bars = stores + 4 * 2 * kStore;
+    const uint32_t bars = stores + kEpilogueWarps * kStore;
     const uint32_t full = bars, empty = bars + 8 * kStages, acc_full = bars + 16 * kStages, acc_empty = acc_full + 16;
     const uint32_t tmem_slot = acc_empty + 16, abort_addr = tmem_slot + 4;
     unsigned char *gen = smem_raw + (base - smem_u32(smem_raw));
@@ -251,6 +258,11 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
 
+    if (threadIdx.x == 32) {
+        prefetch_tmap(&maps.a[0]);
+        prefetch_tmap(&maps.b[0]);
+        if (MODE == kGrads) { prefetch_tmap(&maps.a[1]); prefetch_tmap(&maps.b[1]); }
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, 1);
@@ -258,11 +270,10 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, 8);   // four epilogue warps of both CTAs
+            mbar_init(acc_empty + 8 * i, 2 * kEpilogueWarps);   // of both CTAs
         }
         fence_mbar_init();
         *abort_flag = 0;
-        if (blockIdx.x == 0 && p.clear_err) *p.err = kDevErrNone;   // a timeout comes a second later at the earliest
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -274,8 +285,13 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
     cluster_sync();
     fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(gen + (tmem_slot - base));
+    // The next kernel of the stream may take the SMs as they fall free; this one touches memory once the last is done.
+    start_next();
+    wait_previous();
+    if (threadIdx.x == 0 && blockIdx.x == 0 && p.clear_err) *p.err = kDevErrNone;   // a timeout comes a second later at the earliest
 
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int width = MODE == kLogits ? p.width : kTile;
     if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
@@ -285,12 +301,12 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 const Product &q = p.p[c.which];
                 const CUtensorMap *ma = &maps.a[c.which], *mb = &maps.b[c.which];
                 const bool a_mn = MODE == kGrads && c.which == 0, b_mn = MODE == kGrads;
-                const int m0 = c.m * kTile + (int)rank * kHalf, n0 = c.n * kTile + (int)rank * kHalf;
+                const int m0 = c.m * kTile + (int)rank * kHalf, n0 = c.n * width + (int)rank * (width / 2);
                 for (int k = c.k0; k < c.k1; ++k, ++it) {
                     const uint32_t s = it % kStages, ph = (it / kStages) & 1;
                     if (!wait_bar(empty + 8 * s, ph ^ 1, abort_flag, p.err)) { ok = false; break; }
                     const uint32_t bar = map_to_rank(full + 8 * s, 0);
-                    if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * kStageBytes);
+                    if (rank == 0) mbar_expect_tx(full + 8 * s, kStageBytes + width * kDepth * 2);
                     const uint32_t sa = base + s * kStageBytes, sb = sa + kStageBytes / 2;
                     if (a_mn) {
                         load_2d(sa, ma, m0, k * kDepth, bar);
@@ -323,7 +339,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 const Tile c = tile_of<MODE>(p, t);
                 if (c.k0 >= c.k1) continue;
                 const bool a_mn = MODE == kGrads && c.which == 0, b_mn = MODE == kGrads;
-                const uint32_t idesc = idesc_bf16(kTile, kTile, a_mn, b_mn);
+                const uint32_t idesc = idesc_bf16(kTile, width, a_mn, b_mn);
                 const uint32_t buf = tiles & 1, use = tiles >> 1;
                 ++tiles;
                 if (!wait_bar(acc_empty + 8 * buf, (use & 1) ^ 1, abort_flag, p.err)) break;
@@ -346,16 +362,17 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
         }
     } else {
         const uint32_t quarter = warp & 3;                     // the 32 tensor-memory lanes a warp may read
-        const uint32_t buf0 = stores + quarter * 2 * kStore;
+        const int chunks = width / 32;
+        const uint32_t buf0 = stores + (warp - 2) * kStore;
         const uint32_t leader_empty = map_to_rank(acc_empty, 0);
-        uint32_t tiles = 0, nstore = 0;
+        uint32_t tiles = 0;
         for (int t = pair; t < p.tiles; t += pairs) {
             const Tile c = tile_of<MODE>(p, t);
             if (c.k0 >= c.k1) continue;
             const uint32_t buf = tiles & 1, use = tiles >> 1;
             ++tiles;
             const int row0 = c.m * kTile + (int)rank * kHalf + (int)quarter * 32, row = row0 + lane;
-            const int col0 = c.n * kTile;
+            const int col0 = c.n * width;
             const bool in = row < p.N;
             int target = -1;
             float lse = 0.f, dw_scale = 1.f;
@@ -370,11 +387,11 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
             const uint32_t src = tmem + buf * 256 + (quarter << 21);   // lane field: bits 16 and up
             float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
-            for (int ch = 0; ch < 8; ++ch) {
+            for (int ch = 0; ch < chunks; ++ch) {
                 uint32_t r[32];
                 tmem_ld32(src + ch * 32, r);
                 tmem_wait_ld();
-                if (ch == 7) {   // the accumulator is in registers: the next tile but one may have it
+                if (ch == chunks - 1) {   // the accumulator is in registers: the next tile but one may have it
                     fence_before_sync();
                     __syncwarp();
                     if (lane == 0) arrive_remote(leader_empty + 8 * buf);
@@ -407,12 +424,12 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 } else {
                     // 128-byte rows of the warp's buffer: 64 bf16, two chunks of 32 columns, or 32 fp32
                     const bool fp32 = MODE == kGrads && c.which == 1;
-                    const int half = fp32 ? 0 : ch & 1;
-                    if (half == 0) {   // a buffer is written again once the store before the last has read it
-                        if (lane == 0 && nstore >= 2) wait_store_read1();
+                    const int part = fp32 ? 0 : ch & 1;
+                    if (part == 0) {   // the buffer is written again once the last store has read it
+                        if (lane == 0) bulk_wait_read();
                         __syncwarp();
                     }
-                    const uint32_t buf_s = buf0 + (nstore & 1) * kStore + lane * 128;
+                    const uint32_t buf_s = buf0 + lane * 128;
                     if (fp32) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
@@ -436,14 +453,14 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 w[i] = pack_bf16(__uint_as_float(r[8 * j + 2 * i]), __uint_as_float(r[8 * j + 2 * i + 1]));
-                            st_shared16(buf_s + (((4 * half + j) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+                            st_shared16(buf_s + (((4 * part + j) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
                         }
                     }
-                    if (fp32 || half == 1) {
+                    if (fp32 || part == 1) {
                         fence_proxy_async();
                         __syncwarp();
                         if (lane == 0) {
-                            const uint32_t from = buf0 + (nstore & 1) * kStore;
+                            const uint32_t from = buf0;
                             const int x = fp32 ? c0 : c0 - 32;
                             if (MODE == kProb) {
                                 if (x < p.cols && row0 < p.N) store_2d(&maps.out[0], from, x, row0);
@@ -455,7 +472,6 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                             }
                             bulk_commit();
                         }
-                        ++nstore;
                     }
                 }
             }
@@ -473,36 +489,39 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512u) : "memory");
 }
 
-// Joins a row's (max, sum) pairs: 32 rows a block, a warp takes every eighth 256-word tile of them.
-__global__ void __launch_bounds__(256) ce_tc_join_kernel(CeParams p, int words, float *loss, float *lse_out)
+// Joins a row's (max, sum) pairs: 32 rows a block, each warp a share of the `words` pairs of each, first the largest maximum,
+// then the sums in its units.
+constexpr int kJoinWarps = 16;
+
+__global__ void __launch_bounds__(32 * kJoinWarps) ce_tc_join_kernel(const CeParams p, int words, float *loss, float *lse_out)
 {
-    __shared__ float2 sh[8][32];
+    __shared__ float tops[kJoinWarps][32], sums[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * 32 + lane;
+    wait_previous();
+    const float2 *part = p.part + (row < p.N ? row : 0);
     float top = -INFINITY, sum = 0.f;
-    if (row < p.N) {
-        for (int i = warp; i < words; i += 8) {
-            const float2 v = p.part[(int64_t)i * p.N + row];
-            const float higher = fmaxf(top, v.x);
-            const float was = isinf(top) ? 0.f : top, now = isinf(higher) ? 0.f : higher;
-            if (top != -INFINITY) sum *= expf(was - now);
-            sum += v.y * expf(v.x - now);
-            top = higher;
-        }
+#pragma unroll 8
+    for (int i = warp; i < words; i += kJoinWarps) top = fmaxf(top, part[(int64_t)i * p.N].x);
+    tops[warp][lane] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, tops[i][lane]);
+    const float base = isinf(top) ? 0.f : top;   // keeps infinities and NaN in the sum
+#pragma unroll 8
+    for (int i = warp; i < words; i += kJoinWarps) {
+        const float2 v = part[(int64_t)i * p.N];
+        sum += v.y * expf(v.x - base);
     }
-    sh[warp][lane] = make_float2(top, sum);
+    sums[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && row < p.N) {
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, sh[i][lane].x);
-        const float now = isinf(top) ? 0.f : top;
         sum = 0.f;
-        for (int i = 0; i < 8; ++i) {
-            const float2 v = sh[i][lane];
-            sum += v.x == -INFINITY ? v.y : v.y * expf(v.x - now);
-        }
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) sum += sums[i][lane];
         const int t = p.targets[row];
         const bool keep = t >= 0 && t < p.V;
-        const float lse = now + logf(sum);
+        const float lse = base + logf(sum);
         loss[row] = keep ? lse - p.at[row] : 0.f;
         if (lse_out) lse_out[row] = keep ? lse : 0.f;
     }
@@ -558,6 +577,7 @@ __global__ void __launch_bounds__(256) ce_dh_finish_kernel(const float4 *acc, ui
                                                            const float *dloss, int N, int D4, int V, int slices)
 {
     const int64_t n = (int64_t)N * D4;
+    wait_previous();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int row = (int)(i / D4), t = __ldg(targets + row);
         const float f = __ldg(dloss + row);
@@ -601,6 +621,21 @@ bool make_map(CUtensorMap *m, const void *base, int cols, int rows, int64_t pitc
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Columns of the forward's tiles.  Tiles go out in rounds of kPairs, so a few of them are made narrower where that
+// fills the last round: 255 tokens, 50257 words: 197 tiles of 256 columns make three rounds like 225 of 224, an eighth
+// longer ones.  Narrower than 128 the tile's rows of A would be read too often.
+int tile_width(int N, int V)
+{
+    const int64_t mt = ceil_div(N, kTile);
+    int best = kTile;
+    int64_t cost = INT64_MAX;
+    for (int w = kTile; w >= kTile / 2; w -= 32) {
+        const int64_t c = (mt * ceil_div(V, w) + kPairs - 1) / kPairs * w;
+        if (c * 100 < cost * 97) { cost = c; best = w; }
+    }
+    return best;
+}
+
 struct TcWorkspace {
     size_t part, at;          // forward
     // backward: E of a piece [N][piece], h dloss / s of the kept rows [N][D], dh's slices [.][N][D], s
@@ -614,7 +649,7 @@ TcWorkspace tc_layout(int N, int D, int V, bool backward)
     TcWorkspace w = {};
     size_t off = 256;
     if (!backward) {
-        w.part = off; off = align256(off + (size_t)N * ceil_div(V, kTile) * 8);
+        w.part = off; off = align256(off + (size_t)N * ceil_div(V, tile_width(N, V)) * 8);
         w.at = off;   off = align256(off + (size_t)N * 4);
     } else {
         // pieces of equal size whose E takes up to 128 MB
@@ -638,14 +673,30 @@ TcWorkspace tc_layout(int N, int D, int V, bool backward)
     return w;
 }
 
+// Launches beside the end of the stream's last kernel; the kernel itself waits for it.
+template <class Kernel, class... Args>
+cudaError_t launch_early(Kernel kernel, unsigned grid, unsigned threads, int smem, cudaStream_t st, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int MODE>
 cudaError_t launch(const CeMaps &maps, const CeParams &p, cudaStream_t st)
 {
     const cudaError_t e = cudaFuncSetAttribute(ce_tc_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int pairs = p.tiles < kPairs ? p.tiles : kPairs;
-    ce_tc_kernel<MODE><<<2 * pairs, kThreads, kSmem, st>>>(maps, p);
-    return cudaGetLastError();
+    return launch_early(ce_tc_kernel<MODE>, 2 * pairs, kThreads, kSmem, st, maps, p);
 }
 
 unsigned grid_for(int64_t items)
@@ -666,10 +717,11 @@ cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st)
     char *w = (char *)a.workspace;
     CeMaps maps;
     memset(&maps, 0, sizeof(maps));
-    if (!make_map(&maps.a[0], a.h, a.D, a.N, a.D, kHalf) || !make_map(&maps.b[0], a.w, a.D, a.V, a.D, kHalf))
-        return cudaErrorInvalidValue;
     CeParams p = {};
-    p.p[0] = {ceil_div(a.N, kTile), ceil_div(a.V, kTile), ceil_div(a.D, kDepth), 1, 0};
+    p.width = tile_width(a.N, a.V);
+    if (!make_map(&maps.a[0], a.h, a.D, a.N, a.D, kHalf) || !make_map(&maps.b[0], a.w, a.D, a.V, a.D, p.width / 2))
+        return cudaErrorInvalidValue;
+    p.p[0] = {ceil_div(a.N, kTile), ceil_div(a.V, p.width), ceil_div(a.D, kDepth), 1, 0};
     p.tiles0 = p.tiles = p.p[0].mt * p.p[0].nt;
     p.N = a.N; p.V = a.V; p.D = a.D; p.cols = a.V;
     p.targets = a.targets;
@@ -679,8 +731,7 @@ cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st)
     p.clear_err = 1;
     const cudaError_t e = launch<kLogits>(maps, p, st);
     if (e != cudaSuccess) return e;
-    ce_tc_join_kernel<<<ceil_div(a.N, 32), 256, 0, st>>>(p, p.p[0].nt, a.loss, a.lse);
-    return cudaGetLastError();
+    return launch_early(ce_tc_join_kernel, ceil_div(a.N, 32), 32 * kJoinWarps, 0, st, p, p.p[0].nt, a.loss, a.lse);
 }
 
 cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st)
@@ -689,6 +740,7 @@ cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st)
     char *w = (char *)a.workspace;
     const int mt = ceil_div(a.N, kTile), dt = ceil_div(a.D, kTile);
     CeParams p = {};
+    p.width = kTile;
     p.N = a.N; p.V = a.V; p.D = a.D;
     p.targets = a.targets; p.lse_in = a.lse_in;
     p.scale = (float *)(w + ws.scale);
@@ -729,10 +781,9 @@ cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st)
         e = launch<kGrads>(md, p, st);
         if (e != cudaSuccess) return e;
     }
-    if (a.dh)
-        ce_dh_finish_kernel<<<grid_for((int64_t)a.N * a.D / 4), 256, 0, st>>>(
-            (const float4 *)(w + ws.acc), (uint2 *)a.dh, a.targets, a.dloss, a.N, a.D / 4, a.V, ws.slices);
-    return cudaGetLastError();
+    if (!a.dh) return cudaSuccess;
+    return launch_early(ce_dh_finish_kernel, grid_for((int64_t)a.N * a.D / 4), 256, 0, st, (const float4 *)(w + ws.acc),
+                        (uint2 *)a.dh, a.targets, a.dloss, a.N, a.D / 4, a.V, ws.slices);
 }
 
 }  // namespace gdn
