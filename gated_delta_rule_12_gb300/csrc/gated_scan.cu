@@ -229,40 +229,48 @@ struct Exchange {
     }
 };
 
-// ROWS rows of 8 L bytes into a warp's slot; row i at src + i * step elements, rows from `rows` on and channels behind
-// D as zeros.  CW: bytes that a copy may move at once, by the alignment of the rows; 2 (a row of an odd number of bf16)
-// has no asynchronous copy and goes through registers.
-template <typename T, int L, int ROWS, int CW>
+// A warp's slot: its rows of 8 L bytes, R of a group together, and after each group of short rows another 8 L bytes, so
+// that the groups, which read one row each, find theirs in different banks (without it the backward pass of
+// 1 x 4999 x 1001 waits on shared memory more than on anything else).
+template <int L, int R>
+struct Slot {
+    static constexpr int kPad = L < 16 ? 8 * L : 0;
+    static constexpr int kGroup = R * 8 * L + kPad;
+    static constexpr int kBytes = kGroup * (32 / L);
+    // row r0 + down * i, where down is a power of two and r0 < down
+    template <int DOWN>
+    static __device__ __forceinline__ uint32_t at(int r0, int i)
+    {
+        const int group = DOWN >= R ? r0 / R + i * (DOWN / R) : i * DOWN / R;
+        return (r0 + DOWN * i) * (8 * L) + group * kPad;
+    }
+};
+
+// A warp's 32 / L groups of R rows into its slot; row i at src + i * step elements, rows from `rows` on and channels
+// behind D as zeros.  CW: bytes that a copy may move at once, by the alignment of the rows; 2 (a row of an odd number
+// of bf16) has no asynchronous copy and goes through registers.
+template <typename T, int L, int R, int CW>
 __device__ __forceinline__ void fetch(uint32_t slot, const T *src, int step, int rows, int channels)
 {
-    const int lane = threadIdx.x & 31;
-    if constexpr (CW == 16) {
-        constexpr int across = L / 2, down = 32 / across;   // copies a row; rows a step
-        const int col = (lane % across) * (16 / (int)sizeof(T)), r0 = lane / across;
+    constexpr int ROWS = R * 32 / L;
+    constexpr int across = CW == 16 ? L / 2 : L * 2, down = 32 / across;   // copies a row; rows a step
+    const int lane = threadIdx.x & 31, col = (lane % across) * ((CW == 16 ? 16 : 4) / (int)sizeof(T)), r0 = lane / across;
+    const uint32_t to = slot + (lane % across) * (CW == 16 ? 16 : 4);
+    if constexpr (CW >= 4) {
         const T *p = src + ((int64_t)step * r0 + col);
         const bool live = col < channels;
 #pragma unroll
         for (int i = 0; i < ROWS / down; ++i) {
             const bool in = live && r0 + down * i < rows;
-            asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;"
-                         :: "r"(slot + lane * 16 + i * 512), "l"(in ? p + (int64_t)step * (down * i) : src),
-                            "r"(in ? 16 : 0) : "memory");
-        }
-    } else if constexpr (CW == 4) {
-        constexpr int across = L * 2 < 32 ? L * 2 : 32, down = 32 / across, per = 4 / sizeof(T);
-        const int col = (lane % across) * per, r0 = lane / across;
-        const T *p = src + ((int64_t)step * r0 + col);
-        const bool live = col < channels;
-#pragma unroll
-        for (int i = 0; i < ROWS / down; ++i) {
-            const bool in = live && r0 + down * i < rows;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
-                         :: "r"(slot + lane * 4 + i * 128), "l"(in ? p + (int64_t)step * (down * i) : src),
-                            "r"(in ? 4 : 0) : "memory");
+            const T *from = p + (int64_t)step * (down * i);   // read if `in`
+            if constexpr (CW == 16)
+                asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;"
+                             :: "r"(to + Slot<L, R>::template at<down>(r0, i)), "l"(from), "r"(in ? 16 : 0) : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                             :: "r"(to + Slot<L, R>::template at<down>(r0, i)), "l"(from), "r"(in ? 4 : 0) : "memory");
         }
     } else {
-        constexpr int across = L * 2 < 32 ? L * 2 : 32, down = 32 / across;
-        const int col = (lane % across) * 2, r0 = lane / across;
         uint32_t w[ROWS / down];
 #pragma unroll
         for (int i = 0; i < ROWS / down; ++i) {
@@ -273,7 +281,7 @@ __device__ __forceinline__ void fetch(uint32_t slot, const T *src, int step, int
         }
 #pragma unroll
         for (int i = 0; i < ROWS / down; ++i)
-            asm volatile("st.shared.b32 [%0], %1;" :: "r"(slot + lane * 4 + i * 128), "r"(w[i]) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" :: "r"(to + Slot<L, R>::template at<down>(r0, i)), "r"(w[i]) : "memory");
     }
 }
 
@@ -307,6 +315,19 @@ __device__ __forceinline__ uint2 words(uint32_t at)
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
+// The k-th longest of up to 32 packed sequences (the first of equals): the long ones start first.
+__device__ __forceinline__ int by_length(const GatedScanArgs &a, int k)
+{
+    const int lane = threadIdx.x & 31;
+    const int len = lane < a.N ? __ldg(a.cu + lane + 1) - __ldg(a.cu + lane) : -1;
+    int longer = 0;
+    for (int i = 0; i < a.N; ++i) {
+        const int other = __shfl_sync(0xffffffffu, len, i);
+        longer += other > len || (other == len && i < lane);
+    }
+    return __ffs(__ballot_sync(0xffffffffu, lane < a.N && longer == k)) - 1;
+}
+
 // What a CTA works on: one sequence (with the cluster's other CTAs, along time) and one block of L kVec channels.
 template <typename T, int L>
 struct Work {
@@ -317,6 +338,7 @@ struct Work {
         rank = blockIdx.x % csize;
         const int unit = blockIdx.x / csize;
         n = unit / nblocks;
+        if (a.cu && a.N <= 32) n = by_length(a, n);
         ch0 = (unit % nblocks) * (L * kVec<T>);
         channels = min(a.D - ch0, (L * kVec<T>));
         mine = channels - (threadIdx.x & (L - 1)) * kVec<T>;
@@ -347,22 +369,33 @@ __device__ __forceinline__ int rows_left(int64_t from, int len, int most)
     return (int)max((int64_t)0, min((int64_t)most, len - from));
 }
 
-// -expm1(g) on a pair
-__device__ __forceinline__ Pair gate_of(Pair g)
+// 1 - exp(g), given a = exp(g): the series of exp(g) - 1 where |g| <= 1/2 and the difference would lose bits (the next
+// term is under 2^-26 of the sum), else the difference.
+__device__ __forceinline__ Pair gate_of(Pair g, Pair a)
 {
-    float a, b;
-    split(g, a, b);
-    return pair(-expm1f(a), -expm1f(b));
+    Pair s = both(1.f / 40320.f);
+    s = fma2(s, g, both(1.f / 5040.f));
+    s = fma2(s, g, both(1.f / 720.f));
+    s = fma2(s, g, both(1.f / 120.f));
+    s = fma2(s, g, both(1.f / 24.f));
+    s = fma2(s, g, both(1.f / 6.f));
+    s = fma2(s, g, both(0.5f));
+    s = fma2(s, g, both(1.f));
+    float g0, g1, a0, a1, s0, s1;
+    split(g, g0, g1);
+    split(a, a0, a1);
+    split(mul2(s, g), s0, s1);
+    return pair(fabsf(g0) <= 0.5f ? -s0 : 1.f - a0, fabsf(g1) <= 0.5f ? -s1 : 1.f - a1);
 }
 
 // An iteration takes csize * nwarps * R * 32 / L rows.  Rows pass through a ring of each warp's own slots by asynchronous
 // copies, so only the joins need barriers.  A group scans its R rows from 0 (S and H), the joined carry comes in,
 // and the rows are run again from it out of registers: memory is read once and written once.
 template <typename T, bool GATE, int CW, int L, int R, int STAGES, int WARPS, bool CLUSTER>
-__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), WARPS > 8 ? 1 : 2)
+__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), 16 / WARPS)
 scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 {
-    constexpr int NP = kPairs<T>, ROWS = R * 32 / L, SLOT = R * 256;
+    constexpr int NP = kPairs<T>, ROWS = R * 32 / L, SLOT = Slot<L, R>::kBytes;
     extern __shared__ __align__(128) unsigned char smem[];
     const int warp = threadIdx.x >> 5, nwarps = (blockDim.x >> 5) - (CLUSTER ? 1 : 0);
     const Work<T, L> w(a, nblocks, csize);
@@ -379,7 +412,7 @@ scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 
     const uint32_t slots = shared_addr(smem) + warp * STAGES * 2 * SLOT;
     const int group = (threadIdx.x & 31) / L;
-    const uint32_t own = group * R * L * 8 + (threadIdx.x & (L - 1)) * 8;
+    const uint32_t own = group * Slot<L, R>::kGroup + (threadIdx.x & (L - 1)) * 8;
     const int64_t base = w.tok0 * a.D + w.ch0;
     Pair carry[NP];
     w.get(a.init_state, a, carry);
@@ -387,8 +420,8 @@ scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
     auto load = [&](int64_t t, int st) {
         const int rows = rows_left(t, w.len, ROWS);
         const int64_t at = base + (rows > 0 ? t * a.D : 0);
-        fetch<T, L, ROWS, CW>(slots + st * 2 * SLOT, (const T *)a.g + at, a.D, rows, w.channels);
-        fetch<T, L, ROWS, CW>(slots + (st * 2 + 1) * SLOT, (const T *)a.x + at, a.D, rows, w.channels);
+        fetch<T, L, R, CW>(slots + st * 2 * SLOT, (const T *)a.g + at, a.D, rows, w.channels);
+        fetch<T, L, R, CW>(slots + (st * 2 + 1) * SLOT, (const T *)a.x + at, a.D, rows, w.channels);
     };
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
@@ -409,8 +442,9 @@ scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 #pragma unroll
             for (int v = 0; v < NP; ++v) {
                 sum[v] = add2(sum[v], al[i][v]);
-                if (GATE) u[i][v] = mul2(u[i][v], gate_of(al[i][v]));
-                al[i][v] = decay<T>(al[i][v]);
+                const Pair g = al[i][v];
+                al[i][v] = decay<T>(g);
+                if (GATE) u[i][v] = mul2(u[i][v], gate_of(g, al[i][v]));
                 h[v] = fma2(al[i][v], h[v], u[i][v]);
             }
         }
@@ -434,10 +468,10 @@ scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 
 // The same from the end: row i of a warp's slot is token len - 1 - (r0 + i), its h the one before.
 template <typename T, bool GATE, int CW, int L, int R, int STAGES, int WARPS, bool CLUSTER>
-__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), WARPS > 8 ? 1 : 2)
+__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), 16 / WARPS)
 scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 {
-    constexpr int NP = kPairs<T>, NT = GATE ? 4 : 3, ROWS = R * 32 / L, SLOT = R * 256;
+    constexpr int NP = kPairs<T>, NT = GATE ? 4 : 3, ROWS = R * 32 / L, SLOT = Slot<L, R>::kBytes;
     extern __shared__ __align__(128) unsigned char smem[];
     const int warp = threadIdx.x >> 5, nwarps = (blockDim.x >> 5) - (CLUSTER ? 1 : 0);
     const Work<T, L> w(a, nblocks, csize);
@@ -454,7 +488,7 @@ scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 
     const uint32_t slots = shared_addr(smem) + warp * STAGES * NT * SLOT;
     const int group = (threadIdx.x & 31) / L;
-    const uint32_t own = group * R * L * 8 + (threadIdx.x & (L - 1)) * 8;
+    const uint32_t own = group * Slot<L, R>::kGroup + (threadIdx.x & (L - 1)) * 8;
     const int64_t last = (w.tok0 + w.len - 1) * a.D + w.ch0;
     Pair carry[NP];
     w.get(a.dfinal, a, carry);
@@ -463,10 +497,10 @@ scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
         const int rows = rows_left(r, w.len, ROWS), before = rows_left(r, w.len - 1, ROWS);   // the first token has none
         const int64_t at = rows > 0 ? last - r * a.D : 0;
         const uint32_t s = slots + st * NT * SLOT;
-        fetch<T, L, ROWS, CW>(s, (const T *)a.g + at, -a.D, rows, w.channels);
-        fetch<T, L, ROWS, CW>(s + SLOT, (const T *)a.dout + at, -a.D, rows, w.channels);
-        fetch<T, L, ROWS, CW>(s + 2 * SLOT, (const T *)a.h + (before > 0 ? at - a.D : 0), -a.D, before, w.channels);
-        if (GATE) fetch<T, L, ROWS, CW>(s + 3 * SLOT, (const T *)a.x + at, -a.D, rows, w.channels);
+        fetch<T, L, R, CW>(s, (const T *)a.g + at, -a.D, rows, w.channels);
+        fetch<T, L, R, CW>(s + SLOT, (const T *)a.dout + at, -a.D, rows, w.channels);
+        fetch<T, L, R, CW>(s + 2 * SLOT, (const T *)a.h + (before > 0 ? at - a.D : 0), -a.D, before, w.channels);
+        if (GATE) fetch<T, L, R, CW>(s + 3 * SLOT, (const T *)a.x + at, -a.D, rows, w.channels);
     };
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
@@ -509,7 +543,7 @@ scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
             for (int v = 0; v < NP; ++v) {
                 const Pair dh = add2(d[i][v], e[v]);
                 e[v] = mul2(al[i][v], dh);
-                vx[v] = GATE ? mul2(gate_of(g[v]), dh) : dh;
+                vx[v] = GATE ? mul2(gate_of(g[v], al[i][v]), dh) : dh;
                 vg[v] = mul2(e[v], GATE ? fma2(x[v], pair(-1.f, -1.f), prev[v]) : prev[v]);
             }
             if (i < rows) {
@@ -597,8 +631,9 @@ Cut cut(const GatedScanArgs &a, int vec, int R)
 }
 
 template <typename T, int L, int R, class Kernel>
-cudaError_t launch(Kernel kernel, const GatedScanArgs &a, int slot_bytes, Cut c, cudaStream_t st)
+cudaError_t launch(Kernel kernel, const GatedScanArgs &a, int slots, Cut c, cudaStream_t st)
 {
+    const int slot_bytes = slots * Slot<L, R>::kBytes;   // of a warp
     const int nblocks = ceil_div(a.D, L * kVec<T>);
     const int64_t units = (int64_t)a.N * nblocks;
     const int most = ceil_div(a.T > 0 ? a.T : 1, R * 32 / L);
@@ -635,25 +670,25 @@ int copy_width(const GatedScanArgs &a)
 template <typename T, bool GATE, int CW>
 cudaError_t fwd_cw(const GatedScanArgs &a, cudaStream_t st)
 {
-    constexpr int R = 8, S = 2, SLOTS = S * 2 * R * 256;
+    constexpr int R = 8, S = 2, TENSORS = 2;
     const Cut c = cut(a, kVec<T>, R);
-    if (c.csize > 1) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 15, true>, a, SLOTS, c, st);
-    if (c.warps > 8) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 16, false>, a, SLOTS, c, st);
-    if (c.lanes == 4) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 8, false>, a, SLOTS, c, st);
-    if (c.lanes == 8) return launch<T, 8, R>(scan_fwd_kernel<T, GATE, CW, 8, R, S, 8, false>, a, SLOTS, c, st);
-    return launch<T, 16, R>(scan_fwd_kernel<T, GATE, CW, 16, R, S, 8, false>, a, SLOTS, c, st);
+    if (c.csize > 1) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 15, true>, a, S * TENSORS, c, st);
+    if (c.warps > 8) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 16, false>, a, S * TENSORS, c, st);
+    if (c.lanes == 4) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 8, false>, a, S * TENSORS, c, st);
+    if (c.lanes == 8) return launch<T, 8, R>(scan_fwd_kernel<T, GATE, CW, 8, R, S, 8, false>, a, S * TENSORS, c, st);
+    return launch<T, 16, R>(scan_fwd_kernel<T, GATE, CW, 16, R, S, 8, false>, a, S * TENSORS, c, st);
 }
 
 template <typename T, bool GATE, int CW>
 cudaError_t bwd_cw(const GatedScanArgs &a, cudaStream_t st)
 {
-    constexpr int R = GATE ? 4 : 8, S = 2, SLOTS = S * (GATE ? 4 : 3) * R * 256;
+    constexpr int R = GATE ? 4 : 8, S = 2, TENSORS = GATE ? 4 : 3;
     const Cut c = cut(a, kVec<T>, R);
-    if (c.csize > 1) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 15, true>, a, SLOTS, c, st);
-    if (c.warps > 8) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 16, false>, a, SLOTS, c, st);
-    if (c.lanes == 4) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 8, false>, a, SLOTS, c, st);
-    if (c.lanes == 8) return launch<T, 8, R>(scan_bwd_kernel<T, GATE, CW, 8, R, S, 8, false>, a, SLOTS, c, st);
-    return launch<T, 16, R>(scan_bwd_kernel<T, GATE, CW, 16, R, S, 8, false>, a, SLOTS, c, st);
+    if (c.csize > 1) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 15, true>, a, S * TENSORS, c, st);
+    if (c.warps > 8) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 16, false>, a, S * TENSORS, c, st);
+    if (c.lanes == 4) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 8, false>, a, S * TENSORS, c, st);
+    if (c.lanes == 8) return launch<T, 8, R>(scan_bwd_kernel<T, GATE, CW, 8, R, S, 8, false>, a, S * TENSORS, c, st);
+    return launch<T, 16, R>(scan_bwd_kernel<T, GATE, CW, 16, R, S, 8, false>, a, S * TENSORS, c, st);
 }
 
 template <typename T, bool GATE>

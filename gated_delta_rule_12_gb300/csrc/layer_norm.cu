@@ -124,8 +124,6 @@ __device__ __forceinline__ float total(Pair p)
     return a + b;
 }
 
-__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
-
 // Sums of N values over a team, the same bits in every thread of it: shuffles within a warp, then, for teams of
 // several warps, their sums in order through `sh` behind a barrier of the team's own.
 template <int TEAM, int N>

@@ -34,4 +34,6 @@ __device__ __forceinline__ Pair mul2(Pair a, Pair b)
     return r;
 }
 
+__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
+
 }  // namespace gdn
