@@ -425,49 +425,45 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _stream_of(t, stream):
-    if stream is None:
-        return _raw_stream(t.get_device())
-    return getattr(stream, "cuda_stream", stream)
+    return _raw_stream(t.get_device()) if stream is None else getattr(stream, "cuda_stream", stream)
 
 
 def _made_here(stream, *ts):
     """Tensors that a wrapper allocated (from the current stream's memory) are used by a kernel on ``stream``: the
     allocator keeps them until that work is done."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream)
-        for t in ts:
-            if t is not None:
-                t.record_stream(stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream)
+    for t in ts:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _check_scan_args(x, g, cu_seqlens, dtype, states, same):
     """Shapes, dtypes, placement and contiguity of a gated-scan call; returns (B, T, D, N).  ``states`` are the
     [N,D] fp32 tensors, ``same`` further tensors that must match g."""
-    if g.dim() != 3:
+    shape = g.shape
+    if len(shape) != 3:
         raise ValueError("x and g must be [B,T,D]")
-    B, T, D = g.shape
+    B, T, D = shape
     N = B
     if cu_seqlens is not None:
-        if cu_seqlens.dtype != torch.int32:
+        if cu_seqlens.dtype is not torch.int32:
             raise TypeError("cu_seqlens must be int32")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or B != 1:
             raise ValueError("cu_seqlens must be [N+1] with N >= 1, and B = 1")
         N = cu_seqlens.numel() - 1
     for t in (x, g, *same):
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError("x, g and the other token tensors must share one dtype")
-        if t.shape != g.shape:
-            raise ValueError("x, g and the other token tensors must share one shape")
+        if t is not None:
+            if t.dtype is not dtype:
+                raise TypeError("x, g and the other token tensors must share one dtype")
+            if t.shape != shape:
+                raise ValueError("x, g and the other token tensors must share one shape")
     for t in states:
-        if t is None:
-            continue
-        if t.dtype != _F32:
-            raise TypeError("states must be float32")
-        if tuple(t.shape) != (N, D):
-            raise ValueError(f"states must be [N,D] = {(N, D)}")
+        if t is not None:
+            if t.dtype is not _F32:
+                raise TypeError("states must be float32")
+            if t.shape != (N, D):
+                raise ValueError(f"states must be [N,D] = {(N, D)}")
     _need_cuda(x, g, cu_seqlens, *states, *same)
     return B, T, D, N
 
@@ -481,7 +477,8 @@ def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, input_gate=False, out
     None.  Returns ``(out, final_state)``; final_state is None if not requested.
     """
     lib = _lib or load_library()
-    B, T, D, N = _check_scan_args(x, g, cu_seqlens, x.dtype, (init_state, final_state), (x, out))
+    B, T, D, N = _check_scan_args(x, g, cu_seqlens, x.dtype, (init_state, final_state), (out,))
+    made = (None if out is not None else 1, None if final_state is not None else 1)
     if out is None:
         out = _empty_like(x)
     if final_state is None and output_final_state:
@@ -491,7 +488,8 @@ def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, input_gate=False, out
                                 _dt(x), int(bool(input_gate)), _stream_of(g, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_gated_scan_fwd")
-    _made_here(stream, out, final_state)
+    if stream is not None:
+        _made_here(stream, made[0] and out, made[1] and final_state)
     return out, final_state
 
 
@@ -512,54 +510,65 @@ def gated_scan_bwd(x, g, out, dout, init_state=None, dfinal_state=None, cu_seqle
                                 _stream_of(g, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_gated_scan_bwd")
-    _made_here(stream, dx, dg, dinit)
+    if stream is not None:
+        _made_here(stream, dx, dg, dinit)
     return dx, dg, dinit
+
+
+def _sound(t, dtype):
+    """What a kernel takes: the dtype, on the GPU, contiguous."""
+    return t.dtype is dtype and t.is_cuda and t.is_contiguous()
 
 
 def gated_scan_step(state, x, g, input_gate=False, out=None, stream=None):
     """One token of the gated scan per sequence (``gdn_gated_scan_step``); ``state`` [N,D] fp32 is updated in
     place.  x, g [N,D] (fp32 or bf16).  Returns out [N,D]."""
     lib = _lib or load_library()
-    if state.dim() != 2 or x.shape != state.shape or g.shape != state.shape or (out is not None and
-                                                                                out.shape != state.shape):
+    shape, dtype = state.shape, x.dtype
+    if len(shape) != 2 or x.shape != shape or g.shape != shape or (out is not None and out.shape != shape):
         raise ValueError("gated_scan_step: state, x, g and out must be [N,D]")
-    if state.dtype != _F32:
+    if state.dtype is not _F32:
         raise TypeError("state must be float32")
-    if out is None:
-        out = _empty_like(x)
-    if g.dtype != x.dtype or out.dtype != x.dtype:
+    made = out is None
+    if g.dtype is not dtype or (not made and out.dtype is not dtype):
         raise TypeError("x, g and out must share one dtype")
     _need_cuda(state, x, g, out)
-    N, D = state.shape
+    if made:
+        out = _empty_like(x)
+    N, D = shape
     rc = lib.gdn_gated_scan_step(state.data_ptr(), x.data_ptr(), g.data_ptr(), out.data_ptr(), N, D, _dt(x),
-                                 int(bool(input_gate)), _stream_of(g, stream))
+                                 1 if input_gate else 0, _stream_of(x, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_gated_scan_step")
-    _made_here(stream, out)
+    if stream is not None and made:
+        _made_here(stream, out)
     return out
 
 
 def _check_norm_args(x, params, stats, same):
     """Shapes, dtypes, placement and contiguity of a layer-norm call; returns (rows, D)."""
-    if x.dim() < 1 or x.shape[-1] < 1:
+    shape = x.shape
+    if not shape or shape[-1] < 1:
         raise ValueError("x must be [..., D] with D >= 1")
-    D = x.shape[-1]
+    D = shape[-1]
     rows = x.numel() // D
     for t in params:
-        if t is not None and t.dtype != _F32:
-            raise TypeError("weight and bias must be float32")
-        if t is not None and (t.dim() != 1 or t.numel() != D):
-            raise ValueError("weight and bias must be [D]")
+        if t is not None:
+            if t.dtype is not _F32:
+                raise TypeError("weight and bias must be float32")
+            if t.shape != (D,):
+                raise ValueError("weight and bias must be [D]")
     for t in stats:
-        if t.dtype != _F32:
+        if t.dtype is not _F32:
             raise TypeError("mean and rstd must be float32")
         if t.numel() != rows:
             raise ValueError("mean and rstd must hold one value a row")
     for t in same:
-        if t is not None and t.dtype != x.dtype:
-            raise TypeError("x and the other row tensors must share one dtype")
-        if t is not None and t.shape != x.shape:
-            raise ValueError("x and the other row tensors must share one shape")
+        if t is not None:
+            if t.dtype is not x.dtype:
+                raise TypeError("x and the other row tensors must share one dtype")
+            if t.shape != shape:
+                raise ValueError("x and the other row tensors must share one shape")
     _need_cuda(x, *params, *stats, *same)
     return rows, D
 
@@ -568,17 +577,28 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     """Layer norm over the last axis (``gdn_layer_norm_fwd``).  x [..., D] (fp32 or bf16); weight, bias [D] fp32 or
     None.  Returns ``(out, mean, rstd)``, the statistics fp32 of shape ``x.shape[:-1]``."""
     lib = _lib or load_library()
-    rows, D = _check_norm_args(x, (weight, bias), (), (out,))
+    # everything in order takes the short way; the long one says what is not
+    shape = x.shape
+    D = shape[-1] if shape else 0
+    if D > 0 and out is None and x.is_cuda and x.is_contiguous() and \
+            (weight is None or (_sound(weight, _F32) and weight.shape == (D,))) and \
+            (bias is None or (_sound(bias, _F32) and bias.shape == (D,))):
+        rows = x.numel() // D
+    else:
+        rows, D = _check_norm_args(x, (weight, bias), (), (out,))
     dt = _dt(x)
-    if out is None:
+    made = out is None
+    if made:
         out = _empty_like(x)
-    mean = _empty(x.shape[:-1], dtype=_F32, device=x.device)
+    mean = _empty(shape[:-1], dtype=_F32, device=x.device)
     rstd = _empty_like(mean)
-    rc = lib.gdn_layer_norm_fwd(x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), mean.data_ptr(),
-                                rstd.data_ptr(), rows, D, dt, float(eps), _stream_of(x, stream))
+    rc = lib.gdn_layer_norm_fwd(x.data_ptr(), None if weight is None else weight.data_ptr(),
+                                None if bias is None else bias.data_ptr(), out.data_ptr(), mean.data_ptr(),
+                                rstd.data_ptr(), rows, D, dt, eps, _stream_of(x, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_layer_norm_fwd")
-    _made_here(stream, out, mean, rstd)
+    if stream is not None:
+        _made_here(stream, out if made else None, mean, rstd)
     return out, mean, rstd
 
 
@@ -587,44 +607,56 @@ def layer_norm_bwd_workspace_size(rows, D, dtype=torch.bfloat16) -> int:
     return int(load_library().gdn_layer_norm_bwd_workspace_size(rows, D, dt))
 
 
+def _workspace(given, need, device):
+    """The caller's workspace and its size, or one of the size needed."""
+    if given is None:
+        need = max(256, need)
+        return _empty(need, dtype=torch.uint8, device=device), need
+    _need_cuda(given)
+    return given, given.numel() * given.element_size()
+
+
 def layer_norm_bwd(dout, x, mean, rstd, weight=None, workspace=None, stream=None):
     """Backward of ``layer_norm_fwd`` (``gdn_layer_norm_bwd``): returns ``(dx, dweight, dbias)``, the last two [D]
     fp32.  ``mean`` and ``rstd`` are the forward's."""
     lib = _lib or load_library()
     rows, D = _check_norm_args(x, (weight,), (mean, rstd), (dout,))
     dt = _dt(x)
+    device = x.device
     dx = _empty_like(x)
-    dw = _empty(D, dtype=_F32, device=x.device)
+    dw = _empty(D, dtype=_F32, device=device)
     db = _empty_like(dw)
-    if workspace is None:
-        workspace = _empty(max(256, lib.gdn_layer_norm_bwd_workspace_size(rows, D, dt)), dtype=torch.uint8,
-                                device=x.device)
-    _need_cuda(workspace)
+    ws, size = _workspace(workspace, 0 if workspace is not None else
+                          lib.gdn_layer_norm_bwd_workspace_size(rows, D, dt), device)
     rc = lib.gdn_layer_norm_bwd(dout.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
-                                dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, D, dt, workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream_of(x, stream))
+                                dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, D, dt, ws.data_ptr(), size,
+                                _stream_of(x, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_layer_norm_bwd")
-    _made_here(stream, dx, dw, db, workspace)
+    if stream is not None:
+        _made_here(stream, dx, dw, db, ws if workspace is None else None)
     return dx, dw, db
 
 
 def _check_ce_args(h, weight, targets, rows):
-    if h.dim() != 2 or weight.dim() != 2 or h.shape[1] != weight.shape[1]:
+    """Shapes, dtypes, placement and contiguity of a cross-entropy call; returns (N, D, V)."""
+    hs, ws = h.shape, weight.shape
+    if len(hs) != 2 or len(ws) != 2 or hs[1] != ws[1]:
         raise ValueError("h must be [N,D] and weight [V,D]")
-    if weight.dtype != h.dtype:
+    if weight.dtype is not h.dtype:
         raise TypeError("h and weight must share one dtype")
-    if targets.dtype != torch.int32:
+    if targets.dtype is not torch.int32:
         raise TypeError("targets must be int32")
-    if tuple(targets.shape) != (h.shape[0],):
+    N = hs[0]
+    if targets.shape != (N,):
         raise ValueError("targets must be [N]")
     for t in rows:
-        if t.dtype != _F32:
+        if t.dtype is not _F32:
             raise TypeError("lse and dloss must be float32")
-        if tuple(t.shape) != (h.shape[0],):
+        if t.shape != (N,):
             raise ValueError("lse and dloss must be [N]")
     _need_cuda(h, weight, targets, *rows)
-    return h.shape[0], h.shape[1], weight.shape[0]
+    return N, hs[1], ws[0]
 
 
 def linear_cross_entropy_workspace_size(N, D, V, dtype=torch.bfloat16, backward=False) -> int:
@@ -642,18 +674,17 @@ def linear_cross_entropy_fwd(h, weight, targets, workspace=None, stream=None):
     lib = _lib or load_library()
     N, D, V = _check_ce_args(h, weight, targets, ())
     dt = _dt(h)
-    loss = _empty(N, dtype=_F32, device=h.device)
+    device = h.device
+    loss = _empty(N, dtype=_F32, device=device)
     lse = _empty_like(loss)
-    if workspace is None:
-        workspace = _empty(max(256, lib.gdn_linear_cross_entropy_workspace_size(N, D, V, dt, 0)),
-                                dtype=torch.uint8, device=h.device)
-    _need_cuda(workspace)
+    ws, size = _workspace(workspace, 0 if workspace is not None else
+                          lib.gdn_linear_cross_entropy_workspace_size(N, D, V, dt, 0), device)
     rc = lib.gdn_linear_cross_entropy_fwd(h.data_ptr(), weight.data_ptr(), targets.data_ptr(), loss.data_ptr(),
-                                          lse.data_ptr(), N, D, V, dt, workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(), _stream_of(h, stream))
+                                          lse.data_ptr(), N, D, V, dt, ws.data_ptr(), size, _stream_of(h, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_linear_cross_entropy_fwd")
-    _made_here(stream, loss, lse, workspace)
+    if stream is not None:
+        _made_here(stream, loss, lse, ws if workspace is None else None)
     return loss, lse
 
 
@@ -664,17 +695,15 @@ def linear_cross_entropy_bwd(h, weight, targets, lse, dloss, workspace=None, str
     N, D, V = _check_ce_args(h, weight, targets, (lse, dloss))
     dt = _dt(h)
     dh, dw = _empty_like(h), _empty_like(weight)
-    if workspace is None:
-        workspace = _empty(max(256, lib.gdn_linear_cross_entropy_workspace_size(N, D, V, dt, 1)),
-                                dtype=torch.uint8, device=h.device)
-    _need_cuda(workspace)
+    ws, size = _workspace(workspace, 0 if workspace is not None else
+                          lib.gdn_linear_cross_entropy_workspace_size(N, D, V, dt, 1), h.device)
     rc = lib.gdn_linear_cross_entropy_bwd(h.data_ptr(), weight.data_ptr(), targets.data_ptr(), lse.data_ptr(),
-                                          dloss.data_ptr(), dh.data_ptr(), dw.data_ptr(), N, D, V, dt,
-                                          workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                          _stream_of(h, stream))
+                                          dloss.data_ptr(), dh.data_ptr(), dw.data_ptr(), N, D, V, dt, ws.data_ptr(),
+                                          size, _stream_of(h, stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_linear_cross_entropy_bwd")
-    _made_here(stream, dh, dw, workspace)
+    if stream is not None:
+        _made_here(stream, dh, dw, ws if workspace is None else None)
     return dh, dw
 
 

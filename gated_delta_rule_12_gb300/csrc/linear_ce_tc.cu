@@ -71,8 +71,9 @@ struct CeParams {
     int N, V, D;
     int v0, cols;             // the piece (kProb), the whole vocabulary (kLogits)
     int accumulate;           // kGrads: dh adds to the earlier pieces' sums
+    int direct;               // kGrads: the only piece, dh in one slice: its tiles are the result
     const int32_t *targets;
-    const float *lse_in;
+    const float *lse_in, *dloss;
     const float *scale;       // kGrads: s
     float2 *part;             // kLogits: [tiles of `width` words][N]
     float *at;                // kLogits: [N]
@@ -375,13 +376,15 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
             const int col0 = c.n * width;
             const bool in = row < p.N;
             int target = -1;
-            float lse = 0.f, dw_scale = 1.f;
-            if (MODE != kGrads && in) {
+            float lse = 0.f, scale = 1.f;
+            const bool direct = MODE == kGrads && c.which == 1 && p.direct;
+            if ((MODE != kGrads || direct) && in) {
                 target = __ldg(p.targets + row);
                 if (MODE == kProb) lse = __ldg(p.lse_in + row);
+                if (direct) scale = __ldg(p.dloss + row);
             }
-            if (MODE == kGrads && c.which == 0) dw_scale = __ldg(p.scale);
-            const bool keep = target >= 0 && target < p.V;
+            if (MODE == kGrads && c.which == 0) scale = __ldg(p.scale);
+            const bool keep = (MODE == kGrads && !direct) || (target >= 0 && target < p.V);
             if (!__all_sync(0xffffffffu, wait_bar(acc_full + 8 * buf, use & 1, abort_flag, p.err))) break;
             fence_after_sync();
             const uint32_t src = tmem + buf * 256 + (quarter << 21);   // lane field: bits 16 and up
@@ -423,7 +426,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                     sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
                 } else {
                     // 128-byte rows of the warp's buffer: 64 bf16, two chunks of 32 columns, or 32 fp32
-                    const bool fp32 = MODE == kGrads && c.which == 1;
+                    const bool fp32 = MODE == kGrads && c.which == 1 && !direct;
                     const int part = fp32 ? 0 : ch & 1;
                     if (part == 0) {   // the buffer is written again once the last store has read it
                         if (lane == 0) bulk_wait_read();
@@ -445,7 +448,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                             }
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * dw_scale);
+                            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(keep ? __uint_as_float(r[j]) * scale : 0.f);
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -467,7 +470,8 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                             } else if (c.which == 0) {
                                 if (x < p.D && row0 < p.cols) store_2d(&maps.out[0], from, x, p.v0 + row0);
                             } else if (x < p.D && row0 < p.N) {
-                                if (p.accumulate) add_3d(&maps.out[1], from, x, row0, c.s);
+                                if (direct) store_2d(&maps.out[1], from, x, row0);
+                                else if (p.accumulate) add_3d(&maps.out[1], from, x, row0, c.s);
                                 else store_3d(&maps.out[1], from, x, row0, c.s);
                             }
                             bulk_commit();
@@ -527,26 +531,29 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_tc_join_kernel(const CePar
     }
 }
 
-// s = max |dloss| over the kept rows, finite, and 1 where that is 0.
-__global__ void __launch_bounds__(1024) ce_scale_kernel(const float *dloss, const int32_t *targets, int N, int V,
-                                                        float *scale)
+// s = max |dloss| over the kept rows, finite, and 1 where that is 0; the same in every thread of the block.
+__device__ __forceinline__ float largest_weight(const float *dloss, const int32_t *targets, int N, int V)
 {
     __shared__ float sh[32];
     float m = 0.f;
-    for (int i = threadIdx.x; i < N; i += 1024) {
-        const int t = targets[i];
-        if (t >= 0 && t < V) m = fmaxf(m, fabsf(dloss[i]));
+    for (int i = threadIdx.x; i < N; i += blockDim.x) {
+        const int t = __ldg(targets + i);
+        if (t >= 0 && t < V) m = fmaxf(m, fabsf(__ldg(dloss + i)));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        m = sh[threadIdx.x];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (threadIdx.x == 0) *scale = m > 0.f ? fminf(m, 3.402823466e38f) : 1.f;
-    }
+    m = 0.f;
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) m = fmaxf(m, sh[i]);
+    return m > 0.f ? fminf(m, 3.402823466e38f) : 1.f;
+}
+
+__global__ void __launch_bounds__(1024) ce_scale_kernel(const float *dloss, const int32_t *targets, int N, int V,
+                                                        float *scale)
+{
+    const float s = largest_weight(dloss, targets, N, V);
+    if (threadIdx.x == 0) *scale = s;
 }
 
 __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t v, float f)
@@ -554,12 +561,16 @@ __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t v, float f)
     return pack_bf16(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
 }
 
-// h dloss / s, the ignored rows zeroed: a zero of E times what such a row holds could be NaN.
+// h dloss / s, the ignored rows zeroed: a zero of E times what such a row holds could be NaN.  OWN: every block finds
+// s by itself, which is quicker than a launch before this one up to kOwnScale tokens.
+constexpr int kOwnScale = 4096;
+
+template <bool OWN>
 __global__ void __launch_bounds__(256) ce_weighted_rows_kernel(const uint4 *h, uint4 *out, const int32_t *targets,
-                                                               const float *dloss, const float *scale, int N, int D8,
-                                                               int V)
+                                                               const float *dloss, float *scale, int N, int D8, int V)
 {
-    const float s = *scale;
+    const float s = OWN ? largest_weight(dloss, targets, N, V) : *scale;
+    if (OWN && blockIdx.x == 0 && threadIdx.x == 0) *scale = s;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)N * D8; i += (int64_t)gridDim.x * 256) {
         const int row = (int)(i / D8), t = __ldg(targets + row);
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -642,6 +653,7 @@ struct TcWorkspace {
     size_t e, hk, acc, scale;
     size_t total;
     int piece, slices;
+    bool direct;              // one piece, one slice: dh needs no sums
 };
 
 TcWorkspace tc_layout(int N, int D, int V, bool backward)
@@ -663,10 +675,12 @@ TcWorkspace tc_layout(int N, int D, int V, bool backward)
         int s = ceil_div(2 * kPairs, dh_tiles);
         if (s > 32) s = 32;
         if (s > per) s = per;      // four stages a slice at least
+        if (per <= 4) s = 1;       // up to 1024 words in all: short enough, and no slices to join
         w.slices = s < 1 ? 1 : s;
+        w.direct = w.slices == 1 && w.piece >= V;
         w.e = off;   off = align256(off + (size_t)N * w.piece * 2);
         w.hk = off;  off = align256(off + (size_t)N * D * 2);
-        w.acc = off; off = align256(off + (size_t)w.slices * N * D * 4);
+        w.acc = off; off = align256(off + (w.direct ? 0 : (size_t)w.slices * N * D * 4));
         w.scale = off; off += 256;
     }
     w.total = off;
@@ -742,20 +756,26 @@ cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st)
     CeParams p = {};
     p.width = kTile;
     p.N = a.N; p.V = a.V; p.D = a.D;
-    p.targets = a.targets; p.lse_in = a.lse_in;
+    p.targets = a.targets; p.lse_in = a.lse_in; p.dloss = a.dloss;
+    p.direct = ws.direct;
     p.scale = (float *)(w + ws.scale);
     p.err = (unsigned *)w;
     if (a.dw) {
-        ce_scale_kernel<<<1, 1024, 0, st>>>(a.dloss, a.targets, a.N, a.V, (float *)(w + ws.scale));
-        ce_weighted_rows_kernel<<<grid_for((int64_t)a.N * a.D / 8), 256, 0, st>>>(
-            (const uint4 *)a.h, (uint4 *)(w + ws.hk), a.targets, a.dloss, p.scale, a.N, a.D / 8, a.V);
+        const bool own = a.N <= kOwnScale;
+        if (!own) ce_scale_kernel<<<1, 1024, 0, st>>>(a.dloss, a.targets, a.N, a.V, (float *)(w + ws.scale));
+        (own ? ce_weighted_rows_kernel<true> : ce_weighted_rows_kernel<false>)
+            <<<grid_for((int64_t)a.N * a.D / 8), 256, 0, st>>>((const uint4 *)a.h, (uint4 *)(w + ws.hk), a.targets,
+                                                               a.dloss, (float *)(w + ws.scale), a.N, a.D / 8, a.V);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
     }
     CeMaps mg, md;
     memset(&mg, 0, sizeof(mg));
     memset(&md, 0, sizeof(md));
     bool ok = make_map(&mg.a[0], a.h, a.D, a.N, a.D, kHalf) && make_map(&mg.b[0], a.w, a.D, a.V, a.D, kHalf) &&
               make_map(&md.b[0], w + ws.hk, a.D, a.N, a.D, kDepth) && make_map(&md.b[1], a.w, a.D, a.V, a.D, kDepth) &&
-              make_map(&md.out[1], w + ws.acc, a.D, a.N, a.D, 32, true, ws.slices);
+              (!a.dh || (ws.direct ? make_map(&md.out[1], a.dh, a.D, a.N, a.D, 32)
+                                   : make_map(&md.out[1], w + ws.acc, a.D, a.N, a.D, 32, true, ws.slices)));
     if (a.dw) ok = ok && make_map(&md.out[0], a.dw, a.D, a.V, a.D, 32);
     if (!ok) return cudaErrorInvalidValue;
     for (int v0 = 0; v0 < a.V; v0 += ws.piece) {
@@ -781,7 +801,7 @@ cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st)
         e = launch<kGrads>(md, p, st);
         if (e != cudaSuccess) return e;
     }
-    if (!a.dh) return cudaSuccess;
+    if (!a.dh || ws.direct) return cudaSuccess;
     return launch_early(ce_dh_finish_kernel, grid_for((int64_t)a.N * a.D / 4), 256, 0, st, (const float4 *)(w + ws.acc),
                         (uint2 *)a.dh, a.targets, a.dloss, a.N, a.D / 4, a.V, ws.slices);
 }
