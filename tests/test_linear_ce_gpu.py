@@ -186,3 +186,16 @@ def test_workspace_left_dirty_by_another_call():
         f1 = gdn.linear_cross_entropy_fwd(h, w, t, workspace=ws0)
         g1 = gdn.linear_cross_entropy_bwd(h, w, t, f1[1], dl, workspace=ws)
         assert all(torch.equal(p, q) for p, q in zip(f0 + g0, f1 + g1))
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("f32", 64), ("bf16", 61)])
+def test_error_word_reads_clear_after_a_call(dtype, D):
+    h, w, t, dl = make(70, D, 300, dtype, seed=9)
+    for backward in (False, True):
+        ws = torch.full((gdn.linear_cross_entropy_workspace_size(70, D, 300, DT[dtype], backward),), 255,
+                        dtype=torch.uint8, device="cuda")
+        if backward:
+            gdn.linear_cross_entropy_bwd(h, w, t, lse, dl, workspace=ws)
+        else:
+            _, lse = gdn.linear_cross_entropy_fwd(h, w, t, workspace=ws)
+        gdn.check_device_error(ws)
