@@ -249,8 +249,8 @@ struct Slot {
 // A warp's 32 / L groups of R rows into its slot; row i at src + i * step elements, rows from `rows` on and channels
 // behind D as zeros.  CW: bytes that a copy may move at once, by the alignment of the rows; 2 (a row of an odd number
 // of bf16) has no asynchronous copy and goes through registers.
-template <typename T, int L, int R, int CW>
-__device__ __forceinline__ void fetch(uint32_t slot, const T *src, int step, int rows, int channels)
+template <typename T, int L, int R, int CW, bool WHOLE>
+__device__ __forceinline__ void fetch_some(uint32_t slot, const T *src, int step, int rows, int channels)
 {
     constexpr int ROWS = R * 32 / L;
     constexpr int across = CW == 16 ? L / 2 : L * 2, down = 32 / across;   // copies a row; rows a step
@@ -261,7 +261,7 @@ __device__ __forceinline__ void fetch(uint32_t slot, const T *src, int step, int
         const bool live = col < channels;
 #pragma unroll
         for (int i = 0; i < ROWS / down; ++i) {
-            const bool in = live && r0 + down * i < rows;
+            const bool in = WHOLE || (live && r0 + down * i < rows);
             const T *from = p + (int64_t)step * (down * i);   // read if `in`
             if constexpr (CW == 16)
                 asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;"
@@ -285,10 +285,19 @@ __device__ __forceinline__ void fetch(uint32_t slot, const T *src, int step, int
     }
 }
 
+// Nearly all of them are whole: those go without the tests, a third of the instructions of the 4-byte copies.
+template <typename T, int L, int R, int CW>
+__device__ __forceinline__ void fetch(uint32_t slot, const T *src, int step, int rows, int channels)
+{
+    if (CW > 2 && rows == R * 32 / L && channels == L * kVec<T>) fetch_some<T, L, R, CW, true>(slot, src, step, rows, channels);
+    else fetch_some<T, L, R, CW, false>(slot, src, step, rows, channels);
+}
+
 // The lane's channels of one row; `mine` = how many of them lie before D.
-template <typename T, int CW>
+template <typename T, int CW, bool WHOLE>
 __device__ __forceinline__ void put(T *dst, const Pair (&v)[kPairs<T>], int mine)
 {
+    if (WHOLE) mine = kVec<T>;
     const uint2 w = pack<T>(v);
     if constexpr (CW == 16) {
         if (mine > 0) *reinterpret_cast<uint2 *>(dst) = w;
@@ -328,6 +337,9 @@ __device__ __forceinline__ int by_length(const GatedScanArgs &a, int k)
     return __ffs(__ballot_sync(0xffffffffu, lane < a.N && longer == k)) - 1;
 }
 
+struct Yes { __device__ constexpr bool operator()() const { return true; } };
+struct No { __device__ constexpr bool operator()() const { return false; } };
+
 // What a CTA works on: one sequence (with the cluster's other CTAs, along time) and one block of L kVec channels.
 template <typename T, int L>
 struct Work {
@@ -343,6 +355,11 @@ struct Work {
         channels = min(a.D - ch0, (L * kVec<T>));
         mine = channels - (threadIdx.x & (L - 1)) * kVec<T>;
         span(a, n, tok0, len);
+    }
+    // whether all the warp's groups have all their rows and channels
+    __device__ __forceinline__ bool whole(int rows, int most) const
+    {
+        return channels == L * kVec<T> && __all_sync(0xffffffffu, rows == most);
     }
     __device__ __forceinline__ void get(const float *s, const GatedScanArgs &a, Pair (&p)[kPairs<T>]) const
     {
@@ -455,12 +472,16 @@ scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
         ex.template join<CLUSTER>(turn, sum, h, carry, in);
         const int rows = rows_left(t0 + group * R, w.len, R);
         T *out = (T *)a.out + (base + (t0 + group * R) * a.D + (threadIdx.x & (L - 1)) * kVec<T>);
+        auto emit = [&](auto whole) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
+            for (int i = 0; i < R; ++i) {
 #pragma unroll
-            for (int v = 0; v < NP; ++v) in[v] = fma2(al[i][v], in[v], u[i][v]);
-            if (i < rows) put<T, CW>(out + (int64_t)a.D * i, in, w.mine);
-        }
+                for (int v = 0; v < NP; ++v) in[v] = fma2(al[i][v], in[v], u[i][v]);
+                if (whole() || i < rows) put<T, CW, whole()>(out + (int64_t)a.D * i, in, w.mine);
+            }
+        };
+        if (CW > 2 && w.whole(rows, R)) emit(Yes());
+        else emit(No());
     }
     wait_copies<0>();
     if (w.rank == 0 && warp == 0 && group == 0) w.set(a.final_state, a, carry);
@@ -530,27 +551,31 @@ scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
         const int rows = rows_left(rh, w.len, R);
         const int64_t start = w.len - 1 - rh;   // the row of the sequence's first token
         const int64_t at = last - rh * a.D + (threadIdx.x & (L - 1)) * kVec<T>;
+        auto emit = [&](auto whole) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            Pair prev[NP], x[NP], g[NP], vx[NP], vg[NP];
-            unpack<T>(words(shh + i * (8 * L)), prev);
-            if (i == start) w.get(a.init_state, a, prev);
-            if (GATE) {
-                unpack<T>(words(sx + i * (8 * L)), x);
-                unpack<T>(words(sg + i * (8 * L)), g);
-            }
+            for (int i = 0; i < R; ++i) {
+                Pair prev[NP], x[NP], g[NP], vx[NP], vg[NP];
+                unpack<T>(words(shh + i * (8 * L)), prev);
+                if (i == start) w.get(a.init_state, a, prev);
+                if (GATE) {
+                    unpack<T>(words(sx + i * (8 * L)), x);
+                    unpack<T>(words(sg + i * (8 * L)), g);
+                }
 #pragma unroll
-            for (int v = 0; v < NP; ++v) {
-                const Pair dh = add2(d[i][v], e[v]);
-                e[v] = mul2(al[i][v], dh);
-                vx[v] = GATE ? mul2(gate_of(g[v], al[i][v]), dh) : dh;
-                vg[v] = mul2(e[v], GATE ? fma2(x[v], pair(-1.f, -1.f), prev[v]) : prev[v]);
+                for (int v = 0; v < NP; ++v) {
+                    const Pair dh = add2(d[i][v], e[v]);
+                    e[v] = mul2(al[i][v], dh);
+                    vx[v] = GATE ? mul2(gate_of(g[v], al[i][v]), dh) : dh;
+                    vg[v] = mul2(e[v], GATE ? fma2(x[v], pair(-1.f, -1.f), prev[v]) : prev[v]);
+                }
+                if (whole() || i < rows) {
+                    put<T, CW, whole()>((T *)a.dx + at - (int64_t)a.D * i, vx, w.mine);
+                    put<T, CW, whole()>((T *)a.dg + at - (int64_t)a.D * i, vg, w.mine);
+                }
             }
-            if (i < rows) {
-                put<T, CW>((T *)a.dx + at - (int64_t)a.D * i, vx, w.mine);
-                put<T, CW>((T *)a.dg + at - (int64_t)a.D * i, vg, w.mine);
-            }
-        }
+        };
+        if (CW > 2 && w.whole(rows, R)) emit(Yes());
+        else emit(No());
         __syncwarp();
         load(r0 + STAGES * per, stage);
         commit_copies();
