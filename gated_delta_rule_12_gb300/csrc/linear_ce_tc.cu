@@ -11,7 +11,8 @@
 // brings shared-memory traffic under the 128 B a clock that one-CTA tiles of this size exceed.
 // Roles: warp 0 issues the TMA loads of its CTA, warp 1 of the even CTA the MMAs, warps 2-5 the epilogue (a thread a
 // row; 32 tensor-memory lanes a warp).  Eight epilogue warps, half of the columns each, measured slower (255 tokens,
-// 50257 words: 35 us against 31).
+// 50257 words: 35 us against 31), and so did tiles of fewer columns where they fill the last round of pairs better
+// (225 tiles of 224 columns instead of 197 of 256: 30.0 us against 29.6; 8192 x 2048 x 32768 with 128: 918 against 547).
 //
 // Precision: operands are bf16, sums fp32.  E is rounded to bf16 (relative 2^-8, independent from entry to entry, as
 // exact as the inputs that it meets).  It is kept free of dloss: a target's entry is mostly close to -1, where bf16 is
@@ -67,7 +68,6 @@ struct Product {
 struct CeParams {
     Product p[2];             // kGrads: dW, dh; else p[0]
     int tiles0, tiles;        // tiles of p[0]; of both
-    int width;                // columns of a tile; kTile but for kLogits
     int N, V, D;
     int v0, cols;             // the piece (kProb), the whole vocabulary (kLogits)
     int accumulate;           // kGrads: dh adds to the earlier pieces' sums
@@ -75,7 +75,7 @@ struct CeParams {
     const int32_t *targets;
     const float *lse_in, *dloss;
     const float *scale;       // kGrads: s
-    float2 *part;             // kLogits: [tiles of `width` words][N]
+    float2 *part;             // kLogits: [tiles of 256 words][N]
     float *at;                // kLogits: [N]
     unsigned *err;
     int clear_err;            // the call's first kernel
@@ -292,7 +292,6 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
     if (threadIdx.x == 0 && blockIdx.x == 0 && p.clear_err) *p.err = kDevErrNone;   // a timeout comes a second later at the earliest
 
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int width = MODE == kLogits ? p.width : kTile;
     if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
@@ -302,12 +301,12 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 const Product &q = p.p[c.which];
                 const CUtensorMap *ma = &maps.a[c.which], *mb = &maps.b[c.which];
                 const bool a_mn = MODE == kGrads && c.which == 0, b_mn = MODE == kGrads;
-                const int m0 = c.m * kTile + (int)rank * kHalf, n0 = c.n * width + (int)rank * (width / 2);
+                const int m0 = c.m * kTile + (int)rank * kHalf, n0 = c.n * kTile + (int)rank * kHalf;
                 for (int k = c.k0; k < c.k1; ++k, ++it) {
                     const uint32_t s = it % kStages, ph = (it / kStages) & 1;
                     if (!wait_bar(empty + 8 * s, ph ^ 1, abort_flag, p.err)) { ok = false; break; }
                     const uint32_t bar = map_to_rank(full + 8 * s, 0);
-                    if (rank == 0) mbar_expect_tx(full + 8 * s, kStageBytes + width * kDepth * 2);
+                    if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * kStageBytes);
                     const uint32_t sa = base + s * kStageBytes, sb = sa + kStageBytes / 2;
                     if (a_mn) {
                         load_2d(sa, ma, m0, k * kDepth, bar);
@@ -340,7 +339,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 const Tile c = tile_of<MODE>(p, t);
                 if (c.k0 >= c.k1) continue;
                 const bool a_mn = MODE == kGrads && c.which == 0, b_mn = MODE == kGrads;
-                const uint32_t idesc = idesc_bf16(kTile, width, a_mn, b_mn);
+                const uint32_t idesc = idesc_bf16(kTile, kTile, a_mn, b_mn);
                 const uint32_t buf = tiles & 1, use = tiles >> 1;
                 ++tiles;
                 if (!wait_bar(acc_empty + 8 * buf, (use & 1) ^ 1, abort_flag, p.err)) break;
@@ -363,7 +362,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
         }
     } else {
         const uint32_t quarter = warp & 3;                     // the 32 tensor-memory lanes a warp may read
-        const int chunks = width / 32;
+        constexpr int chunks = kTile / 32;
         const uint32_t buf0 = stores + (warp - 2) * kStore;
         const uint32_t leader_empty = map_to_rank(acc_empty, 0);
         uint32_t tiles = 0;
@@ -373,7 +372,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
             const uint32_t buf = tiles & 1, use = tiles >> 1;
             ++tiles;
             const int row0 = c.m * kTile + (int)rank * kHalf + (int)quarter * 32, row = row0 + lane;
-            const int col0 = c.n * width;
+            const int col0 = c.n * kTile;
             const bool in = row < p.N;
             int target = -1;
             float lse = 0.f, scale = 1.f;
@@ -632,21 +631,6 @@ bool make_map(CUtensorMap *m, const void *base, int cols, int rows, int64_t pitc
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Columns of the forward's tiles.  Tiles go out in rounds of kPairs, so a few of them are made narrower where that
-// fills the last round: 255 tokens, 50257 words: 197 tiles of 256 columns make three rounds like 225 of 224, an eighth
-// longer ones.  Narrower than 128 the tile's rows of A would be read too often.
-int tile_width(int N, int V)
-{
-    const int64_t mt = ceil_div(N, kTile);
-    int best = kTile;
-    int64_t cost = INT64_MAX;
-    for (int w = kTile; w >= kTile / 2; w -= 32) {
-        const int64_t c = (mt * ceil_div(V, w) + kPairs - 1) / kPairs * w;
-        if (c * 100 < cost * 97) { cost = c; best = w; }
-    }
-    return best;
-}
-
 struct TcWorkspace {
     size_t part, at;          // forward
     // backward: E of a piece [N][piece], h dloss / s of the kept rows [N][D], dh's slices [.][N][D], s
@@ -661,7 +645,7 @@ TcWorkspace tc_layout(int N, int D, int V, bool backward)
     TcWorkspace w = {};
     size_t off = 256;
     if (!backward) {
-        w.part = off; off = align256(off + (size_t)N * ceil_div(V, tile_width(N, V)) * 8);
+        w.part = off; off = align256(off + (size_t)N * ceil_div(V, kTile) * 8);
         w.at = off;   off = align256(off + (size_t)N * 4);
     } else {
         // pieces of equal size whose E takes up to 128 MB
@@ -732,10 +716,9 @@ cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st)
     CeMaps maps;
     memset(&maps, 0, sizeof(maps));
     CeParams p = {};
-    p.width = tile_width(a.N, a.V);
-    if (!make_map(&maps.a[0], a.h, a.D, a.N, a.D, kHalf) || !make_map(&maps.b[0], a.w, a.D, a.V, a.D, p.width / 2))
+    if (!make_map(&maps.a[0], a.h, a.D, a.N, a.D, kHalf) || !make_map(&maps.b[0], a.w, a.D, a.V, a.D, kHalf))
         return cudaErrorInvalidValue;
-    p.p[0] = {ceil_div(a.N, kTile), ceil_div(a.V, p.width), ceil_div(a.D, kDepth), 1, 0};
+    p.p[0] = {ceil_div(a.N, kTile), ceil_div(a.V, kTile), ceil_div(a.D, kDepth), 1, 0};
     p.tiles0 = p.tiles = p.p[0].mt * p.p[0].nt;
     p.N = a.N; p.V = a.V; p.D = a.D; p.cols = a.V;
     p.targets = a.targets;
@@ -754,7 +737,6 @@ cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st)
     char *w = (char *)a.workspace;
     const int mt = ceil_div(a.N, kTile), dt = ceil_div(a.D, kTile);
     CeParams p = {};
-    p.width = kTile;
     p.N = a.N; p.V = a.V; p.D = a.D;
     p.targets = a.targets; p.lse_in = a.lse_in; p.dloss = a.dloss;
     p.direct = ws.direct;

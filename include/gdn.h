@@ -320,8 +320,10 @@ gdn_status gdn_prologue_chunk_fwd(const void *xq, const void *xk, const void *xv
  *   init_state    [N, D] fp32 or NULL for zeros; final_state [N, D] fp32 or NULL to skip (may alias init_state);
  *                 a sequence without tokens passes its initial state on.
  *   cu_seqlens    as gdn_chunk_fwd (NULL: N = B sequences of T tokens; else packed, B = 1, N = num_seqs).
- *   T >= 0, D >= 1, no other limit on either; every pointer aligned to its element size (16-byte aligned rows take
- *   the fast path).  out must not overlap x or g.  The recurrence runs in fp32; out is rounded to dt once.
+ *   T >= 0, D >= 1, no other limit on either; every pointer aligned to its element size (rows that start on 16-byte
+ *   boundaries take the fast path).  out must not overlap x or g.  The recurrence runs in fp32; out is rounded to dt
+ *   once.  A state of exactly 0 stays 0 however much the gates grow; a run of rows whose gates grow beyond fp32's
+ *   range makes any other state infinite.
  * No workspace.  Results do not depend on timing.
  * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
  */
@@ -392,9 +394,11 @@ gdn_status gdn_layer_norm_bwd(const void *dout, const void *x, const float *mean
  *   targets       [N] int32.  A row whose target lies outside [0, V) is ignored: its loss and lse are 0.
  *   loss          [N] fp32;  lse [N] fp32 or NULL to skip (the backward pass needs it).
  *   0 <= N <= 2^23, D >= 1, V >= 1 (larger N: GDN_ERR_UNSUPPORTED).
- *   workspace     at least gdn_linear_cross_entropy_workspace_size(..., backward = 0) bytes, 256-byte aligned; its
- *                 first 256 bytes hold the device error word read by gdn_check_device_error.
- * Logits and sums are fp32.
+ *   workspace     at least gdn_linear_cross_entropy_workspace_size(..., backward = 0) bytes, 256-byte aligned (about
+ *                 N V / 32 bytes); its first 256 bytes hold the device error word read by gdn_check_device_error (a
+ *                 call with N = 0 leaves it as it is).
+ * Logits and sums are fp32.  bf16 with D a multiple of 8 runs on the tensor cores, other sizes and fp32 on the CUDA
+ * cores.  Results do not depend on timing.
  * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_CUDA.
  */
 size_t gdn_linear_cross_entropy_workspace_size(int32_t N, int32_t D, int32_t V, gdn_dtype dt, int32_t backward);
@@ -411,8 +415,10 @@ gdn_status gdn_linear_cross_entropy_fwd(const void *h, const void *weight, const
  *   dh            [N, D] dtype dt or NULL to skip;  dweight [V, D] dtype dt or NULL to skip.  Overwritten; both
  *                 16-byte aligned.
  * Ignored rows get a zero dh and add nothing to dweight, whatever their h and dloss hold.
- *   workspace     as the forward call, with backward = 1.
- * Errors as the forward call.
+ *   workspace     as the forward call, with backward = 1: up to 128 MB for a piece of the vocabulary, a copy of h and
+ *                 fp32 sums of dh.
+ * On the tensor cores softmax - onehot enters the products rounded to bf16, and so does dloss h, in units of the largest
+ * |dloss| (exact where all rows weigh the same); sums are fp32.  Errors as the forward call.
  */
 gdn_status gdn_linear_cross_entropy_bwd(const void *h, const void *weight, const int32_t *targets,
                                         const float *lse, const float *dloss,
