@@ -471,9 +471,15 @@ gdn_status gdn_layer_norm_bwd(const void *dout, const void *x, const float *mean
     return launch_layer_norm_bwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+// launch grids and tile counts stay within 32 bits
+static bool ce_size_supported(int32_t N, int32_t V)
+{
+    return N <= (1 << 23) && V <= (1 << 30) && (int64_t)N * V <= (int64_t)1 << 45;
+}
+
 size_t gdn_linear_cross_entropy_workspace_size(int32_t N, int32_t D, int32_t V, gdn_dtype dt, int32_t backward)
 {
-    if (N < 0 || N > (1 << 23) || D < 1 || V < 1 || (dt != GDN_F32 && dt != GDN_BF16)) return 0;
+    if (N < 0 || D < 1 || V < 1 || (dt != GDN_F32 && dt != GDN_BF16) || !ce_size_supported(N, V)) return 0;
     return linear_ce_workspace_bytes(N, D, V, (dt == GDN_BF16) ? 1 : 0, backward != 0);
 }
 
@@ -483,7 +489,7 @@ static gdn_status ce_args(LinearCeArgs &a, const void *h, const void *weight, co
     if (N < 0 || D < 1 || V < 1) return GDN_ERR_INVALID_ARG;
     if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
     if (N > 0 && (!h || !targets)) return GDN_ERR_INVALID_ARG;
-    if (N > (1 << 23)) return GDN_ERR_UNSUPPORTED;
+    if (!ce_size_supported(N, V)) return GDN_ERR_UNSUPPORTED;
     if (!weight) return GDN_ERR_INVALID_ARG;
     if (!aligned16(h) || !aligned16(weight) || !aligned_to(targets, 4)) return GDN_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace & 255u) != 0) return GDN_ERR_WORKSPACE;

@@ -180,7 +180,7 @@ __device__ __forceinline__ float inv_sqrt(float v)
 {
     const float r = rsqrtf(v);
     const float e = fmaf(v * r, -r, 1.f);
-    return r < 1e18f ? fmaf(0.5f * r, e, r) : r;   // v = 0 has no step: infinite as it is
+    return r > 0.f && r < 1e18f ? fmaf(0.5f * r, e, r) : r;   // v = 0 and infinite v have no step
 }
 
 // TEAM: threads of a row's team where they are a part of a warp or a warp, 0 for `team` threads of several warps.

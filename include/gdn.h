@@ -393,7 +393,7 @@ gdn_status gdn_layer_norm_bwd(const void *dout, const void *x, const float *mean
  *   h             [N, D] dtype dt;  weight [V, D] dtype dt;  both 16-byte aligned and contiguous.
  *   targets       [N] int32.  A row whose target lies outside [0, V) is ignored: its loss and lse are 0.
  *   loss          [N] fp32;  lse [N] fp32 or NULL to skip (the backward pass needs it).
- *   0 <= N <= 2^23, D >= 1, V >= 1 (larger N: GDN_ERR_UNSUPPORTED).
+ *   0 <= N <= 2^23, D >= 1, 1 <= V <= 2^30, N V <= 2^45 (beyond: GDN_ERR_UNSUPPORTED).
  *   workspace     at least gdn_linear_cross_entropy_workspace_size(..., backward = 0) bytes, 256-byte aligned (about
  *                 N V / 32 bytes); its first 256 bytes hold the device error word read by gdn_check_device_error (a
  *                 call with N = 0 leaves it as it is).

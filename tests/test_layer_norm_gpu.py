@@ -70,6 +70,17 @@ def test_constant_rows(D):
     assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=1e-6)
 
 
+@pytest.mark.parametrize("D", [64, 2048])
+def test_rows_whose_variance_leaves_fp32(D):
+    """Squares beyond fp32: rstd is 0 and the row its bias, as 1 / sqrt(inf) has it; no NaN."""
+    x = torch.randn(3, D).cuda()
+    x[1] *= 1e25
+    b = torch.randn(D).cuda()
+    y, mean, rstd = gdn.layer_norm_fwd(x, None, b)
+    assert rstd[1] == 0 and torch.equal(y[1], b) and torch.isfinite(mean).all()
+    assert torch.isfinite(y).all() and (rstd[[0, 2]] > 0).all()
+
+
 def test_rows_do_not_mix():
     """NaN and infinities stay in their rows, and reach the sums over rows."""
     x, w, b, dy = make(40, 512, "f32", seed=3)

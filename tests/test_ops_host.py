@@ -74,7 +74,8 @@ def test_norm_bwd_refusals(lib, over, code):
                                        (dict(h=None), 1), (dict(w=None), 1), (dict(t=None), 1), (dict(loss=None), 1),
                                        (dict(h=FAKE + 8), 1), (dict(w=FAKE + 4), 1), (dict(t=FAKE + 2), 1),
                                        (dict(lse=FAKE + 2), 1), (dict(ws=None), 3), (dict(ws=FAKE + 128), 3),
-                                       (dict(wsb=100), 3), (dict(N=(1 << 23) + 1), 2)])
+                                       (dict(wsb=100), 3), (dict(N=(1 << 23) + 1), 2), (dict(V=(1 << 30) + 1), 2),
+                                       (dict(N=1 << 23, V=(1 << 22) + 1), 2)])
 def test_ce_fwd_refusals(lib, over, code):
     assert call(lib.gdn_linear_cross_entropy_fwd, CE, over) == code
 
@@ -82,7 +83,8 @@ def test_ce_fwd_refusals(lib, over, code):
 @pytest.mark.parametrize("over,code", [(dict(N=-1), 1), (dict(D=0), 1), (dict(V=0), 1), (dict(dt=3), 1),
                                        (dict(h=None), 1), (dict(w=None), 1), (dict(t=None), 1), (dict(lse=None), 1),
                                        (dict(dl=None), 1), (dict(dh=FAKE + 8), 1), (dict(dw=FAKE + 8), 1),
-                                       (dict(ws=None), 3), (dict(wsb=100), 3), (dict(N=(1 << 23) + 1), 2)])
+                                       (dict(ws=None), 3), (dict(wsb=100), 3), (dict(N=(1 << 23) + 1), 2),
+                                       (dict(V=(1 << 30) + 1), 2)])
 def test_ce_bwd_refusals(lib, over, code):
     assert call(lib.gdn_linear_cross_entropy_bwd, CE_BWD, over) == code
 
