@@ -409,7 +409,7 @@ __device__ __forceinline__ Pair gate_of(Pair g, Pair a)
 // copies, so only the joins need barriers.  A group scans its R rows from 0 (S and H), the joined carry comes in,
 // and the rows are run again from it out of registers: memory is read once and written once.
 template <typename T, bool GATE, int CW, int L, int R, int STAGES, int WARPS, bool CLUSTER>
-__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), 16 / WARPS)
+__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), CLUSTER ? 1 : 2)
 scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 {
     constexpr int NP = kPairs<T>, ROWS = R * 32 / L, SLOT = Slot<L, R>::kBytes;
@@ -489,7 +489,7 @@ scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 
 // The same from the end: row i of a warp's slot is token len - 1 - (r0 + i), its h the one before.
 template <typename T, bool GATE, int CW, int L, int R, int STAGES, int WARPS, bool CLUSTER>
-__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), 16 / WARPS)
+__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), CLUSTER || (GATE && R == 8) ? 1 : 2)
 scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 {
     constexpr int NP = kPairs<T>, NT = GATE ? 4 : 3, ROWS = R * 32 / L, SLOT = Slot<L, R>::kBytes;
@@ -630,28 +630,34 @@ __global__ void __launch_bounds__(256) scan_step_kernel(float *state, const T *x
 
 // How the work is cut: lanes a row, warps a CTA, CTAs a cluster.
 //
-// One CTA of 8 warps takes some 2 us an iteration however few rows that is, so what is needed is enough CTAs, two on
-// each of 152 SMs, with many rows each.  Blocks of 128-byte rows come first (19 x 2048 x 1024 bf16, 304 CTAs: 42 us,
-// 5.6 TB/s).  Where they are fewer than 228, narrower rows, whose neighbours in the warp go along time instead, make
-// more CTAs of more rows (4 x 2048 x 2048: 16 lanes 27.8 us, 8 lanes 24.7, 4 lanes 34.8, forward).  Packed sequences
-// of unequal lengths are held up by the longest, so they take more CTAs (8 sequences, 32768 x 2048: 189, 126, 129 us).
-// A cluster's join costs about 2 us more an iteration (4 x 2048 x 2048 in clusters of two: 45 us), so it serves only
-// where 32-byte rows leave most SMs idle (1 x 32768 x 64, clusters of 16: 60 us with 128-byte rows, 19 us with 32-byte
-// rows; 438 us in one CTA).
+// An iteration of a CTA takes some 2 us however few rows that is, so what is needed is enough CTAs with many rows each.
+// Rows of 128 bytes (16 lanes) come first; where they make fewer than 80 CTAs, narrower ones, whose groups in the warp
+// go along time instead, make more CTAs of more rows (device time of the forward pass, bf16, N x T x D, with 16, 8 and
+// 4 lanes a row: 64 x 2048 x 512 73, 76, 94 us; 11 x 3292 x 256 36, 21, 21 us; 2 x 4096 x 1024 44, 24, 15 us).  Packed
+// sequences of unequal lengths are held up by the longest and take more CTAs (8 sequences, 32768 x 2048: 185, 115, 108
+// before the rows were padded apart in shared memory).  16 warps a CTA measured slower throughout (2 x 4096 x 1024: 17).
+//
+// A cluster's join adds 2 to 3 us an iteration (4 x 2048 x 2048 in clusters of two: 75 us instead of 24), so clusters
+// serve only where 32-byte rows still leave most SMs idle over a long time, and no more of them than the GPU holds at
+// once: a GPC's 16 to 20 SMs fit four clusters of four but two of eight (1 x 32768 x 64, 4 CTAs of rows: 97 us alone,
+// 38 in clusters of 4, 25 of 8, 18 of 16; 1 x 16384 x 256, 16 CTAs: 50 alone, 23 of 4, 31 of 8; 1 x 8192 x 512, 32
+// CTAs: 26 alone, 23 of 2, 15 of 4, 32 of 8).
 struct Cut { int lanes, warps, csize; };
+
+constexpr int kClusterWarps = 15;   // and the one that hands over
 
 Cut cut(const GatedScanArgs &a, int vec, int R)
 {
     Cut c = {16, 8, 1};
-    const int T = a.T;
+    const int64_t longest = a.cu ? (3 * (int64_t)a.T / a.N + 1 < a.T ? 3 * (int64_t)a.T / a.N + 1 : a.T) : a.T;
     auto units = [&] { return (int64_t)a.N * ceil_div(a.D, c.lanes * vec); };
     auto rows = [&] { return (int64_t)c.csize * c.warps * R * 32 / c.lanes; };
-    while (c.lanes > 4 && units() < (a.cu ? 912 : 228) && rows() < T) c.lanes /= 2;
-    if (c.lanes > 4 || units() >= 228 || rows() >= T) return c;
-    c.warps = 16;
-    if (units() >= 76 || rows() >= T) return c;
-    c.warps = 15;
-    while (c.csize < 16 && units() * c.csize * 2 <= 152 && rows() < T) c.csize *= 2;
+    while (c.lanes > 4 && units() < (a.cu ? 912 : 80) && rows() < longest) c.lanes /= 2;
+    if (c.lanes > 4 || longest <= 4 * rows()) return c;
+    const int most[] = {50, 34, 14, 7};   // clusters of 2, 4, 8, 16
+    c.warps = kClusterWarps;
+    for (int i = 0; i < 4 && units() <= most[i] && rows() < longest; ++i) c.csize *= 2;
+    if (c.csize == 1) c.warps = 8;
     return c;
 }
 
@@ -697,8 +703,7 @@ cudaError_t fwd_cw(const GatedScanArgs &a, cudaStream_t st)
 {
     constexpr int R = 8, S = 2, TENSORS = 2;
     const Cut c = cut(a, kVec<T>, R);
-    if (c.csize > 1) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 15, true>, a, S * TENSORS, c, st);
-    if (c.warps > 8) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 16, false>, a, S * TENSORS, c, st);
+    if (c.csize > 1) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, kClusterWarps, true>, a, S * TENSORS, c, st);
     if (c.lanes == 4) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 8, false>, a, S * TENSORS, c, st);
     if (c.lanes == 8) return launch<T, 8, R>(scan_fwd_kernel<T, GATE, CW, 8, R, S, 8, false>, a, S * TENSORS, c, st);
     return launch<T, 16, R>(scan_fwd_kernel<T, GATE, CW, 16, R, S, 8, false>, a, S * TENSORS, c, st);
@@ -709,8 +714,10 @@ cudaError_t bwd_cw(const GatedScanArgs &a, cudaStream_t st)
 {
     constexpr int R = GATE ? 4 : 8, S = 2, TENSORS = GATE ? 4 : 3;
     const Cut c = cut(a, kVec<T>, R);
-    if (c.csize > 1) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 15, true>, a, S * TENSORS, c, st);
-    if (c.warps > 8) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 16, false>, a, S * TENSORS, c, st);
+    if (c.csize > 1) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, kClusterWarps, true>, a, S * TENSORS, c, st);
+    // With the gate, 8 rows a thread leave room for one CTA an SM: as many as there are where they are few.
+    if (GATE && c.lanes == 4 && (int64_t)a.N * ceil_div(a.D, 4 * kVec<T>) <= 152)
+        return launch<T, 4, 8>(scan_bwd_kernel<T, GATE, CW, 4, 8, S, 8, false>, a, S * TENSORS, c, st);
     if (c.lanes == 4) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 8, false>, a, S * TENSORS, c, st);
     if (c.lanes == 8) return launch<T, 8, R>(scan_bwd_kernel<T, GATE, CW, 8, R, S, 8, false>, a, S * TENSORS, c, st);
     return launch<T, 16, R>(scan_bwd_kernel<T, GATE, CW, 16, R, S, 8, false>, a, S * TENSORS, c, st);
