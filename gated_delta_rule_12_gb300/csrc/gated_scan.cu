@@ -229,82 +229,165 @@ struct Exchange {
     }
 };
 
-// A warp's slot: its rows of 8 L bytes, R of a group together, and after each group of short rows another 8 L bytes, so
-// that the groups, which read one row each, find theirs in different banks (without it the backward pass of
-// 1 x 4999 x 1001 waits on shared memory more than on anything else).
-template <int L, int R>
+// How rows get into shared memory, by their alignment (device time of the backward pass, bf16, N x T x D).
+//   kWhole    every row starts on a 16-byte boundary: copies of 16 bytes.
+//   kWords    bf16, every row on a 4-byte boundary: copies of 4 bytes.
+//   kShifted  rows anywhere in tensors that start on 16-byte boundaries: the 16-byte chunks that hold a row are copied,
+//             and it is read where it lies in them.  4 x 2048 x 2049: 57 us, element by element 249; fp32 4 x 2048 x
+//             1001: 42 us, by words 64.  For rows that words fit, the three reads of each lane cost bf16 more than
+//             they save: 8 x 28544 x 26 124 us, by words 62; 4 x 2048 x 2050 57 and 68, forward 39 and 34.
+//   kElements anything else: element by element through registers.
+enum { kWhole = 16, kWords = 4, kShifted = 1, kElements = 2 };
+
+// A warp's slot: its rows, R of a group together, and a gap after each group of short rows, so that the groups, which
+// read one row each, find theirs in different banks (without it the backward pass of 1 x 4999 x 1001 waited on shared
+// memory more than on anything else).
+template <int L, int R, int CW>
 struct Slot {
-    static constexpr int kPad = L < 16 ? 8 * L : 0;
-    static constexpr int kGroup = R * 8 * L + kPad;
-    static constexpr int kBytes = kGroup * (32 / L);
+    static constexpr int kPitch = 8 * L + (CW == kShifted ? 16 : 0);
+    static constexpr int kPad = L < 16 ? ((8 * L - R * kPitch) % 128 + 128) % 128 : 0;
+    static constexpr int kGroup = R * kPitch + kPad;
+    static constexpr int kBytes = (kGroup * (32 / L) + 127) / 128 * 128;
+    static __device__ __forceinline__ uint32_t at(int row) { return row * kPitch + row / R * kPad; }
     // row r0 + down * i, where down is a power of two and r0 < down
     template <int DOWN>
     static __device__ __forceinline__ uint32_t at(int r0, int i)
     {
         const int group = DOWN >= R ? r0 / R + i * (DOWN / R) : i * DOWN / R;
-        return (r0 + DOWN * i) * (8 * L) + group * kPad;
+        return (r0 + DOWN * i) * kPitch + group * kPad;
     }
 };
 
-// A warp's 32 / L groups of R rows into its slot; row i at src + i * step elements, rows from `rows` on and channels
-// behind D as zeros.  CW: bytes that a copy may move at once, by the alignment of the rows; 2 (a row of an odd number
-// of bf16) has no asynchronous copy and goes through registers.
+// A warp's 32 / L groups of R rows into its slot; row i at src + i * step elements, rows from `rows` on as zeros and
+// channels behind D as anything; `end` is the tensor's.
 template <typename T, int L, int R, int CW, bool WHOLE>
-__device__ __forceinline__ void fetch_some(uint32_t slot, const T *src, int step, int rows, int channels)
+__device__ __forceinline__ void fetch_some(uint32_t slot, const T *src, const T *end, int step, int rows, int channels)
 {
+    using S = Slot<L, R, CW>;
     constexpr int ROWS = R * 32 / L;
-    constexpr int across = CW == 16 ? L / 2 : L * 2, down = 32 / across;   // copies a row; rows a step
-    const int lane = threadIdx.x & 31, col = (lane % across) * ((CW == 16 ? 16 : 4) / (int)sizeof(T)), r0 = lane / across;
-    const uint32_t to = slot + (lane % across) * (CW == 16 ? 16 : 4);
-    if constexpr (CW >= 4) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (CW == kWhole) {
+        constexpr int across = L / 2, down = 32 / across;   // copies a row; rows a step
+        const int col = (lane % across) * (16 / (int)sizeof(T)), r0 = lane / across;
         const T *p = src + ((int64_t)step * r0 + col);
         const bool live = col < channels;
 #pragma unroll
         for (int i = 0; i < ROWS / down; ++i) {
             const bool in = WHOLE || (live && r0 + down * i < rows);
             const T *from = p + (int64_t)step * (down * i);   // read if `in`
-            if constexpr (CW == 16)
+            asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;"
+                         :: "r"(slot + (lane % across) * 16 + S::template at<down>(r0, i)), "l"(from), "r"(in ? 16 : 0)
+                         : "memory");
+        }
+    } else if constexpr (CW == kWords) {
+        constexpr int across = L * 2 < 32 ? L * 2 : 32, down = 32 / across, per = 4 / (int)sizeof(T);
+        const int col = (lane % across) * per, r0 = lane / across;
+        const T *p = src + ((int64_t)step * r0 + col);
+        const bool live = col < channels;
+#pragma unroll
+        for (int i = 0; i < ROWS / down; ++i) {
+            const bool in = WHOLE || (live && r0 + down * i < rows);
+            const T *from = p + (int64_t)step * (down * i);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                         :: "r"(slot + (lane % across) * 4 + S::template at<down>(r0, i)), "l"(from), "r"(in ? 4 : 0)
+                         : "memory");
+        }
+    } else if constexpr (CW == kShifted) {
+        constexpr int across = L / 2 + 1, items = ROWS * across;
+#pragma unroll
+        for (int i = 0; i < (items + 31) / 32; ++i) {
+            const int k = lane + 32 * i, r = k / across, chunk = k - r * across;
+            const uintptr_t row = reinterpret_cast<uintptr_t>(src + (int64_t)step * r);
+            const uintptr_t from = (row & ~(uintptr_t)15) + 16 * chunk;
+            // up to the row's last byte, and no further than the tensor's
+            int bytes = 0;
+            if (r < rows && from < row + channels * sizeof(T))
+                bytes = (int)min((uintptr_t)16, reinterpret_cast<uintptr_t>(end) - from);
+            if (items % 32 == 0 || k < items)
                 asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;"
-                             :: "r"(to + Slot<L, R>::template at<down>(r0, i)), "l"(from), "r"(in ? 16 : 0) : "memory");
-            else
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
-                             :: "r"(to + Slot<L, R>::template at<down>(r0, i)), "l"(from), "r"(in ? 4 : 0) : "memory");
+                             :: "r"(slot + S::at(r) + 16 * chunk), "l"(from), "r"(bytes) : "memory");
         }
     } else {
+        constexpr int across = L * 2 < 32 ? L * 2 : 32, down = 32 / across, per = 4 / (int)sizeof(T);
+        const int col = (lane % across) * per, r0 = lane / across;
         uint32_t w[ROWS / down];
 #pragma unroll
         for (int i = 0; i < ROWS / down; ++i) {
-            const unsigned short *p = reinterpret_cast<const unsigned short *>(src + (int64_t)step * (r0 + down * i)) + col;
+            const T *p = src + ((int64_t)step * (r0 + down * i) + col);
             const bool in = r0 + down * i < rows;
-            w[i] = in && col < channels ? __ldg(p) : 0u;
-            if (in && col + 1 < channels) w[i] |= (uint32_t)__ldg(p + 1) << 16;
+            w[i] = 0;
+            if constexpr (sizeof(T) == 4) {
+                if (in && col < channels) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p));
+            } else {
+                if (in && col < channels) w[i] = __ldg(reinterpret_cast<const unsigned short *>(p));
+                if (in && col + 1 < channels) w[i] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p) + 1) << 16;
+            }
         }
 #pragma unroll
         for (int i = 0; i < ROWS / down; ++i)
-            asm volatile("st.shared.b32 [%0], %1;" :: "r"(to + Slot<L, R>::template at<down>(r0, i)), "r"(w[i]) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;"
+                         :: "r"(slot + (lane % across) * 4 + S::template at<down>(r0, i)), "r"(w[i]) : "memory");
     }
 }
 
 // Nearly all of them are whole: those go without the tests, a third of the instructions of the 4-byte copies.
 template <typename T, int L, int R, int CW>
-__device__ __forceinline__ void fetch(uint32_t slot, const T *src, int step, int rows, int channels)
+__device__ __forceinline__ void fetch(uint32_t slot, const T *src, const T *end, int step, int rows, int channels)
 {
-    if (CW > 2 && rows == R * 32 / L && channels == L * kVec<T>) fetch_some<T, L, R, CW, true>(slot, src, step, rows, channels);
-    else fetch_some<T, L, R, CW, false>(slot, src, step, rows, channels);
+    if ((CW == kWhole || CW == kWords) && rows == R * 32 / L && channels == L * kVec<T>)
+        fetch_some<T, L, R, CW, true>(slot, src, end, step, rows, channels);
+    else
+        fetch_some<T, L, R, CW, false>(slot, src, end, step, rows, channels);
 }
 
-// The lane's channels of one row; `mine` = how many of them lie before D.
-template <typename T, int CW, bool WHOLE>
+// The lane's channels of one row, out of a slot.  shift: where the row starts in its first chunk (kShifted).
+template <typename T, int CW>
+__device__ __forceinline__ uint2 words(uint32_t at, uint32_t shift)
+{
+    uint2 w;
+    if constexpr (CW != kShifted) {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(at));
+    } else if constexpr (sizeof(T) == 4) {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w.x) : "r"(at + shift));
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w.y) : "r"(at + shift + 4));
+    } else {
+        const uint32_t from = at + (shift & ~3u);
+        uint32_t a, b, c = 0;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a) : "r"(from));
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(b) : "r"(from + 4));
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.shared.b32 %0, [%1];\n\t}"
+                     : "+r"(c) : "r"(from + 8), "r"(shift & 2));
+        w.x = __funnelshift_r(a, b, (shift & 2) * 8);
+        w.y = __funnelshift_r(b, c, (shift & 2) * 8);
+    }
+    return w;
+}
+
+// The lane's channels of one row; `mine` = how many of them lie before D.  WHOLE: all of the group's.
+template <typename T, int L, int CW, bool WHOLE>
 __device__ __forceinline__ void put(T *dst, const Pair (&v)[kPairs<T>], int mine)
 {
-    if (WHOLE) mine = kVec<T>;
     const uint2 w = pack<T>(v);
-    if constexpr (CW == 16) {
-        if (mine > 0) *reinterpret_cast<uint2 *>(dst) = w;
-    } else if constexpr (CW == 4) {
+    if constexpr (CW == kWhole) {
+        if (WHOLE || mine > 0) *reinterpret_cast<uint2 *>(dst) = w;
+    } else if constexpr (sizeof(T) == 4 || CW == kWords) {
         constexpr int per = 4 / sizeof(T);
-        if (mine > 0) *reinterpret_cast<uint32_t *>(dst) = w.x;
-        if (mine > per) *reinterpret_cast<uint32_t *>(dst + per) = w.y;
+        if (WHOLE || mine > 0) *reinterpret_cast<uint32_t *>(dst) = w.x;
+        if (WHOLE || mine > per) *reinterpret_cast<uint32_t *>(dst + per) = w.y;
+    } else if constexpr (WHOLE) {
+        // a row at an odd element: its words are made of neighbours, the last one with the next lane's first
+        const int lane = threadIdx.x & (L - 1);
+        const uint32_t next = __shfl_down_sync(0xffffffffu, w.x, 1);
+        if ((reinterpret_cast<uintptr_t>(dst) & 2) == 0) {
+            *reinterpret_cast<uint32_t *>(dst) = w.x;
+            *reinterpret_cast<uint32_t *>(dst + 2) = w.y;
+        } else {
+            unsigned short *p = reinterpret_cast<unsigned short *>(dst);
+            if (lane == 0) p[0] = (unsigned short)w.x;
+            *reinterpret_cast<uint32_t *>(dst + 1) = __funnelshift_r(w.x, w.y, 16);
+            if (lane < L - 1) *reinterpret_cast<uint32_t *>(dst + 3) = __funnelshift_r(w.y, next, 16);
+            else p[3] = (unsigned short)(w.y >> 16);
+        }
     } else {
         unsigned short *p = reinterpret_cast<unsigned short *>(dst);
         if (mine > 0) p[0] = (unsigned short)w.x;
@@ -312,13 +395,6 @@ __device__ __forceinline__ void put(T *dst, const Pair (&v)[kPairs<T>], int mine
         if (mine > 2) p[2] = (unsigned short)w.y;
         if (mine > 3) p[3] = (unsigned short)(w.y >> 16);
     }
-}
-
-__device__ __forceinline__ uint2 words(uint32_t at)
-{
-    uint2 w;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(at));
-    return w;
 }
 
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -344,7 +420,7 @@ struct No { __device__ constexpr bool operator()() const { return false; } };
 template <typename T, int L>
 struct Work {
     int n, ch0, channels, rank, len, mine;
-    int64_t tok0;
+    int64_t tok0, total;   // the first token; elements of a tensor
     __device__ __forceinline__ Work(const GatedScanArgs &a, int nblocks, int csize)
     {
         rank = blockIdx.x % csize;
@@ -355,6 +431,7 @@ struct Work {
         channels = min(a.D - ch0, (L * kVec<T>));
         mine = channels - (threadIdx.x & (L - 1)) * kVec<T>;
         span(a, n, tok0, len);
+        total = (int64_t)(a.cu ? 1 : a.N) * a.T * a.D;
     }
     // whether all the warp's groups have all their rows and channels
     __device__ __forceinline__ bool whole(int rows, int most) const
@@ -412,7 +489,7 @@ template <typename T, bool GATE, int CW, int L, int R, int STAGES, int WARPS, bo
 __global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), CLUSTER ? 1 : 2)
 scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 {
-    constexpr int NP = kPairs<T>, ROWS = R * 32 / L, SLOT = Slot<L, R>::kBytes;
+    constexpr int NP = kPairs<T>, ROWS = R * 32 / L, SLOT = Slot<L, R, CW>::kBytes, PITCH = Slot<L, R, CW>::kPitch;
     extern __shared__ __align__(128) unsigned char smem[];
     const int warp = threadIdx.x >> 5, nwarps = (blockDim.x >> 5) - (CLUSTER ? 1 : 0);
     const Work<T, L> w(a, nblocks, csize);
@@ -429,16 +506,16 @@ scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 
     const uint32_t slots = shared_addr(smem) + warp * STAGES * 2 * SLOT;
     const int group = (threadIdx.x & 31) / L;
-    const uint32_t own = group * Slot<L, R>::kGroup + (threadIdx.x & (L - 1)) * 8;
-    const int64_t base = w.tok0 * a.D + w.ch0;
+    const uint32_t own = group * Slot<L, R, CW>::kGroup + (threadIdx.x & (L - 1)) * 8;
+    const int64_t base = w.tok0 * a.D + w.ch0, total = w.total;
     Pair carry[NP];
     w.get(a.init_state, a, carry);
     int64_t t0 = (int64_t)(w.rank * nwarps + warp) * ROWS;   // the warp's first row of the iteration
     auto load = [&](int64_t t, int st) {
         const int rows = rows_left(t, w.len, ROWS);
         const int64_t at = base + (rows > 0 ? t * a.D : 0);
-        fetch<T, L, R, CW>(slots + st * 2 * SLOT, (const T *)a.g + at, a.D, rows, w.channels);
-        fetch<T, L, R, CW>(slots + (st * 2 + 1) * SLOT, (const T *)a.x + at, a.D, rows, w.channels);
+        fetch<T, L, R, CW>(slots + st * 2 * SLOT, (const T *)a.g + at, (const T *)a.g + total, a.D, rows, w.channels);
+        fetch<T, L, R, CW>(slots + (st * 2 + 1) * SLOT, (const T *)a.x + at, (const T *)a.x + total, a.D, rows, w.channels);
     };
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
@@ -449,13 +526,15 @@ scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
         wait_copies<STAGES - 1>();
         __syncwarp();
         const uint32_t sg = slots + stage * 2 * SLOT + own, sx = sg + SLOT;
+        // where the group's rows start in their chunks: byte offsets, of which 4 bits matter
+        const uint32_t off = (uint32_t)(base + (t0 + group * R) * a.D) * (uint32_t)sizeof(T), inc = (uint32_t)a.D * sizeof(T);
         Pair al[R][NP], u[R][NP], sum[NP], h[NP], in[NP];
 #pragma unroll
         for (int v = 0; v < NP; ++v) sum[v] = h[v] = 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            unpack<T>(words(sg + i * (8 * L)), al[i]);   // rows behind the end: g = x = 0, the identity
-            unpack<T>(words(sx + i * (8 * L)), u[i]);
+            unpack<T>(words<T, CW>(sg + i * PITCH, (off + i * inc) & 15), al[i]);   // rows behind the end: g = x = 0, the identity
+            unpack<T>(words<T, CW>(sx + i * PITCH, (off + i * inc) & 15), u[i]);
 #pragma unroll
             for (int v = 0; v < NP; ++v) {
                 sum[v] = add2(sum[v], al[i][v]);
@@ -477,10 +556,10 @@ scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
             for (int i = 0; i < R; ++i) {
 #pragma unroll
                 for (int v = 0; v < NP; ++v) in[v] = fma2(al[i][v], in[v], u[i][v]);
-                if (whole() || i < rows) put<T, CW, whole()>(out + (int64_t)a.D * i, in, w.mine);
+                if (whole() || i < rows) put<T, L, CW, whole()>(out + (int64_t)a.D * i, in, w.mine);
             }
         };
-        if (CW > 2 && w.whole(rows, R)) emit(Yes());
+        if (w.whole(rows, R)) emit(Yes());
         else emit(No());
     }
     wait_copies<0>();
@@ -492,7 +571,7 @@ template <typename T, bool GATE, int CW, int L, int R, int STAGES, int WARPS, bo
 __global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), CLUSTER || (GATE && R == 8) ? 1 : 2)
 scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 {
-    constexpr int NP = kPairs<T>, NT = GATE ? 4 : 3, ROWS = R * 32 / L, SLOT = Slot<L, R>::kBytes;
+    constexpr int NP = kPairs<T>, NT = GATE ? 4 : 3, ROWS = R * 32 / L, SLOT = Slot<L, R, CW>::kBytes, PITCH = Slot<L, R, CW>::kPitch;
     extern __shared__ __align__(128) unsigned char smem[];
     const int warp = threadIdx.x >> 5, nwarps = (blockDim.x >> 5) - (CLUSTER ? 1 : 0);
     const Work<T, L> w(a, nblocks, csize);
@@ -509,8 +588,8 @@ scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 
     const uint32_t slots = shared_addr(smem) + warp * STAGES * NT * SLOT;
     const int group = (threadIdx.x & 31) / L;
-    const uint32_t own = group * Slot<L, R>::kGroup + (threadIdx.x & (L - 1)) * 8;
-    const int64_t last = (w.tok0 + w.len - 1) * a.D + w.ch0;
+    const uint32_t own = group * Slot<L, R, CW>::kGroup + (threadIdx.x & (L - 1)) * 8;
+    const int64_t last = (w.tok0 + w.len - 1) * a.D + w.ch0, total = w.total;
     Pair carry[NP];
     w.get(a.dfinal, a, carry);
     int64_t r0 = (int64_t)(w.rank * nwarps + warp) * ROWS;
@@ -518,10 +597,11 @@ scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
         const int rows = rows_left(r, w.len, ROWS), before = rows_left(r, w.len - 1, ROWS);   // the first token has none
         const int64_t at = rows > 0 ? last - r * a.D : 0;
         const uint32_t s = slots + st * NT * SLOT;
-        fetch<T, L, R, CW>(s, (const T *)a.g + at, -a.D, rows, w.channels);
-        fetch<T, L, R, CW>(s + SLOT, (const T *)a.dout + at, -a.D, rows, w.channels);
-        fetch<T, L, R, CW>(s + 2 * SLOT, (const T *)a.h + (before > 0 ? at - a.D : 0), -a.D, before, w.channels);
-        if (GATE) fetch<T, L, R, CW>(s + 3 * SLOT, (const T *)a.x + at, -a.D, rows, w.channels);
+        fetch<T, L, R, CW>(s, (const T *)a.g + at, (const T *)a.g + total, -a.D, rows, w.channels);
+        fetch<T, L, R, CW>(s + SLOT, (const T *)a.dout + at, (const T *)a.dout + total, -a.D, rows, w.channels);
+        fetch<T, L, R, CW>(s + 2 * SLOT, (const T *)a.h + (before > 0 ? at - a.D : 0), (const T *)a.h + total, -a.D, before,
+                           w.channels);
+        if (GATE) fetch<T, L, R, CW>(s + 3 * SLOT, (const T *)a.x + at, (const T *)a.x + total, -a.D, rows, w.channels);
     };
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
@@ -532,13 +612,14 @@ scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
         wait_copies<STAGES - 1>();
         __syncwarp();
         const uint32_t sg = slots + stage * NT * SLOT + own, sd = sg + SLOT, shh = sd + SLOT, sx = shh + SLOT;
+        const uint32_t off = (uint32_t)(last - (r0 + group * R) * a.D) * (uint32_t)sizeof(T), inc = (uint32_t)a.D * sizeof(T);
         Pair al[R][NP], d[R][NP], sum[NP], h[NP], e[NP];
 #pragma unroll
         for (int v = 0; v < NP; ++v) sum[v] = h[v] = 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            unpack<T>(words(sg + i * (8 * L)), al[i]);
-            unpack<T>(words(sd + i * (8 * L)), d[i]);
+            unpack<T>(words<T, CW>(sg + i * PITCH, (off - i * inc) & 15), al[i]);
+            unpack<T>(words<T, CW>(sd + i * PITCH, (off - i * inc) & 15), d[i]);
 #pragma unroll
             for (int v = 0; v < NP; ++v) {
                 sum[v] = add2(sum[v], al[i][v]);
@@ -555,11 +636,11 @@ scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 Pair prev[NP], x[NP], g[NP], vx[NP], vg[NP];
-                unpack<T>(words(shh + i * (8 * L)), prev);
+                unpack<T>(words<T, CW>(shh + i * PITCH, (off - (i + 1) * inc) & 15), prev);
                 if (i == start) w.get(a.init_state, a, prev);
                 if (GATE) {
-                    unpack<T>(words(sx + i * (8 * L)), x);
-                    unpack<T>(words(sg + i * (8 * L)), g);
+                    unpack<T>(words<T, CW>(sx + i * PITCH, (off - i * inc) & 15), x);
+                    unpack<T>(words<T, CW>(sg + i * PITCH, (off - i * inc) & 15), g);
                 }
 #pragma unroll
                 for (int v = 0; v < NP; ++v) {
@@ -569,12 +650,12 @@ scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
                     vg[v] = mul2(e[v], GATE ? fma2(x[v], pair(-1.f, -1.f), prev[v]) : prev[v]);
                 }
                 if (whole() || i < rows) {
-                    put<T, CW, whole()>((T *)a.dx + at - (int64_t)a.D * i, vx, w.mine);
-                    put<T, CW, whole()>((T *)a.dg + at - (int64_t)a.D * i, vg, w.mine);
+                    put<T, L, CW, whole()>((T *)a.dx + at - (int64_t)a.D * i, vx, w.mine);
+                    put<T, L, CW, whole()>((T *)a.dg + at - (int64_t)a.D * i, vg, w.mine);
                 }
             }
         };
-        if (CW > 2 && w.whole(rows, R)) emit(Yes());
+        if (w.whole(rows, R)) emit(Yes());
         else emit(No());
         __syncwarp();
         load(r0 + STAGES * per, stage);
@@ -644,9 +725,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(float *state, const T *x
 // CTAs: 26 alone, 23 of 2, 15 of 4, 32 of 8).
 struct Cut { int lanes, warps, csize; };
 
-constexpr int kClusterWarps = 15;   // and the one that hands over
-
-Cut cut(const GatedScanArgs &a, int vec, int R)
+// cluster_warps: as many as shared memory holds, beside the one that hands over
+Cut cut(const GatedScanArgs &a, int vec, int R, int cluster_warps)
 {
     Cut c = {16, 8, 1};
     const int64_t longest = a.cu ? (3 * (int64_t)a.T / a.N + 1 < a.T ? 3 * (int64_t)a.T / a.N + 1 : a.T) : a.T;
@@ -655,16 +735,16 @@ Cut cut(const GatedScanArgs &a, int vec, int R)
     while (c.lanes > 4 && units() < (a.cu ? 912 : 80) && rows() < longest) c.lanes /= 2;
     if (c.lanes > 4 || longest <= 4 * rows()) return c;
     const int most[] = {50, 34, 14, 7};   // clusters of 2, 4, 8, 16
-    c.warps = kClusterWarps;
+    c.warps = cluster_warps;
     for (int i = 0; i < 4 && units() <= most[i] && rows() < longest; ++i) c.csize *= 2;
     if (c.csize == 1) c.warps = 8;
     return c;
 }
 
-template <typename T, int L, int R, class Kernel>
+template <typename T, int L, int R, int CW, class Kernel>
 cudaError_t launch(Kernel kernel, const GatedScanArgs &a, int slots, Cut c, cudaStream_t st)
 {
-    const int slot_bytes = slots * Slot<L, R>::kBytes;   // of a warp
+    const int slot_bytes = slots * Slot<L, R, CW>::kBytes;   // of a warp
     const int nblocks = ceil_div(a.D, L * kVec<T>);
     const int64_t units = (int64_t)a.N * nblocks;
     const int most = ceil_div(a.T > 0 ? a.T : 1, R * 32 / L);
@@ -689,56 +769,65 @@ cudaError_t launch(Kernel kernel, const GatedScanArgs &a, int slots, Cut c, cuda
     return cudaLaunchKernelEx(&cfg, kernel, a, nblocks, c.csize);
 }
 
-// Bytes that one copy may move: every row of every tensor has to start on a multiple of them.
 template <typename T>
-int copy_width(const GatedScanArgs &a)
+int copies_of(const GatedScanArgs &a)
 {
-    const uintptr_t all = (uintptr_t)a.x | (uintptr_t)a.g | (uintptr_t)a.out | (uintptr_t)a.h | (uintptr_t)a.dout |
-                          (uintptr_t)a.dx | (uintptr_t)a.dg | (uintptr_t)a.D * sizeof(T);
-    return (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 2;
+    const uintptr_t bases = (uintptr_t)a.x | (uintptr_t)a.g | (uintptr_t)a.out | (uintptr_t)a.h | (uintptr_t)a.dout |
+                            (uintptr_t)a.dx | (uintptr_t)a.dg, rows = (uintptr_t)a.D * sizeof(T);
+    if (((bases | rows) & 15) == 0) return kWhole;
+    if (sizeof(T) == 2 && ((bases | rows) & 3) == 0) return kWords;
+    return (bases & 15) == 0 ? kShifted : kElements;
 }
 
 template <typename T, bool GATE, int CW>
 cudaError_t fwd_cw(const GatedScanArgs &a, cudaStream_t st)
 {
-    constexpr int R = 8, S = 2, TENSORS = 2;
-    const Cut c = cut(a, kVec<T>, R);
-    if (c.csize > 1) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, kClusterWarps, true>, a, S * TENSORS, c, st);
-    if (c.lanes == 4) return launch<T, 4, R>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 8, false>, a, S * TENSORS, c, st);
-    if (c.lanes == 8) return launch<T, 8, R>(scan_fwd_kernel<T, GATE, CW, 8, R, S, 8, false>, a, S * TENSORS, c, st);
-    return launch<T, 16, R>(scan_fwd_kernel<T, GATE, CW, 16, R, S, 8, false>, a, S * TENSORS, c, st);
+    constexpr int R = 8, S = 2, SLOTS = S * 2, CLUSTER_WARPS = 15;
+    if constexpr (CW != kElements) {   // that one is there for being right
+        const Cut c = cut(a, kVec<T>, R, CLUSTER_WARPS);
+        if (c.csize > 1)
+            return launch<T, 4, R, CW>(scan_fwd_kernel<T, GATE, CW, 4, R, S, CLUSTER_WARPS, true>, a, SLOTS, c, st);
+        if (c.lanes == 4) return launch<T, 4, R, CW>(scan_fwd_kernel<T, GATE, CW, 4, R, S, 8, false>, a, SLOTS, c, st);
+        if (c.lanes == 8) return launch<T, 8, R, CW>(scan_fwd_kernel<T, GATE, CW, 8, R, S, 8, false>, a, SLOTS, c, st);
+    }
+    return launch<T, 16, R, CW>(scan_fwd_kernel<T, GATE, CW, 16, R, S, 8, false>, a, SLOTS, Cut{16, 8, 1}, st);
 }
 
 template <typename T, bool GATE, int CW>
 cudaError_t bwd_cw(const GatedScanArgs &a, cudaStream_t st)
 {
-    constexpr int R = GATE ? 4 : 8, S = 2, TENSORS = GATE ? 4 : 3;
-    const Cut c = cut(a, kVec<T>, R);
-    if (c.csize > 1) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, kClusterWarps, true>, a, S * TENSORS, c, st);
-    // With the gate, 8 rows a thread leave room for one CTA an SM: as many as there are where they are few.
-    if (GATE && c.lanes == 4 && (int64_t)a.N * ceil_div(a.D, 4 * kVec<T>) <= 152)
-        return launch<T, 4, 8>(scan_bwd_kernel<T, GATE, CW, 4, 8, S, 8, false>, a, S * TENSORS, c, st);
-    if (c.lanes == 4) return launch<T, 4, R>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 8, false>, a, S * TENSORS, c, st);
-    if (c.lanes == 8) return launch<T, 8, R>(scan_bwd_kernel<T, GATE, CW, 8, R, S, 8, false>, a, S * TENSORS, c, st);
-    return launch<T, 16, R>(scan_bwd_kernel<T, GATE, CW, 16, R, S, 8, false>, a, S * TENSORS, c, st);
+    constexpr int R = GATE ? 4 : 8, S = 2, SLOTS = S * (GATE ? 4 : 3), CLUSTER_WARPS = CW == kShifted ? 10 : 15;
+    if constexpr (CW != kElements) {
+        const Cut c = cut(a, kVec<T>, R, CLUSTER_WARPS);
+        if (c.csize > 1)
+            return launch<T, 4, R, CW>(scan_bwd_kernel<T, GATE, CW, 4, R, S, CLUSTER_WARPS, true>, a, SLOTS, c, st);
+        // With the gate, 8 rows a thread leave room for one CTA an SM: as many as there are where they are few.
+        if (GATE && c.lanes == 4 && (int64_t)a.N * ceil_div(a.D, 4 * kVec<T>) <= 152)
+            return launch<T, 4, 8, CW>(scan_bwd_kernel<T, GATE, CW, 4, 8, S, 8, false>, a, SLOTS, c, st);
+        if (c.lanes == 4) return launch<T, 4, R, CW>(scan_bwd_kernel<T, GATE, CW, 4, R, S, 8, false>, a, SLOTS, c, st);
+        if (c.lanes == 8) return launch<T, 8, R, CW>(scan_bwd_kernel<T, GATE, CW, 8, R, S, 8, false>, a, SLOTS, c, st);
+    }
+    return launch<T, 16, R, CW>(scan_bwd_kernel<T, GATE, CW, 16, R, S, 8, false>, a, SLOTS, Cut{16, 8, 1}, st);
 }
 
 template <typename T, bool GATE>
 cudaError_t fwd(const GatedScanArgs &a, cudaStream_t st)
 {
-    const int cw = copy_width<T>(a);
+    const int c = copies_of<T>(a);
     if constexpr (sizeof(T) == 2)
-        if (cw == 2) return fwd_cw<T, GATE, 2>(a, st);
-    return cw == 16 ? fwd_cw<T, GATE, 16>(a, st) : fwd_cw<T, GATE, 4>(a, st);
+        if (c == kWords) return fwd_cw<T, GATE, kWords>(a, st);
+    return c == kWhole ? fwd_cw<T, GATE, kWhole>(a, st) : c == kShifted ? fwd_cw<T, GATE, kShifted>(a, st)
+                                                                        : fwd_cw<T, GATE, kElements>(a, st);
 }
 
 template <typename T, bool GATE>
 cudaError_t bwd(const GatedScanArgs &a, cudaStream_t st)
 {
-    const int cw = copy_width<T>(a);
+    const int c = copies_of<T>(a);
     if constexpr (sizeof(T) == 2)
-        if (cw == 2) return bwd_cw<T, GATE, 2>(a, st);
-    return cw == 16 ? bwd_cw<T, GATE, 16>(a, st) : bwd_cw<T, GATE, 4>(a, st);
+        if (c == kWords) return bwd_cw<T, GATE, kWords>(a, st);
+    return c == kWhole ? bwd_cw<T, GATE, kWhole>(a, st) : c == kShifted ? bwd_cw<T, GATE, kShifted>(a, st)
+                                                                        : bwd_cw<T, GATE, kElements>(a, st);
 }
 
 template <typename T, bool GATE>

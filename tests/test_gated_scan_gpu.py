@@ -47,7 +47,8 @@ def run_and_check(d, gate, use_init=True):
 @pytest.mark.parametrize("gate", [False, True])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("N,T,D", [(1, 1, 1), (2, 3, 64), (3, 17, 33), (1, 257, 130), (2, 600, 96), (5, 64, 8),
-                                   (1, 1025, 66), (300, 2, 24), (1, 5000, 20), (2, 129, 1000)])
+                                   (1, 1025, 66), (300, 2, 24), (1, 5000, 20), (2, 129, 1000), (1, 9000, 19), (2, 4500, 22),
+                                   (1, 3001, 24), (4, 700, 81), (30, 90, 257), (85, 40, 36)])
 def test_scan_against_the_definition(N, T, D, dtype, gate):
     run_and_check(make(N, T, D, dtype, seed=N * T + D), gate, use_init=(T % 2 == 1))
 
@@ -173,8 +174,9 @@ def test_state_in_place_and_pieces_of_a_sequence():
 
 def test_pointers_off_the_fast_path():
     """Rows of a size or at an address that no vector access fits."""
-    for D, off in ((64, 1), (64, 3), (63, 0), (66, 2)):
-        buf = torch.randn(2 * 100 * D + 8).to(torch.bfloat16).cuda()
+    for D, off, dtype in ((64, 1, "bf16"), (64, 3, "bf16"), (63, 0, "bf16"), (66, 2, "bf16"), (64, 1, "f32"),
+                          (63, 2, "f32"), (63, 3, "bf16")):
+        buf = torch.randn(2 * 100 * D + 8).to(DT[dtype]).cuda()
         x = buf[off:off + 100 * D].view(1, 100, D)
         g = -buf[off + 100 * D:off + 200 * D].abs().view(1, 100, D).mul_(0.1)
         d = {"x": x, "g": g, "dout": x.clone(), "init": torch.randn(1, D).cuda(), "dfinal": torch.randn(1, D).cuda(),
