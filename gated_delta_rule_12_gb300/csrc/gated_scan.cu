@@ -482,11 +482,19 @@ __device__ __forceinline__ Pair gate_of(Pair g, Pair a)
     return pair(fabsf(g0) <= 0.5f ? -s0 : 1.f - a0, fabsf(g1) <= 0.5f ? -s1 : 1.f - a1);
 }
 
+// CTAs that registers are limited for.  Copies by words hold so many addresses that 128 registers spill over them:
+// backward 1 x 25951 x 1546 364 us with two CTAs' registers, 215 with one's, 4 x 2048 x 2050 68 and 52; forward 141 and
+// 126 with 4 lanes a row, but 32 and 35 (16 x 1000 x 1002) with 16.
+constexpr int ctas_an_sm(bool backward, bool gate, int cw, int L, int R, bool cluster)
+{
+    return cluster || (backward && gate && R == 8) || (cw == kWords && (backward || L == 4)) ? 1 : 2;
+}
+
 // An iteration takes csize * nwarps * R * 32 / L rows.  Rows pass through a ring of each warp's own slots by asynchronous
 // copies, so only the joins need barriers.  A group scans its R rows from 0 (S and H), the joined carry comes in,
 // and the rows are run again from it out of registers: memory is read once and written once.
 template <typename T, bool GATE, int CW, int L, int R, int STAGES, int WARPS, bool CLUSTER>
-__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), CLUSTER ? 1 : 2)
+__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), ctas_an_sm(false, GATE, CW, L, R, CLUSTER))
 scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 {
     constexpr int NP = kPairs<T>, ROWS = R * 32 / L, SLOT = Slot<L, R, CW>::kBytes, PITCH = Slot<L, R, CW>::kPitch;
@@ -568,7 +576,7 @@ scan_fwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 
 // The same from the end: row i of a warp's slot is token len - 1 - (r0 + i), its h the one before.
 template <typename T, bool GATE, int CW, int L, int R, int STAGES, int WARPS, bool CLUSTER>
-__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), CLUSTER || (GATE && R == 8) ? 1 : 2)
+__global__ void __launch_bounds__(32 * WARPS + (CLUSTER ? 32 : 0), ctas_an_sm(true, GATE, CW, L, R, CLUSTER))
 scan_bwd_kernel(const GatedScanArgs a, int nblocks, int csize)
 {
     constexpr int NP = kPairs<T>, NT = GATE ? 4 : 3, ROWS = R * 32 / L, SLOT = Slot<L, R, CW>::kBytes, PITCH = Slot<L, R, CW>::kPitch;
