@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kSMs = 152;
 
-// VW elements as one access: 16 bytes, or one element where rows are not aligned for more.
+// VW elements as one access: 16 bytes, or two bf16 or one element where rows are not aligned for more.
 template <typename T, int VW>
 struct Raw {
     static constexpr int kWords = VW * sizeof(T) / 4 > 0 ? VW * sizeof(T) / 4 : 1;
@@ -59,7 +59,7 @@ struct Ring {
         if constexpr (kBytes == 16)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                          :: "r"(slot(stage, tensor, v)), "l"(p), "r"(in ? 16 : 0) : "memory");
-        else if constexpr (sizeof(T) == 4)
+        else if constexpr (VW * sizeof(T) == 4)
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
                          :: "r"(slot(stage, tensor, v)), "l"(p), "r"(in ? 4 : 0) : "memory");
         else
@@ -99,6 +99,12 @@ __device__ __forceinline__ void put(T *p, const Pair (&y)[N], int v)
         float a, b;
         split(y[v / 2], a, b);
         *p = from_f32<T>(v & 1 ? b : a);
+    } else if constexpr (VW == 2) {
+        float a, b;
+        uint32_t w;
+        split(y[v], a, b);
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+        *reinterpret_cast<uint32_t *>(p) = w;
     } else if constexpr (sizeof(T) == 4) {
         float4 r;
         split(y[2 * v], r.x, r.y);
@@ -599,11 +605,22 @@ cudaError_t run(const LayerNormArgs &a, cudaStream_t st)
 #undef GDN_NORM1
 }
 
-bool vectors_fit(const LayerNormArgs &a)
+// Bytes of an access that every row's start fits.
+int access_of(const LayerNormArgs &a)
 {
     const uintptr_t all = (uintptr_t)a.x | (uintptr_t)a.out | (uintptr_t)a.dout | (uintptr_t)a.dx |
                           (uintptr_t)a.D * (a.dt ? 2 : 4);
-    return (all & 15) == 0;
+    return (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 2;
+}
+
+template <typename T, bool BWD>
+cudaError_t run_rows(const LayerNormArgs &a, cudaStream_t st)
+{
+    const int access = access_of(a);
+    if (access == 16) return run<T, 16 / sizeof(T), BWD>(a, st);
+    if constexpr (sizeof(T) == 2)
+        if (access == 4) return run<T, 2, BWD>(a, st);
+    return run<T, 1, BWD>(a, st);
 }
 
 template <typename T>
@@ -613,13 +630,13 @@ cudaError_t fwd(const LayerNormArgs &a, cudaStream_t st)
         long_fwd_kernel<T><<<(unsigned)(a.rows < kSMs * 8 ? a.rows : kSMs * 8), kThreads, 0, st>>>(a);
         return cudaGetLastError();
     }
-    return vectors_fit(a) ? run<T, 16 / sizeof(T), false>(a, st) : run<T, 1, false>(a, st);
+    return run_rows<T, false>(a, st);
 }
 
 template <typename T>
 cudaError_t bwd(const LayerNormArgs &a, cudaStream_t st)
 {
-    if (a.D <= kMost) return vectors_fit(a) ? run<T, 16 / sizeof(T), true>(a, st) : run<T, 1, true>(a, st);
+    if (a.D <= kMost) return run_rows<T, true>(a, st);
     const unsigned blocks = (unsigned)(a.rows < kSMs * 8 ? a.rows : kSMs * 8);
     if (a.dx && blocks) long_dx_kernel<T><<<blocks, kThreads, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();

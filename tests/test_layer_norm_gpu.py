@@ -41,7 +41,8 @@ def run_and_check(x, w, b, dy, eps=1e-5):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,D", [(1, 1), (1, 2), (3, 7), (5, 8), (33, 64), (1000, 128), (7, 129), (16, 200),
                                     (130, 256), (19, 1001), (64, 1024), (9, 2048), (300, 2056), (5, 5120), (4, 8192),
-                                    (3, 8200), (2, 20000), (3, 70001), (4099, 24), (2500, 40)])
+                                    (3, 8200), (2, 20000), (3, 70001), (4099, 24), (2500, 40), (90, 22),
+                                    (70, 254), (40, 1002), (6, 4098), (3, 10002), (3, 15001)])
 def test_norm_against_the_definition(rows, D, dtype):
     run_and_check(*make(rows, D, dtype, seed=rows + D))
 
