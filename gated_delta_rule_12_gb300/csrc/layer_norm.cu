@@ -10,9 +10,11 @@
 // memory and leave one partial row a CTA, which a second kernel adds up.  Rows come four ahead through asynchronous
 // copies: 32 KB of them in flight on an SM, as registers one row ahead allow, held the backward pass to 3.9 TB/s and
 // the norm over heads (131072 x 128) to 2.6.  Rows of more than 16384 elements go through kernels that read them again.
+// bf16 rows on 4-byte boundaries go by words, an odd number of them element by element (48841 x 686 backward 55 us, 687
+// 173 us).
 //
-// Measured (GB300, bf16, device time): forward 8192 x 2048 14.8 us (4.6 TB/s); backward 25.2 us, 131072 x 128 backward
-// 24.1 us (4.0 and 4.2 TB/s), of which about 3 us are the second kernel and the gap before it.
+// Measured (GB300, bf16, device time): forward 8192 x 2048 15.1 us (4.4 TB/s); backward 25.2 us, 131072 x 128 backward
+// 24.0 us (4.0 and 4.2 TB/s), of which about 3 us are the second kernel and the gap before it.
 #include "common.cuh"
 #include "kernels.h"
 #include "pairs.cuh"
