@@ -10,8 +10,8 @@
 // memory and leave one partial row a CTA, which a second kernel adds up.  Rows come four ahead through asynchronous
 // copies: 32 KB of them in flight on an SM, as registers one row ahead allow, held the backward pass to 3.9 TB/s and
 // the norm over heads (131072 x 128) to 2.6.  Rows of more than 16384 elements go through kernels that read them again.
-// bf16 rows on 4-byte boundaries go by words, an odd number of them element by element (48841 x 686 backward 55 us, 687
-// 173 us).
+// Rows of other lengths than 16-byte accesses fit go by the 16-byte chunks that they lie in (48841 x 687 bf16: forward
+// 42 us, backward 53 us; element by element 93 and 173), unless their tensors start elsewhere.
 //
 // Measured (GB300, bf16, device time): forward 8192 x 2048 15.1 us (4.4 TB/s); backward 25.2 us, 131072 x 128 backward
 // 24.0 us (4.0 and 4.2 TB/s), of which about 3 us are the second kernel and the gap before it.
@@ -27,6 +27,7 @@ namespace {
 // ---------------------------------------------------------------------------
 
 constexpr int kSMs = 152;
+static_assert(kSMs % 8 == 0, "a team's rows all have to start at the same place of a 16-byte chunk");
 
 // VW elements as one access: 16 bytes, or two bf16 or one element where rows are not aligned for more.
 template <typename T, int VW>
@@ -37,6 +38,13 @@ struct Raw {
     {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
         else return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    }
+    __device__ __forceinline__ void drop(int n)   // the first n elements become 0
+    {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k)
+            if constexpr (sizeof(T) == 4) w[k] = k < n ? 0u : w[k];
+            else w[k] = 2 * k + 1 < n ? 0u : 2 * k < n ? w[k] & 0xffff0000u : w[k];
     }
 };
 
@@ -68,6 +76,13 @@ struct Ring {
             asm volatile("st.shared.b32 [%0], %1;"
                          :: "r"(slot(stage, tensor, v)),
                             "r"(in ? (uint32_t)__ldcs(reinterpret_cast<const unsigned short *>(p)) : 0u) : "memory");
+    }
+    // the first `left` elements of an access of 16 bytes, zeros behind them
+    __device__ __forceinline__ void load_some(int stage, int tensor, int v, const T *p, int left) const
+    {
+        const int bytes = min(max(left * (int)sizeof(T), 0), 16);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     :: "r"(slot(stage, tensor, v)), "l"(p), "r"(bytes) : "memory");
     }
     __device__ __forceinline__ void read(int stage, int tensor, Raw<T, VW> (&r)[NV]) const
     {
@@ -122,6 +137,18 @@ __device__ __forceinline__ void put(T *p, const Pair (&y)[N], int v)
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
         }
         *reinterpret_cast<uint4 *>(p) = r;
+    }
+}
+
+// The same for an access of which only columns c to c + VW - 1 within [0, D) are the row's.
+template <typename T, int VW, int N>
+__device__ __forceinline__ void put_some(T *p, const Pair (&y)[N], int v, int c, int D)
+{
+#pragma unroll
+    for (int j = 0; j < VW; ++j) {
+        float e[2];
+        split(y[(v * VW + j) / 2], e[0], e[1]);
+        if (c + j >= 0 && c + j < D) p[j] = from_f32<T>(e[j & 1]);
     }
 }
 
@@ -191,9 +218,18 @@ __device__ __forceinline__ float inv_sqrt(float v)
     return r > 0.f && r < 1e18f ? fmaf(0.5f * r, e, r) : r;   // v = 0 and infinite v have no step
 }
 
+// How rows lie to the accesses.
+//   kPartial  every row starts with an access, the last may be missing for some threads.
+//   kFull     the same, and the row fills the team: no access is missing.
+//   kShifted  rows of any length in tensors that start on 16-byte boundaries: the accesses are the 16-byte chunks of
+//             memory, and the first and the last of a row hold elements of its neighbours.  The grid's teams are a
+//             multiple of 8, so a team's rows all start at the same place of their first chunk (`ph` elements into it)
+//             and its threads keep their columns.
+enum { kPartial, kFull, kShifted };
+
 // TEAM: threads of a row's team where they are a part of a warp or a warp, 0 for `team` threads of several warps.
-// MAX: most threads a CTA.  FULL: the row fills the team, no access is missing.
-template <typename T, int VW, int NV, int TEAM, int MAX, bool FULL>
+// MAX: most threads a CTA.
+template <typename T, int VW, int NV, int TEAM, int MAX, int FIT>
 __global__ void __launch_bounds__(MAX, MAX == 256 ? (NV * VW <= 8 ? 4 : NV * VW <= 16 ? 3 : 2) : 1)
 rows_fwd_kernel(const LayerNormArgs a, int team)
 {
@@ -208,31 +244,39 @@ rows_fwd_kernel(const LayerNormArgs a, int team)
     const int lane = threadIdx.x % team, teams = blockDim.x / team;
     const int64_t step = (int64_t)gridDim.x * teams;
     const float inv = 1.f / (float)a.D;
-    bool live[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) live[v] = FULL || (v * team + lane) * VW < a.D;
     // every team of a CTA goes through the same number of rows: the shuffles take whole warps
     int64_t r = (int64_t)blockIdx.x * teams + threadIdx.x / team;
-    const T *next = (const T *)a.x + r * a.D + lane * VW;
-    T *y = (T *)a.out + r * a.D + lane * VW;
+    const int ph = FIT == kShifted ? (int)(r * a.D % VW) : 0;
+    bool live[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) live[v] = FIT == kFull || (v * team + lane) * VW - ph < a.D;
+    const T *next = (const T *)a.x + r * a.D - ph + lane * VW;
+    T *y = (T *)a.out + r * a.D - ph + lane * VW;
     const int64_t step_d = step * a.D;
     auto load = [&](int stage, bool in) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) ring.load(stage, 0, v, next + v * team * VW, in && live[v]);
+        for (int v = 0; v < NV; ++v)
+            if constexpr (FIT == kShifted)
+                ring.load_some(stage, 0, v, next + v * team * VW, in ? a.D + ph - (v * team + lane) * VW : 0);
+            else
+                ring.load(stage, 0, v, next + v * team * VW, in && live[v]);
         commit_copies();
         next += step_d;
     };
 #pragma unroll
     for (int k = 0; k < kStages; ++k) load(k, r + k * step < a.rows);
     Pair w[NP], b[NP];
+    uint32_t dead = 0;   // kShifted: the elements that are not the row's
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         float wv[2], bv[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int v = (2 * i + k) / VW, c = (v * team + lane) * VW + (2 * i + k) % VW;
-            wv[k] = live[v] && a.weight ? a.weight[c] : 1.f;
-            bv[k] = live[v] && a.bias ? a.bias[c] : 0.f;
+            const int v = (2 * i + k) / VW, c = (v * team + lane) * VW - ph + (2 * i + k) % VW;
+            const bool is = live[v] && (FIT != kShifted || (c >= 0 && c < a.D));
+            wv[k] = is && a.weight ? a.weight[c] : 1.f;
+            bv[k] = is && a.bias ? a.bias[c] : 0.f;
+            if (FIT == kShifted && !is) dead |= 1u << (2 * i + k);
         }
         w[i] = pair(wv[0], wv[1]);
         b[i] = pair(bv[0], bv[1]);
@@ -243,6 +287,7 @@ rows_fwd_kernel(const LayerNormArgs a, int team)
         Raw<T, VW> raw[NV];
         wait_copies<kStages - 1>();
         ring.read(stage, 0, raw);
+        if (FIT == kShifted && lane == 0) raw[0].drop(ph);
         Pair x[NP], p = 0, q = 0;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -257,15 +302,23 @@ rows_fwd_kernel(const LayerNormArgs a, int team)
         const float mean = s[0] * inv;
         p = q = 0;
 #pragma unroll
+        for (int i = 0; i < NP; ++i) x[i] = add2(x[i], both(-mean));
+        if (FIT == kShifted && dead)
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                float lo, hi;
+                split(x[i], lo, hi);
+                x[i] = pair(dead >> (2 * i) & 1 ? 0.f : lo, dead >> (2 * i + 1) & 1 ? 0.f : hi);
+            }
+#pragma unroll
         for (int i = 0; i < NP; ++i) {
-            x[i] = add2(x[i], both(-mean));
             if constexpr (VW == 1) {   // columns behind D take no part
                 if (!live[2 * i + 1]) {
                     float lo, hi;
                     split(x[i], lo, hi);
                     x[i] = pair(live[2 * i] ? lo : 0.f, 0.f);
                 }
-            } else {
+            } else if constexpr (FIT != kShifted) {
                 if (!live[2 * i / VW]) x[i] = 0;
             }
             if (i & 1) q = fma2(x[i], x[i], q);
@@ -278,8 +331,13 @@ rows_fwd_kernel(const LayerNormArgs a, int team)
 #pragma unroll
             for (int i = 0; i < NP; ++i) x[i] = fma2(mul2(x[i], both(rstd)), w[i], b[i]);
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-                if (live[v]) put<T, VW>(y + v * team * VW, x, v);
+            for (int v = 0; v < NV; ++v) {
+                const int c = (v * team + lane) * VW - ph;
+                if (FIT == kShifted && live[v] && (c < 0 || c + VW > a.D))
+                    put_some<T, VW>(y + v * team * VW, x, v, c, a.D);
+                else if (live[v])
+                    put<T, VW>(y + v * team * VW, x, v);
+            }
             if (lane == 0) {
                 if (a.mean) a.mean[r] = mean;
                 if (a.rstd) a.rstd[r] = rstd;
@@ -289,7 +347,7 @@ rows_fwd_kernel(const LayerNormArgs a, int team)
     wait_copies<0>();
 }
 
-template <typename T, int VW, int NV, int TEAM, int MAX, bool FULL>
+template <typename T, int VW, int NV, int TEAM, int MAX, int FIT>
 __global__ void __launch_bounds__(MAX, MAX == 512 && NV * VW <= 8 ? 2 : 1) rows_bwd_kernel(const LayerNormArgs a, int team)
 {
     extern __shared__ __align__(16) unsigned char smem[];   // the ring; at the end the sums
@@ -303,18 +361,26 @@ __global__ void __launch_bounds__(MAX, MAX == 512 && NV * VW <= 8 ? 2 : 1) rows_
     const int lane = threadIdx.x % team, teams = blockDim.x / team;
     const int64_t step = (int64_t)gridDim.x * teams;
     const float inv = 1.f / (float)a.D;
+    int64_t r = (int64_t)blockIdx.x * teams + threadIdx.x / team;
+    const int ph = FIT == kShifted ? (int)(r * a.D % VW) : 0;
     bool live[NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) live[v] = FULL || (v * team + lane) * VW < a.D;
-    int64_t r = (int64_t)blockIdx.x * teams + threadIdx.x / team;
-    int64_t at = r * a.D + lane * VW;
+    for (int v = 0; v < NV; ++v) live[v] = FIT == kFull || (v * team + lane) * VW - ph < a.D;
+    int64_t at = r * a.D - ph + lane * VW;
     T *dx = (T *)a.dx + at;
     const int64_t step_d = step * a.D;
     auto load = [&](int stage, bool in) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            ring.load(stage, 0, v, (const T *)a.x + at + v * team * VW, in && live[v]);
-            ring.load(stage, 1, v, (const T *)a.dout + at + v * team * VW, in && live[v]);
+            const T *x = (const T *)a.x + at + v * team * VW, *dy = (const T *)a.dout + at + v * team * VW;
+            if constexpr (FIT == kShifted) {
+                const int left = in ? a.D + ph - (v * team + lane) * VW : 0;
+                ring.load_some(stage, 0, v, x, left);
+                ring.load_some(stage, 1, v, dy, left);
+            } else {
+                ring.load(stage, 0, v, x, in && live[v]);
+                ring.load(stage, 1, v, dy, in && live[v]);
+            }
         }
         commit_copies();
         at += step_d;
@@ -332,8 +398,9 @@ __global__ void __launch_bounds__(MAX, MAX == 512 && NV * VW <= 8 ? 2 : 1) rows_
         float wv[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int v = (2 * i + k) / VW, c = (v * team + lane) * VW + (2 * i + k) % VW;
-            wv[k] = live[v] && a.weight ? a.weight[c] : 1.f;
+            const int v = (2 * i + k) / VW, c = (v * team + lane) * VW - ph + (2 * i + k) % VW;
+            const bool is = live[v] && (FIT != kShifted || (c >= 0 && c < a.D));
+            wv[k] = is && a.weight ? a.weight[c] : 1.f;
         }
         w[i] = pair(wv[0], wv[1]);
         dw[i] = db[i] = 0;
@@ -348,6 +415,10 @@ __global__ void __launch_bounds__(MAX, MAX == 512 && NV * VW <= 8 ? 2 : 1) rows_
         wait_copies<kStages - 1>();
         ring.read(stage, 0, rx);
         ring.read(stage, 1, rd);
+        if (FIT == kShifted && lane == 0) {
+            rx[0].drop(ph);
+            rd[0].drop(ph);
+        }
         Pair xh[NP], u[NP], p = 0, q = 0;
         // columns behind D: dy = 0, so u, its sums and the gradients' stay 0
 #pragma unroll
@@ -370,30 +441,35 @@ __global__ void __launch_bounds__(MAX, MAX == 512 && NV * VW <= 8 ? 2 : 1) rows_
             for (int i = 0; i < NP; ++i)
                 u[i] = mul2(both(rstd), add2(u[i], fma2(xh[i], both(-c2), both(-c1))));
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-                if (live[v]) put<T, VW>(dx + v * team * VW, u, v);
+            for (int v = 0; v < NV; ++v) {
+                const int c = (v * team + lane) * VW - ph;
+                if (FIT == kShifted && live[v] && (c < 0 || c + VW > a.D))
+                    put_some<T, VW>(dx + v * team * VW, u, v, c, a.D);
+                else if (live[v])
+                    put<T, VW>(dx + v * team * VW, u, v);
+            }
         }
     }
-    // the CTA's teams: those of a warp by shuffles, then one row [dw | db] a warp or team in shared memory, in order
+    // the CTA's teams: those of a warp by shuffles, where they have the same columns, then one row [dw | db] a warp or team in shared memory, in order
     wait_copies<0>();
     if (!a.dweight && !a.dbias) return;
     __syncthreads();
     float *joined = reinterpret_cast<float *>(smem);
-    const int own = TEAM && TEAM < 32 ? 32 : team, rows = blockDim.x / own;
+    const int own = FIT != kShifted && TEAM && TEAM < 32 ? 32 : team, rows = blockDim.x / own;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         float g[4];
         split(dw[i], g[0], g[1]);
         split(db[i], g[2], g[3]);
 #pragma unroll
-        for (int o = TEAM ? TEAM : 32; o < 32; o *= 2)
+        for (int o = FIT != kShifted && TEAM ? TEAM : 32; o < 32; o *= 2)
 #pragma unroll
             for (int k = 0; k < 4; ++k) g[k] += __shfl_xor_sync(0xffffffffu, g[k], o);
         if (threadIdx.x % own == lane)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int v = (2 * i + (k & 1)) / VW, c = (v * team + lane) * VW + (2 * i + (k & 1)) % VW;
-                if (live[v]) joined[((threadIdx.x / own) * 2 + (k >> 1)) * a.D + c] = g[k];
+                const int v = (2 * i + (k & 1)) / VW, c = (v * team + lane) * VW - ph + (2 * i + (k & 1)) % VW;
+                if (live[v] && (FIT != kShifted || (c >= 0 && c < a.D))) joined[((threadIdx.x / own) * 2 + (k >> 1)) * a.D + c] = g[k];
             }
     }
     __syncthreads();
@@ -537,18 +613,18 @@ Shape shape(int D, int vw, int few, int many)
     return {0, 0};
 }
 
-template <typename T, int VW, int NV, int TEAM, int MAX, bool FULL>
+template <typename T, int VW, int NV, int TEAM, int MAX, int FIT>
 cudaError_t run_fwd(const LayerNormArgs &a, int team, cudaStream_t st)
 {
     const int threads = team > 256 ? team : 256, smem = Ring<T, VW, NV, 1, MAX>::bytes(threads);
     const int64_t ctas = (a.rows + threads / team - 1) / (threads / team);
     const int most = kSMs * (threads > 256 ? 1 : NV * VW <= 8 ? 4 : NV * VW <= 16 ? 3 : 2);
     if (smem > 32 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(rows_fwd_kernel<T, VW, NV, TEAM, MAX, FULL>,
+        const cudaError_t e = cudaFuncSetAttribute(rows_fwd_kernel<T, VW, NV, TEAM, MAX, FIT>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    rows_fwd_kernel<T, VW, NV, TEAM, MAX, FULL><<<(unsigned)(ctas < most ? ctas : most), threads, smem, st>>>(a, team);
+    rows_fwd_kernel<T, VW, NV, TEAM, MAX, FIT><<<(unsigned)(ctas < most ? ctas : most), threads, smem, st>>>(a, team);
     return cudaGetLastError();
 }
 
@@ -569,35 +645,36 @@ cudaError_t launch_join(const LayerNormArgs &a, int parts, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, join_kernel, a, parts);
 }
 
-template <typename T, int VW, int NV, int TEAM, int MAX, bool FULL>
+template <typename T, int VW, int NV, int TEAM, int MAX, int FIT>
 cudaError_t run_bwd(const LayerNormArgs &a, int team, cudaStream_t st)
 {
     const int threads = team > MAX ? team : MAX;
     const int64_t ctas = (a.rows + threads / team - 1) / (threads / team);
     const int most = bwd_ctas(a.D), grid = (int)(ctas < most ? (ctas > 0 ? ctas : 1) : most);
     const bool sums = a.dweight || a.dbias;
-    const int own = team < 32 ? 32 : team, joined = sums ? threads / own * 2 * a.D * 4 : 0;
+    const int own = FIT != kShifted && team < 32 ? 32 : team, joined = sums ? threads / own * 2 * a.D * 4 : 0;
     const int ring = Ring<T, VW, NV, 2, MAX>::bytes(threads), smem = joined > ring ? joined : ring;
     if (smem > 32 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(rows_bwd_kernel<T, VW, NV, TEAM, MAX, FULL>,
+        const cudaError_t e = cudaFuncSetAttribute(rows_bwd_kernel<T, VW, NV, TEAM, MAX, FIT>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    rows_bwd_kernel<T, VW, NV, TEAM, MAX, FULL><<<grid, threads, smem, st>>>(a, team);
+    rows_bwd_kernel<T, VW, NV, TEAM, MAX, FIT><<<grid, threads, smem, st>>>(a, team);
     const cudaError_t e = cudaGetLastError();
     return e != cudaSuccess || !sums ? e : launch_join(a, grid, st);
 }
 
-template <typename T, int VW, bool BWD>
+template <typename T, int VW, bool BWD, bool SHIFTED>
 cudaError_t run(const LayerNormArgs &a, cudaStream_t st)
 {
     constexpr int few = VW == 1 ? 4 : 8 / VW, many = VW == 1 ? 16 : (BWD ? 16 : 32) / VW;
-    const Shape s = shape(a.D, VW, few, many);
-    const bool full = VW > 1 && a.D == s.team * VW * (s.wide ? many : few);
-#define GDN_NORM1(NV, TEAM, MAX, FULL) \
-    (BWD ? run_bwd<T, VW, NV, TEAM, MAX, FULL>(a, s.team, st) : run_fwd<T, VW, NV, TEAM, MAX, FULL>(a, s.team, st))
+    const Shape s = shape(SHIFTED ? a.D + VW - 1 : a.D, VW, few, many);
+    const bool full = !SHIFTED && VW > 1 && a.D == s.team * VW * (s.wide ? many : few);
+#define GDN_NORM1(NV, TEAM, MAX, FIT) \
+    (BWD ? run_bwd<T, VW, NV, TEAM, MAX, FIT>(a, s.team, st) : run_fwd<T, VW, NV, TEAM, MAX, FIT>(a, s.team, st))
 #define GDN_NORM(NV, TEAM, FMAX, BMAX) \
-    (full ? GDN_NORM1(NV, TEAM, (BWD ? BMAX : FMAX), (VW > 1)) : GDN_NORM1(NV, TEAM, (BWD ? BMAX : FMAX), false))
+    (full ? GDN_NORM1(NV, TEAM, (BWD ? BMAX : FMAX), (SHIFTED ? kShifted : VW > 1 ? kFull : kPartial)) \
+          : GDN_NORM1(NV, TEAM, (BWD ? BMAX : FMAX), (SHIFTED ? kShifted : kPartial)))
     if (s.team == 8) return GDN_NORM(few, 8, 256, 512);
     if (s.team == 16) return GDN_NORM(few, 16, 256, 512);
     if (s.team == 32) return s.wide ? GDN_NORM(many, 32, 256, 512) : GDN_NORM(few, 32, 256, 512);
@@ -607,22 +684,16 @@ cudaError_t run(const LayerNormArgs &a, cudaStream_t st)
 #undef GDN_NORM1
 }
 
-// Bytes of an access that every row's start fits.
-int access_of(const LayerNormArgs &a)
-{
-    const uintptr_t all = (uintptr_t)a.x | (uintptr_t)a.out | (uintptr_t)a.dout | (uintptr_t)a.dx |
-                          (uintptr_t)a.D * (a.dt ? 2 : 4);
-    return (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 2;
-}
-
 template <typename T, bool BWD>
 cudaError_t run_rows(const LayerNormArgs &a, cudaStream_t st)
 {
-    const int access = access_of(a);
-    if (access == 16) return run<T, 16 / sizeof(T), BWD>(a, st);
+    constexpr int VW = 16 / sizeof(T);
+    const uintptr_t starts = (uintptr_t)a.x | (uintptr_t)a.out | (uintptr_t)a.dout | (uintptr_t)a.dx;
+    if ((starts & 15) == 0 && a.D % VW == 0) return run<T, VW, BWD, false>(a, st);
+    if ((starts & 15) == 0 && a.D + VW - 1 <= kMost) return run<T, VW, BWD, true>(a, st);
     if constexpr (sizeof(T) == 2)
-        if (access == 4) return run<T, 2, BWD>(a, st);
-    return run<T, 1, BWD>(a, st);
+        if ((starts & 3) == 0 && a.D % 2 == 0) return run<T, 2, BWD, false>(a, st);
+    return run<T, 1, BWD, false>(a, st);
 }
 
 template <typename T>

@@ -48,6 +48,31 @@ def test_norm_against_the_definition(rows, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,D", [(40001, 3), (21003, 9), (21003, 57), (11001, 121), (5003, 249), (5003, 251),
+                                    (5003, 254), (3001, 505), (1501, 1013), (700, 2049), (311, 4093), (309, 8187),
+                                    (157, 16377), (3, 16379), (2, 16383)])
+def test_rows_that_start_anywhere(rows, D, dtype):
+    """Several rows a thread where rows start at every place of a 16-byte chunk, and at the edges of the teams."""
+    run_and_check(*make(rows, D, dtype, seed=rows + D))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_neighbours_in_a_chunk_do_not_mix(dtype):
+    """Rows of an odd length share their first and last 16 bytes with other rows; out may be x."""
+    x, w, b, dy = make(60, 509, dtype, seed=9)
+    y0, m0, r0 = gdn.layer_norm_fwd(x, w, b)
+    dx0, _, _ = gdn.layer_norm_bwd(dy, x, m0, r0, w)
+    z = x.clone()
+    gdn.layer_norm_fwd(z, w, b, out=z)
+    assert torch.equal(z, y0)
+    x[1::2], dy[1::2] = float("nan"), float("inf")
+    y, m, r = gdn.layer_norm_fwd(x, w, b)
+    dx, _, _ = gdn.layer_norm_bwd(dy, x, m, r, w)
+    assert torch.equal(y[::2], y0[::2]) and torch.equal(dx[::2], dx0[::2])
+    assert torch.isnan(y[1::2]).all() and torch.isnan(dx[1::2]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,D", [(20, 96), (20, 1000), (4, 9000)])
 def test_without_weight_or_bias(rows, D, dtype):
     x, _, b, dy = make(rows, D, dtype, seed=1)
