@@ -11,7 +11,7 @@
 // copies: 32 KB of them in flight on an SM, as registers one row ahead allow, held the backward pass to 3.9 TB/s and
 // the norm over heads (131072 x 128) to 2.6.  Rows of more than 16384 elements go through kernels that read them again.
 // Rows of other lengths than 16-byte accesses fit go by the 16-byte chunks that they lie in (48841 x 687 bf16: forward
-// 42 us, backward 53 us; element by element 93 and 173), unless their tensors start elsewhere.
+// 41 us, backward 54 us; element by element 93 and 173), unless their tensors start elsewhere.
 //
 // Measured (GB300, bf16, device time): forward 8192 x 2048 15.1 us (4.4 TB/s); backward 25.2 us, 131072 x 128 backward
 // 24.0 us (4.0 and 4.2 TB/s), of which about 3 us are the second kernel and the gap before it.
@@ -57,7 +57,8 @@ struct Ring {
     static constexpr int kFit = 128 * 1024 / (TENSORS * NV * kBytes * (MAX < 512 ? 512 : MAX));
     static constexpr int kStages = kFit >= 4 ? 4 : kFit >= 2 ? 2 : 1;
     uint32_t base;
-    static __host__ __device__ int bytes(int threads) { return kStages * TENSORS * NV * kBytes * threads; }
+    static __host__ __device__ int stage_bytes(int threads) { return TENSORS * NV * kBytes * threads; }
+    static __host__ __device__ int bytes(int threads) { return kStages * stage_bytes(threads); }
     __device__ __forceinline__ explicit Ring(const void *smem)
         : base(static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * kBytes) {}
     __device__ __forceinline__ uint32_t slot(int stage, int tensor, int v) const
@@ -84,16 +85,18 @@ struct Ring {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                      :: "r"(slot(stage, tensor, v)), "l"(p), "r"(bytes) : "memory");
     }
-    __device__ __forceinline__ void read(int stage, int tensor, Raw<T, VW> (&r)[NV]) const
+    template <int N>
+    __device__ __forceinline__ void read(int stage, int tensor, Raw<T, VW> (&r)[N], int from = 0) const
     {
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < N; ++v)
             if constexpr (kBytes == 16)
                 asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(r[v].w[0]), "=r"(r[v].w[1]), "=r"(r[v].w[2]), "=r"(r[v].w[3])
-                             : "r"(slot(stage, tensor, v)) : "memory");
+                             : "r"(slot(stage, tensor, from + v)) : "memory");
             else
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[v].w[0]) : "r"(slot(stage, tensor, v)) : "memory");
+                asm volatile("ld.shared.b32 %0, [%1];"
+                             : "=r"(r[v].w[0]) : "r"(slot(stage, tensor, from + v)) : "memory");
     }
 };
 
@@ -164,15 +167,19 @@ __device__ __forceinline__ float total(Pair p)
 template <int TEAM, int N>
 struct TeamSum {
     float *mine, *all;   // where the warp's sums go, where the team's start
-    int size, warps, barrier, other;
-    __device__ __forceinline__ TeamSum(float *sh, int team_size)   // sh: [2][N][warps of the CTA]
+    int size, barrier, other;
+    __device__ __forceinline__ TeamSum(float *sh, int team_size)   // sh: [2][N][32], a team's part in whole float4s
     {
         size = team_size;
-        warps = team_size / 32;
-        barrier = 1 + threadIdx.x / team_size;
-        mine = sh + (threadIdx.x >> 5);
-        all = sh + (threadIdx.x / team_size) * warps;
-        other = N * (blockDim.x >> 5);      // by turns, so that one barrier a sum is enough
+        const int team = threadIdx.x / team_size;
+        barrier = 1 + team;
+        all = sh + team * ((team_size + 127) / 128 * 4);
+        mine = all + threadIdx.x % team_size / 32;
+        other = N * 32;      // by turns, so that one barrier a sum is enough
+        if constexpr (TEAM == 0) {
+            for (int i = threadIdx.x; i < 2 * N * 32; i += blockDim.x) sh[i] = 0.f;
+            __syncthreads();
+        }
     }
     __device__ __forceinline__ void operator()(float (&v)[N])
     {
@@ -181,24 +188,24 @@ struct TeamSum {
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
         if constexpr (TEAM == 0) {
-            const int row = blockDim.x >> 5;
             if ((threadIdx.x & 31) == 0)
 #pragma unroll
-                for (int i = 0; i < N; ++i) mine[i * row] = v[i];
+                for (int i = 0; i < N; ++i) mine[i * 32] = v[i];
             asm volatile("bar.sync %0, %1;" :: "r"(barrier), "r"(size) : "memory");
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = 0.f;
-            if (warps == 2) {
+            if (size == 64) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const float2 p = *reinterpret_cast<const float2 *>(all + i * row);
+                    const float2 p = *reinterpret_cast<const float2 *>(all + i * 32);
                     v[i] = p.x + p.y;
                 }
             } else {
-                for (int w = 0; w < warps; w += 4)
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = 0.f;
+#pragma unroll 1   // unrolled, it makes the backward kernels spill (8192 x 2048 bf16 28 us)
+                for (int w = 0; 32 * w < size; w += 4)
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        const float4 p = *reinterpret_cast<const float4 *>(all + i * row + w);
+                        const float4 p = *reinterpret_cast<const float4 *>(all + i * 32 + w);
                         v[i] += (p.x + p.y) + (p.z + p.w);
                     }
             }
@@ -347,13 +354,23 @@ rows_fwd_kernel(const LayerNormArgs a, int team)
     wait_copies<0>();
 }
 
+// Stages of the backward kernel's ring for teams of more than 512 threads, 16 elements each: what fits beside the weight.
+__host__ __device__ constexpr int again_stages(int stage_bytes, int threads)
+{
+    return 2 * stage_bytes + 64 * threads <= 226 * 1024 ? 2 : 1;
+}
+
 template <typename T, int VW, int NV, int TEAM, int MAX, int FIT>
 __global__ void __launch_bounds__(MAX, MAX == 512 && NV * VW <= 8 ? 2 : 1) rows_bwd_kernel(const LayerNormArgs a, int team)
 {
     extern __shared__ __align__(16) unsigned char smem[];   // the ring; at the end the sums
     __shared__ __align__(16) float sh[2 * 32 * 2];
     using Rows = Ring<T, VW, NV, 2, MAX>;
-    constexpr int kStages = Rows::kStages;
+    // Teams of more than 512 threads have 64 registers each.  They read a row from the ring again behind its sums, and
+    // the weight from shared memory, instead of keeping both (3581 x 9368 bf16: 76 us, 118 with
+    // them spilled).
+    constexpr bool kAgain = MAX == 1024;
+    const int stages = kAgain ? again_stages(Rows::stage_bytes(blockDim.x), blockDim.x) : Rows::kStages;
     const Rows ring(smem);
     if (TEAM) team = TEAM;
     TeamSum<TEAM, 2> sum(sh, team);
@@ -391,8 +408,9 @@ __global__ void __launch_bounds__(MAX, MAX == 512 && NV * VW <= 8 ? 2 : 1) rows_
     stat[0] = load_stat(r);
     stat[1] = load_stat(r + step);
 #pragma unroll
-    for (int k = 0; k < kStages; ++k) load(k, r + k * step < a.rows);
-    Pair w[NP], dw[NP], db[NP];
+    for (int k = 0; k < stages; ++k) load(k, r + k * step < a.rows);
+    Pair w[kAgain ? 1 : NP], dw[NP], db[NP];
+    Pair *w_row = reinterpret_cast<Pair *>(smem + stages * Rows::stage_bytes(blockDim.x)) + threadIdx.x;   // kAgain
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         float wv[2];
@@ -402,53 +420,72 @@ __global__ void __launch_bounds__(MAX, MAX == 512 && NV * VW <= 8 ? 2 : 1) rows_
             const bool is = live[v] && (FIT != kShifted || (c >= 0 && c < a.D));
             wv[k] = is && a.weight ? a.weight[c] : 1.f;
         }
-        w[i] = pair(wv[0], wv[1]);
+        if constexpr (kAgain) w_row[i * blockDim.x] = pair(wv[0], wv[1]);
+        else w[i] = pair(wv[0], wv[1]);
         dw[i] = db[i] = 0;
     }
-    const int64_t rows_ahead = a.rows - kStages * step;
+    const int64_t rows_ahead = a.rows - stages * step;
     int stage = 0;
     for (int64_t first = (int64_t)blockIdx.x * teams; first < a.rows; first += step, r += step, dx += step_d) {
         const float mean = stat[0].x, rstd = stat[0].y;
         stat[0] = stat[1];
         stat[1] = load_stat(r + 2 * step);
-        Raw<T, VW> rx[NV], rd[NV];
-        wait_copies<kStages - 1>();
-        ring.read(stage, 0, rx);
-        ring.read(stage, 1, rd);
-        if (FIT == kShifted && lane == 0) {
-            rx[0].drop(ph);
-            rd[0].drop(ph);
-        }
-        Pair xh[NP], u[NP], p = 0, q = 0;
-        // columns behind D: dy = 0, so u, its sums and the gradients' stay 0
+        // pairs of the accesses v to v + A - 1: x^ and u, with dy where the gradients' sums take it
+        constexpr int A = kAgain ? (VW == 1 ? 2 : 1) : NV, P = A * VW / 2;
+        Pair xh[P], u[P], p = 0, q = 0;
+        auto take = [&](int v, bool sums) {
+            Raw<T, VW> rx[A], rd[A];
+            ring.read(stage, 0, rx, v);
+            ring.read(stage, 1, rd, v);
+            if (FIT == kShifted && lane == 0 && v == 0) {
+                rx[0].drop(ph);
+                rd[0].drop(ph);
+            }
+            // columns behind D: dy = 0, so u, its sums and the gradients' stay 0
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const Pair dy = get_pair<T, VW, NV>(rd, i);
-            xh[i] = mul2(add2(get_pair<T, VW, NV>(rx, i), both(-mean)), both(rstd));
-            u[i] = mul2(dy, w[i]);
-            p = add2(p, u[i]);
-            q = fma2(u[i], xh[i], q);
-            dw[i] = fma2(dy, xh[i], dw[i]);
-            db[i] = add2(db[i], dy);
-        }
-        load(stage, r < rows_ahead);
-        stage = (stage + 1) & (kStages - 1);
+            for (int i = 0; i < P; ++i) {
+                const int k = v * VW / 2 + i;
+                const Pair dy = get_pair<T, VW, A>(rd, i);
+                xh[i] = mul2(add2(get_pair<T, VW, A>(rx, i), both(-mean)), both(rstd));
+                if constexpr (kAgain) u[i] = mul2(dy, w_row[k * blockDim.x]);
+                else u[i] = mul2(dy, w[k]);
+                if (sums) {
+                    p = add2(p, u[i]);
+                    q = fma2(u[i], xh[i], q);
+                    dw[k] = fma2(dy, xh[i], dw[k]);
+                    db[k] = add2(db[k], dy);
+                }
+            }
+        };
+        if constexpr (!kAgain) wait_copies<Rows::kStages - 1>();
+        else if (stages == 2) wait_copies<1>();
+        else wait_copies<0>();
+#pragma unroll
+        for (int v = 0; v < NV; v += A) take(v, true);
+        if (!kAgain) load(stage, r < rows_ahead);
         float s[2] = {total(p), total(q)};
         sum(s);
         const float c1 = s[0] * inv, c2 = s[1] * inv;
-        if (a.dx && r < a.rows) {
+        const bool write = a.dx && r < a.rows;
+        if (kAgain || write) {
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
-                u[i] = mul2(both(rstd), add2(u[i], fma2(xh[i], both(-c2), both(-c1))));
+            for (int v0 = 0; v0 < NV; v0 += A) {
+                if constexpr (kAgain) take(v0, false);
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int c = (v * team + lane) * VW - ph;
-                if (FIT == kShifted && live[v] && (c < 0 || c + VW > a.D))
-                    put_some<T, VW>(dx + v * team * VW, u, v, c, a.D);
-                else if (live[v])
-                    put<T, VW>(dx + v * team * VW, u, v);
+                for (int i = 0; i < P; ++i)
+                    u[i] = mul2(both(rstd), add2(u[i], fma2(xh[i], both(-c2), both(-c1))));
+#pragma unroll
+                for (int v = 0; v < A; ++v) {
+                    const int c = ((v0 + v) * team + lane) * VW - ph;
+                    T *to = dx + (v0 + v) * team * VW;
+                    if (!write || !live[v0 + v]) continue;
+                    if (FIT == kShifted && (c < 0 || c + VW > a.D)) put_some<T, VW>(to, u, v, c, a.D);
+                    else put<T, VW>(to, u, v);
+                }
             }
         }
+        if (kAgain) load(stage, r < rows_ahead);
+        stage = (stage + 1) & (stages - 1);
     }
     // the CTA's teams: those of a warp by shuffles, where they have the same columns, then one row [dw | db] a warp or team in shared memory, in order
     wait_copies<0>();
@@ -599,8 +636,9 @@ constexpr int kMost = 16384;   // elements of a row that 1024 threads hold
 
 struct Shape { int team, wide; };   // threads a row; whether a thread takes 16 elements or fewer
 
-// The smallest team, a power of two from 8 to 1024, whose threads can take the row at `many` accesses each; a part of
-// a warp, or a warp, at `few` where that is enough.  8192 x 2048 bf16: forward 32 elements a thread 14.8 us, 16
+// The smallest team, whole warps up to 1024 threads, that can take the row at `many` accesses a thread; a part of a
+// warp, or a warp, at `few` where that is enough.  (Teams of powers of two alone: 8192 x 2049 bf16 35 and 39.6 us,
+// these 28 and 29.8.)  8192 x 2048 bf16: forward 32 elements a thread 14.8 us, 16
 // elements 15.5, 8 elements 19.8; backward, whose dw and db take twice as many registers, 16 elements 25.2 us,
 // 8 elements 29.4, 32 elements (spilling) 51.
 Shape shape(int D, int vw, int few, int many)
@@ -608,17 +646,16 @@ Shape shape(int D, int vw, int few, int many)
     const int nvec = ceil_div(D, vw);
     for (int g = 8; g <= 32; g *= 2)
         if (nvec <= g * few) return {g, 0};
-    for (int g = 32; g <= 1024; g *= 2)
-        if (nvec <= g * many) return {g, 1};
-    return {0, 0};
+    return {ceil_div(ceil_div(nvec, many), 32) * 32, 1};
 }
 
 template <typename T, int VW, int NV, int TEAM, int MAX, int FIT>
 cudaError_t run_fwd(const LayerNormArgs &a, int team, cudaStream_t st)
 {
-    const int threads = team > 256 ? team : 256, smem = Ring<T, VW, NV, 1, MAX>::bytes(threads);
+    // a team of several warps is a CTA of its own
+    const int threads = team > 256 ? team : 256 / team * team, smem = Ring<T, VW, NV, 1, MAX>::bytes(threads);
     const int64_t ctas = (a.rows + threads / team - 1) / (threads / team);
-    const int most = kSMs * (threads > 256 ? 1 : NV * VW <= 8 ? 4 : NV * VW <= 16 ? 3 : 2);
+    const int most = kSMs * (threads > 256 ? 1 : (NV * VW <= 8 ? 4 : NV * VW <= 16 ? 3 : 2) * 256 / threads);
     if (smem > 32 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(rows_fwd_kernel<T, VW, NV, TEAM, MAX, FIT>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -648,12 +685,14 @@ cudaError_t launch_join(const LayerNormArgs &a, int parts, cudaStream_t st)
 template <typename T, int VW, int NV, int TEAM, int MAX, int FIT>
 cudaError_t run_bwd(const LayerNormArgs &a, int team, cudaStream_t st)
 {
-    const int threads = team > MAX ? team : MAX;
+    const int threads = MAX / team * team;
     const int64_t ctas = (a.rows + threads / team - 1) / (threads / team);
     const int most = bwd_ctas(a.D), grid = (int)(ctas < most ? (ctas > 0 ? ctas : 1) : most);
     const bool sums = a.dweight || a.dbias;
     const int own = FIT != kShifted && team < 32 ? 32 : team, joined = sums ? threads / own * 2 * a.D * 4 : 0;
-    const int ring = Ring<T, VW, NV, 2, MAX>::bytes(threads), smem = joined > ring ? joined : ring;
+    using Rows = Ring<T, VW, NV, 2, MAX>;
+    const int stage = Rows::stage_bytes(threads);
+    const int ring = MAX == 1024 ? again_stages(stage, threads) * stage + 64 * threads : Rows::bytes(threads), smem = joined > ring ? joined : ring;
     if (smem > 32 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(rows_bwd_kernel<T, VW, NV, TEAM, MAX, FIT>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -670,16 +709,24 @@ cudaError_t run(const LayerNormArgs &a, cudaStream_t st)
     constexpr int few = VW == 1 ? 4 : 8 / VW, many = VW == 1 ? 16 : (BWD ? 16 : 32) / VW;
     const Shape s = shape(SHIFTED ? a.D + VW - 1 : a.D, VW, few, many);
     const bool full = !SHIFTED && VW > 1 && a.D == s.team * VW * (s.wide ? many : few);
-#define GDN_NORM1(NV, TEAM, MAX, FIT) \
-    (BWD ? run_bwd<T, VW, NV, TEAM, MAX, FIT>(a, s.team, st) : run_fwd<T, VW, NV, TEAM, MAX, FIT>(a, s.team, st))
+#define GDN_NORM1(NV, TEAM, FMAX, BMAX, FIT) \
+    if constexpr (BWD) return run_bwd<T, VW, NV, TEAM, BMAX, FIT>(a, s.team, st); \
+    else return run_fwd<T, VW, NV, TEAM, FMAX, FIT>(a, s.team, st)
 #define GDN_NORM(NV, TEAM, FMAX, BMAX) \
-    (full ? GDN_NORM1(NV, TEAM, (BWD ? BMAX : FMAX), (SHIFTED ? kShifted : VW > 1 ? kFull : kPartial)) \
-          : GDN_NORM1(NV, TEAM, (BWD ? BMAX : FMAX), (SHIFTED ? kShifted : kPartial)))
-    if (s.team == 8) return GDN_NORM(few, 8, 256, 512);
-    if (s.team == 16) return GDN_NORM(few, 16, 256, 512);
-    if (s.team == 32) return s.wide ? GDN_NORM(many, 32, 256, 512) : GDN_NORM(few, 32, 256, 512);
-    if (s.team == 1024) return GDN_NORM(many, 0, 1024, 1024);
-    return s.team <= 256 ? GDN_NORM(many, 0, 256, 512) : GDN_NORM(many, 0, 512, 512);
+    do { \
+        if constexpr (SHIFTED) { GDN_NORM1(NV, TEAM, FMAX, BMAX, kShifted); } \
+        if constexpr (VW > 1 && !SHIFTED) \
+            if (full) { GDN_NORM1(NV, TEAM, FMAX, BMAX, kFull); } \
+        if constexpr (!SHIFTED) { GDN_NORM1(NV, TEAM, FMAX, BMAX, kPartial); } \
+    } while (0)
+    if (s.team == 8) GDN_NORM(few, 8, 256, 512);
+    if (s.team == 16) GDN_NORM(few, 16, 256, 512);
+    if (s.team == 32 && !s.wide) GDN_NORM(few, 32, 256, 512);
+    if (s.team == 32) GDN_NORM(many, 32, 256, 512);
+    if constexpr (!BWD)
+        if (s.team <= 256) GDN_NORM(many, 0, 256, 512);
+    if (s.team <= 512) GDN_NORM(many, 0, 512, 512);
+    GDN_NORM(many, 0, 1024, 1024);
 #undef GDN_NORM
 #undef GDN_NORM1
 }
