@@ -11,7 +11,7 @@
 // copies: 32 KB of them in flight on an SM, as registers one row ahead allow, held the backward pass to 3.9 TB/s and
 // the norm over heads (131072 x 128) to 2.6.  Rows of more than 16384 elements go through kernels that read them again.
 // Rows of other lengths than 16-byte accesses fit go by the 16-byte chunks that they lie in (48841 x 687 bf16: forward
-// 41 us, backward 54 us; element by element 93 and 173), unless their tensors start elsewhere.
+// 32 us, backward 54 us; element by element 93 and 173), unless their tensors start elsewhere.
 //
 // Measured (GB300, bf16, device time): forward 8192 x 2048 15.1 us (4.4 TB/s); backward 25.2 us, 131072 x 128 backward
 // 24.0 us (4.0 and 4.2 TB/s), of which about 3 us are the second kernel and the gap before it.
@@ -634,11 +634,11 @@ __global__ void __launch_bounds__(kThreads) long_dw_kernel(const LayerNormArgs a
 
 constexpr int kMost = 16384;   // elements of a row that 1024 threads hold
 
-struct Shape { int team, wide; };   // threads a row; whether a thread takes 16 elements or fewer
+struct Shape { int team, wide; };   // threads a row; 0: `few` accesses each, 1: `many`, 2: three quarters of many
 
 // The smallest team, whole warps up to 1024 threads, that can take the row at `many` accesses a thread; a part of a
-// warp, or a warp, at `few` where that is enough.  (Teams of powers of two alone: 8192 x 2049 bf16 35 and 39.6 us,
-// these 28 and 29.8.)  8192 x 2048 bf16: forward 32 elements a thread 14.8 us, 16
+// warp, or a warp, at `few` where that is enough.  (Powers of two alone: 8192 x 2049 bf16 35 us forward, 39.6
+// backward; whole warps 28 and 29.8.)  8192 x 2048 bf16: forward 32 elements a thread 14.8 us, 16
 // elements 15.5, 8 elements 19.8; backward, whose dw and db take twice as many registers, 16 elements 25.2 us,
 // 8 elements 29.4, 32 elements (spilling) 51.
 Shape shape(int D, int vw, int few, int many)
@@ -707,8 +707,16 @@ template <typename T, int VW, bool BWD, bool SHIFTED>
 cudaError_t run(const LayerNormArgs &a, cudaStream_t st)
 {
     constexpr int few = VW == 1 ? 4 : 8 / VW, many = VW == 1 ? 16 : (BWD ? 16 : 32) / VW;
-    const Shape s = shape(SHIFTED ? a.D + VW - 1 : a.D, VW, few, many);
-    const bool full = !SHIFTED && VW > 1 && a.D == s.team * VW * (s.wide ? many : few);
+    Shape s = shape(SHIFTED ? a.D + VW - 1 : a.D, VW, few, many);
+    if constexpr (!BWD) {
+        // 24 elements a thread where that leaves fewer threads idle (20000 x 1536 bf16 20 us, 32 elements 24; 8192 x
+        // 2049 21.5 and 28; within 5 % it pays less: 3581 x 9368 35 and 33.5), and for shifted fp32 rows, which spill
+        // with 32, unless many more are idle (8192 x 2047 26 and 42)
+        const Shape t = shape(SHIFTED ? a.D + VW - 1 : a.D, VW, few, many * 3 / 4);
+        const float most = SHIFTED && sizeof(T) == 4 ? 1.25f : 0.95f;
+        if (t.wide && t.team <= 512 && t.team * 3 < most * (s.team * 4)) s = {t.team, 2};
+    }
+    const bool full = !SHIFTED && VW > 1 && a.D == s.team * VW * (s.wide == 2 ? many * 3 / 4 : s.wide ? many : few);
 #define GDN_NORM1(NV, TEAM, FMAX, BMAX, FIT) \
     if constexpr (BWD) return run_bwd<T, VW, NV, TEAM, BMAX, FIT>(a, s.team, st); \
     else return run_fwd<T, VW, NV, TEAM, FMAX, FIT>(a, s.team, st)
@@ -722,11 +730,16 @@ cudaError_t run(const LayerNormArgs &a, cudaStream_t st)
     if (s.team == 8) GDN_NORM(few, 8, 256, 512);
     if (s.team == 16) GDN_NORM(few, 16, 256, 512);
     if (s.team == 32 && !s.wide) GDN_NORM(few, 32, 256, 512);
+    if constexpr (!BWD) {
+        if (s.wide == 2 && s.team == 32) GDN_NORM(many * 3 / 4, 32, 256, 512);
+        if (s.wide == 2 && s.team <= 256) GDN_NORM(many * 3 / 4, 0, 256, 512);
+        if (s.wide == 2) GDN_NORM(many * 3 / 4, 0, 512, 512);
+        if (s.team > 32 && s.team <= 256) GDN_NORM(many, 0, 256, 512);
+    }
     if (s.team == 32) GDN_NORM(many, 32, 256, 512);
-    if constexpr (!BWD)
-        if (s.team <= 256) GDN_NORM(many, 0, 256, 512);
-    if (s.team <= 512) GDN_NORM(many, 0, 512, 512);
-    GDN_NORM(many, 0, 1024, 1024);
+    if constexpr (BWD || VW == 1)
+        if (s.team > 512) GDN_NORM(many, 0, 1024, 1024);
+    GDN_NORM(many, 0, 512, 512);
 #undef GDN_NORM
 #undef GDN_NORM1
 }
