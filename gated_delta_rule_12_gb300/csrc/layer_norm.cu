@@ -771,12 +771,16 @@ cudaError_t bwd(const LayerNormArgs &a, cudaStream_t st)
 {
     if (a.D <= kMost) return run_rows<T, true>(a, st);
     const unsigned blocks = (unsigned)(a.rows < kSMs * 8 ? a.rows : kSMs * 8);
-    if (a.dx && blocks) long_dx_kernel<T><<<blocks, kThreads, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || (!a.dweight && !a.dbias)) return e;
-    long_dw_kernel<T><<<dim3(ceil_div(a.D, kThreads), kRowSplits), kThreads, 0, st>>>(a);
-    e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_join(a, kRowSplits, st);
+    // dx may lie over dout, so the sums over rows read dout first
+    cudaError_t e = cudaSuccess;
+    if (a.dweight || a.dbias) {
+        long_dw_kernel<T><<<dim3(ceil_div(a.D, kThreads), kRowSplits), kThreads, 0, st>>>(a);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = launch_join(a, kRowSplits, st);
+    }
+    if (e != cudaSuccess || !a.dx || !blocks) return e;
+    long_dx_kernel<T><<<blocks, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace

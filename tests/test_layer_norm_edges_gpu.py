@@ -1,0 +1,46 @@
+"""Layer norm where its buffers alias."""
+import pytest
+import torch
+
+import gated_delta_rule_12_gb300 as gdn
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from gated_delta_rule_12_gb300 import build
+    build.build()
+    gdn.load_library()
+
+
+def bwd_into(dx, dy, x, mean, rstd, w):
+    """The C entry with the caller's dx; returns the weight's and bias's gradients."""
+    rows, D = x.shape
+    dt = gdn.GDN_BF16 if x.dtype == torch.bfloat16 else gdn.GDN_F32
+    dw, db = torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    ws = torch.empty(gdn.layer_norm_bwd_workspace_size(rows, D, x.dtype), dtype=torch.uint8, device="cuda")
+    rc = gdn.load_library().gdn_layer_norm_bwd(dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                               w.data_ptr(), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, D, dt,
+                                               ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert rc == gdn.GDN_OK
+    return dw, db
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,D", [(60, 509), (40, 2048), (9, 9000), (70, 20000)])
+def test_dx_in_the_place_of_dout(rows, D, dtype):
+    """The same bits as with a dx of its own, for rows in registers and for longer ones."""
+    gen = torch.Generator().manual_seed(D)
+    x, dy = (torch.randn((rows, D), generator=gen).to(DT[dtype]).cuda() for _ in range(2))
+    w = torch.rand(D, generator=gen).cuda() + 0.5
+    _, mean, rstd = gdn.layer_norm_fwd(x, w)
+    want = gdn.layer_norm_bwd(dy, x, mean, rstd, w)
+    buf = dy.clone()
+    dw, db = bwd_into(buf, buf, x, mean, rstd, w)
+    assert torch.equal(buf, want[0])
+    assert torch.equal(dw, want[1]) and torch.equal(db, want[2])
