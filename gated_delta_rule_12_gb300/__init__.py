@@ -7,6 +7,9 @@ the current PyTorch CUDA stream.  Every step of the computation runs in the
 library's CUDA kernels; there is no other code path.  If ``libgdn.so`` cannot
 be loaded the calls raise: there is no fallback.
 
+Every call enqueues on the current stream, or on ``stream=`` where that is given (a torch stream or
+a raw handle).  The caller then orders the inputs before the call and the use of its results behind it.
+
 Entry points (same names as the C ABI, without the ``gdn_`` prefix):
     chunk_fwd(q, k, v, g, beta, ...)      -> (out, final_state)
     decode_step(state, q, k, v, g, beta)  -> out            (state updated in place)
@@ -424,18 +427,25 @@ _empty, _empty_like = torch.empty, torch.empty_like
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _stream_of(t, stream):
-    return _raw_stream(t.get_device()) if stream is None else getattr(stream, "cuda_stream", stream)
+def _stream_of(t):
+    return _raw_stream(t.get_device())
 
 
-def _made_here(stream, *ts):
-    """Tensors that a wrapper allocated (from the current stream's memory) are used by a kernel on ``stream``: the
-    allocator keeps them until that work is done."""
+def _elsewhere(stream, call, *args):
+    """``call(*args)`` on the stream that the caller names, a torch stream or a raw handle.
+
+    It is the current one meanwhile, so outputs and workspaces come from memory that this stream has done with: memory of
+    the caller's current stream may still be in use by work queued there.  What the call made is used on the caller's
+    stream next; the allocator keeps it until that use is over too."""
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream)
-    for t in ts:
-        if t is not None:
-            t.record_stream(stream)
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        got = call(*args)
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None and all(t is not a for a in args):
+            t.record_stream(here)
+    return got
 
 
 def _check_scan_args(x, g, cu_seqlens, dtype, states, same):
@@ -476,20 +486,20 @@ def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, input_gate=False, out
     x, g [B,T,D] (fp32 or bf16, one dtype); init_state [N,D] fp32 or None; cu_seqlens int32 [N+1] (device) or
     None.  Returns ``(out, final_state)``; final_state is None if not requested.
     """
+    if stream is not None:
+        return _elsewhere(stream, gated_scan_fwd, x, g, init_state, cu_seqlens, input_gate, out, final_state,
+                          output_final_state)
     lib = _lib or load_library()
     B, T, D, N = _check_scan_args(x, g, cu_seqlens, x.dtype, (init_state, final_state), (out,))
-    made = (None if out is not None else 1, None if final_state is not None else 1)
     if out is None:
         out = _empty_like(x)
     if final_state is None and output_final_state:
         final_state = _empty((N, D), dtype=_F32, device=x.device)
     rc = lib.gdn_gated_scan_fwd(x.data_ptr(), g.data_ptr(), _ptr(init_state), _ptr(cu_seqlens),
                                 N if cu_seqlens is not None else 0, out.data_ptr(), _ptr(final_state), B, T, D,
-                                _dt(x), int(bool(input_gate)), _stream_of(g, stream))
+                                _dt(x), int(bool(input_gate)), _stream_of(g))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_gated_scan_fwd")
-    if stream is not None:
-        _made_here(stream, made[0] and out, made[1] and final_state)
     return out, final_state
 
 
@@ -498,6 +508,9 @@ def gated_scan_bwd(x, g, out, dout, init_state=None, dfinal_state=None, cu_seqle
     """Backward of ``gated_scan_fwd`` (``gdn_gated_scan_bwd``): returns ``(dx, dg, dinit_state)`` for the loss
     gradients ``dout`` [B,T,D] and ``dfinal_state`` [N,D] (or None).  ``out`` is the forward's output; ``x`` may be
     None without ``input_gate``."""
+    if stream is not None:
+        return _elsewhere(stream, gated_scan_bwd, x, g, out, dout, init_state, dfinal_state, cu_seqlens, input_gate,
+                          want_dinit)
     lib = _lib or load_library()
     if input_gate and x is None:
         raise ValueError("gated_scan_bwd: x is needed with the input gate")
@@ -507,11 +520,9 @@ def gated_scan_bwd(x, g, out, dout, init_state=None, dfinal_state=None, cu_seqle
     rc = lib.gdn_gated_scan_bwd(_ptr(x), g.data_ptr(), out.data_ptr(), dout.data_ptr(), _ptr(init_state),
                                 _ptr(dfinal_state), _ptr(cu_seqlens), N if cu_seqlens is not None else 0,
                                 dx.data_ptr(), dg.data_ptr(), _ptr(dinit), B, T, D, _dt(g), int(bool(input_gate)),
-                                _stream_of(g, stream))
+                                _stream_of(g))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_gated_scan_bwd")
-    if stream is not None:
-        _made_here(stream, dx, dg, dinit)
     return dx, dg, dinit
 
 
@@ -523,25 +534,24 @@ def _sound(t, dtype):
 def gated_scan_step(state, x, g, input_gate=False, out=None, stream=None):
     """One token of the gated scan per sequence (``gdn_gated_scan_step``); ``state`` [N,D] fp32 is updated in
     place.  x, g [N,D] (fp32 or bf16).  Returns out [N,D]."""
+    if stream is not None:
+        return _elsewhere(stream, gated_scan_step, state, x, g, input_gate, out)
     lib = _lib or load_library()
     shape, dtype = state.shape, x.dtype
     if len(shape) != 2 or x.shape != shape or g.shape != shape or (out is not None and out.shape != shape):
         raise ValueError("gated_scan_step: state, x, g and out must be [N,D]")
     if state.dtype is not _F32:
         raise TypeError("state must be float32")
-    made = out is None
-    if g.dtype is not dtype or (not made and out.dtype is not dtype):
+    if g.dtype is not dtype or (out is not None and out.dtype is not dtype):
         raise TypeError("x, g and out must share one dtype")
     _need_cuda(state, x, g, out)
-    if made:
+    if out is None:
         out = _empty_like(x)
     N, D = shape
     rc = lib.gdn_gated_scan_step(state.data_ptr(), x.data_ptr(), g.data_ptr(), out.data_ptr(), N, D, _dt(x),
-                                 1 if input_gate else 0, _stream_of(x, stream))
+                                 1 if input_gate else 0, _stream_of(x))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_gated_scan_step")
-    if stream is not None and made:
-        _made_here(stream, out)
     return out
 
 
@@ -576,6 +586,8 @@ def _check_norm_args(x, params, stats, same):
 def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     """Layer norm over the last axis (``gdn_layer_norm_fwd``).  x [..., D] (fp32 or bf16); weight, bias [D] fp32 or
     None.  Returns ``(out, mean, rstd)``, the statistics fp32 of shape ``x.shape[:-1]``."""
+    if stream is not None:
+        return _elsewhere(stream, layer_norm_fwd, x, weight, bias, eps, out)
     lib = _lib or load_library()
     # everything in order takes the short way; the long one says what is not
     shape = x.shape
@@ -587,18 +599,15 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     else:
         rows, D = _check_norm_args(x, (weight, bias), (), (out,))
     dt = _dt(x)
-    made = out is None
-    if made:
+    if out is None:
         out = _empty_like(x)
     mean = _empty(shape[:-1], dtype=_F32, device=x.device)
     rstd = _empty_like(mean)
     rc = lib.gdn_layer_norm_fwd(x.data_ptr(), None if weight is None else weight.data_ptr(),
                                 None if bias is None else bias.data_ptr(), out.data_ptr(), mean.data_ptr(),
-                                rstd.data_ptr(), rows, D, dt, eps, _stream_of(x, stream))
+                                rstd.data_ptr(), rows, D, dt, eps, _stream_of(x))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_layer_norm_fwd")
-    if stream is not None:
-        _made_here(stream, out if made else None, mean, rstd)
     return out, mean, rstd
 
 
@@ -619,6 +628,8 @@ def _workspace(given, need, device):
 def layer_norm_bwd(dout, x, mean, rstd, weight=None, workspace=None, stream=None):
     """Backward of ``layer_norm_fwd`` (``gdn_layer_norm_bwd``): returns ``(dx, dweight, dbias)``, the last two [D]
     fp32.  ``mean`` and ``rstd`` are the forward's."""
+    if stream is not None:
+        return _elsewhere(stream, layer_norm_bwd, dout, x, mean, rstd, weight, workspace)
     lib = _lib or load_library()
     rows, D = _check_norm_args(x, (weight,), (mean, rstd), (dout,))
     dt = _dt(x)
@@ -630,11 +641,9 @@ def layer_norm_bwd(dout, x, mean, rstd, weight=None, workspace=None, stream=None
                           lib.gdn_layer_norm_bwd_workspace_size(rows, D, dt), device)
     rc = lib.gdn_layer_norm_bwd(dout.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
                                 dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, D, dt, ws.data_ptr(), size,
-                                _stream_of(x, stream))
+                                _stream_of(x))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_layer_norm_bwd")
-    if stream is not None:
-        _made_here(stream, dx, dw, db, ws if workspace is None else None)
     return dx, dw, db
 
 
@@ -671,6 +680,8 @@ def linear_cross_entropy_fwd(h, weight, targets, workspace=None, stream=None):
     h [N,D], weight [V,D] (fp32 or bf16); targets int32 [N], rows with a target outside [0,V) are ignored.
     Returns ``(loss, lse)``, both [N] fp32 and 0 in ignored rows.
     """
+    if stream is not None:
+        return _elsewhere(stream, linear_cross_entropy_fwd, h, weight, targets, workspace)
     lib = _lib or load_library()
     N, D, V = _check_ce_args(h, weight, targets, ())
     dt = _dt(h)
@@ -680,17 +691,17 @@ def linear_cross_entropy_fwd(h, weight, targets, workspace=None, stream=None):
     ws, size = _workspace(workspace, 0 if workspace is not None else
                           lib.gdn_linear_cross_entropy_workspace_size(N, D, V, dt, 0), device)
     rc = lib.gdn_linear_cross_entropy_fwd(h.data_ptr(), weight.data_ptr(), targets.data_ptr(), loss.data_ptr(),
-                                          lse.data_ptr(), N, D, V, dt, ws.data_ptr(), size, _stream_of(h, stream))
+                                          lse.data_ptr(), N, D, V, dt, ws.data_ptr(), size, _stream_of(h))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_linear_cross_entropy_fwd")
-    if stream is not None:
-        _made_here(stream, loss, lse, ws if workspace is None else None)
     return loss, lse
 
 
 def linear_cross_entropy_bwd(h, weight, targets, lse, dloss, workspace=None, stream=None):
     """Gradient of ``linear_cross_entropy_fwd`` (``gdn_linear_cross_entropy_bwd``) for the gradient ``dloss`` [N]
     fp32 of each row's loss: returns ``(dh, dweight)`` in the dtype of h.  ``lse`` is the forward's."""
+    if stream is not None:
+        return _elsewhere(stream, linear_cross_entropy_bwd, h, weight, targets, lse, dloss, workspace)
     lib = _lib or load_library()
     N, D, V = _check_ce_args(h, weight, targets, (lse, dloss))
     dt = _dt(h)
@@ -699,11 +710,9 @@ def linear_cross_entropy_bwd(h, weight, targets, lse, dloss, workspace=None, str
                           lib.gdn_linear_cross_entropy_workspace_size(N, D, V, dt, 1), h.device)
     rc = lib.gdn_linear_cross_entropy_bwd(h.data_ptr(), weight.data_ptr(), targets.data_ptr(), lse.data_ptr(),
                                           dloss.data_ptr(), dh.data_ptr(), dw.data_ptr(), N, D, V, dt, ws.data_ptr(),
-                                          size, _stream_of(h, stream))
+                                          size, _stream_of(h))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_linear_cross_entropy_bwd")
-    if stream is not None:
-        _made_here(stream, dh, dw, ws if workspace is None else None)
     return dh, dw
 
 
