@@ -167,6 +167,23 @@ def _stream(stream):
     return getattr(stream, "cuda_stream", stream)
 
 
+def _elsewhere(stream, call, *args):
+    """``call(*args)`` on the stream that the caller names, a torch stream or a raw handle.
+
+    It is the current one meanwhile, so outputs and workspaces come from memory that this stream has done with: memory of
+    the caller's current stream may still be in use by work queued there.  What the call made is used on the caller's
+    stream next; the allocator keeps it until that use is over too."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream)
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        got = call(*args)
+    given = {id(t) for a in args for t in (a if isinstance(a, (tuple, list)) else (a,))}
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None and id(t) not in given:
+            t.record_stream(here)
+    return got
+
 
 def _check_chunk_args(q, k, v, g, beta, init_state, cu_seqlens, out, final_state):
     """The checks every chunked-forward wrapper makes before it hands raw pointers to the C ABI:
@@ -224,6 +241,9 @@ def chunk_fwd(q, k, v, g, beta, init_state=None, cu_seqlens=None, scale=None, us
     init_state [N,H,dv,dk] fp32 or None; cu_seqlens int32 [N+1] (device) or None.
     Returns ``(out, final_state)``; final_state is None if not requested.
     """
+    if stream is not None:
+        return _elsewhere(stream, chunk_fwd, q, k, v, g, beta, init_state, cu_seqlens, scale, use_qk_l2norm,
+                          out, final_state, output_final_state, workspace, chunk_size)
     lib = load_library()
     B, T, H, dk = q.shape
     dv = v.shape[-1]
@@ -253,6 +273,9 @@ def chunk_bwd(q, k, v, g, beta, dout, init_state=None, dfinal_state=None, cu_seq
               use_qk_l2norm=True, want_dinit=True, workspace=None, chunk_size=CHUNK, stream=None):
     """Backward of ``chunk_fwd`` (``gdn_chunk_bwd``): returns ``(dq, dk, dv, dg, dbeta, dinit_state)``
     for the loss gradients ``dout`` [B,T,H,dv] and ``dfinal_state`` [N,H,dv,dk] (or None)."""
+    if stream is not None:
+        return _elsewhere(stream, chunk_bwd, q, k, v, g, beta, dout, init_state, dfinal_state, cu_seqlens, scale,
+                          use_qk_l2norm, want_dinit, workspace, chunk_size)
     lib = load_library()
     B, T, H, dk = q.shape
     dv = v.shape[-1]
@@ -289,6 +312,8 @@ def decode_step(state, q, k, v, g, beta, scale=None, use_qk_l2norm=True, out=Non
 
     q, k [N,H,dk], v [N,H,dv] (fp32 or bf16); g, beta [N,H] fp32.  Returns out [N,H,dv].
     """
+    if stream is not None:
+        return _elsewhere(stream, decode_step, state, q, k, v, g, beta, scale, use_qk_l2norm, out)
     lib = load_library()
     N, H, dv, dk = state.shape
     if scale is None:
@@ -311,6 +336,8 @@ def decode_multi(state, q, k, v, g, beta, scale=None, use_qk_l2norm=True, out=No
     q, k [N,T,H,dk], v [N,T,H,dv] (fp32 or bf16); g, beta [N,T,H] fp32.  Returns out [N,T,H,dv],
     the same as T successive ``decode_step`` calls.
     """
+    if stream is not None:
+        return _elsewhere(stream, decode_multi, state, q, k, v, g, beta, scale, use_qk_l2norm, out)
     lib = load_library()
     N, H, dv, dk = state.shape
     T = q.shape[1]
@@ -340,6 +367,9 @@ def prologue(xq, xk, xv, wq, wk, wv, a, b, A_log, dt_bias, conv_state_in=None, c
     a, b [B,T,H] fp32; A_log, dt_bias [H] fp32; conv states [N,K-1,H,2dk+dv] (dtype of x) or None.
     Returns ``(q, k, v, g, beta)``; ``out`` may pass those five tensors preallocated.
     """
+    if stream is not None:
+        return _elsewhere(stream, prologue, xq, xk, xv, wq, wk, wv, a, b, A_log, dt_bias, conv_state_in,
+                          conv_state_out, cu_seqlens, out)
     lib = load_library()
     B, T, H, dk = xq.shape
     dv = xv.shape[-1]
@@ -376,6 +406,10 @@ def prologue_chunk_fwd(xq, xk, xv, wq, wk, wv, a, b, A_log, dt_bias, conv_state_
     fp32; a, b [B,T,H] fp32; A_log, dt_bias [H] fp32; conv states [N,K-1,H,2dk+dv] bf16 or None;
     init_state [N,H,dv,dk] fp32 or None; cu_seqlens int32 [N+1] or None.  Returns ``(out, final_state)``.
     """
+    if stream is not None:
+        return _elsewhere(stream, prologue_chunk_fwd, xq, xk, xv, wq, wk, wv, a, b, A_log, dt_bias, conv_state_in,
+                          conv_state_out, init_state, cu_seqlens, scale, use_qk_l2norm, out, final_state,
+                          output_final_state, workspace, chunk_size)
     lib = load_library()
     B, T, H, dk = xq.shape
     dv = xv.shape[-1]
@@ -429,23 +463,6 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 def _stream_of(t):
     return _raw_stream(t.get_device())
-
-
-def _elsewhere(stream, call, *args):
-    """``call(*args)`` on the stream that the caller names, a torch stream or a raw handle.
-
-    It is the current one meanwhile, so outputs and workspaces come from memory that this stream has done with: memory of
-    the caller's current stream may still be in use by work queued there.  What the call made is used on the caller's
-    stream next; the allocator keeps it until that use is over too."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream)
-    here = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        got = call(*args)
-    for t in got if isinstance(got, tuple) else (got,):
-        if t is not None and all(t is not a for a in args):
-            t.record_stream(here)
-    return got
 
 
 def _check_scan_args(x, g, cu_seqlens, dtype, states, same):

@@ -27,7 +27,17 @@ def operators():
     _, mean, rstd = gdn.layer_norm_fwd(x, w, w)
     _, lse = gdn.linear_cross_entropy_fwd(h, head, t)
     state = r(1200, 256)
+    q, gate = r(2, 300, 2, 128).bfloat16(), -0.1 * torch.rand(2, 300, 2, generator=gen, device="cuda")
+    beta, memory = torch.rand(2, 300, 2, generator=gen, device="cuda"), r(2, 2, 128, 128)
+    token = [v[:, 0].contiguous() for v in (q, q, q, gate, beta)]
+    flt, par = 0.5 * r(2, 128, 4), r(2)
     return {
+        "chunked forward": lambda s: gdn.chunk_fwd(q, q, q, gate, beta, stream=s),
+        # all but dg, whose sums over a chunk's rows are atomic and differ in their last bits from call to call
+        "chunked backward": lambda s: [gdn.chunk_bwd(q, q, q, gate, beta, q, stream=s)[i] for i in (0, 1, 2, 4, 5)],
+        "decode": lambda s: (gdn.decode_step(memory.clone() if s is None else memory, *token, stream=s),),
+        "prologue": lambda s: gdn.prologue(q, q, q, flt, flt, flt, gate, beta, par, par, stream=s),
+        "prologue and forward": lambda s: gdn.prologue_chunk_fwd(q, q, q, flt, flt, flt, gate, beta, par, par, stream=s),
         "scan forward": lambda s: gdn.gated_scan_fwd(x, g, stream=s),
         "scan backward": lambda s: gdn.gated_scan_bwd(None, g, out, dy, stream=s),
         "scan step": lambda s: (gdn.gated_scan_step(state.clone() if s is None else state, h, g.view(1200, 256), stream=s),),
@@ -39,7 +49,8 @@ def operators():
 
 
 @pytest.mark.parametrize("name", ["scan forward", "scan backward", "scan step", "norm forward", "norm backward", "loss",
-                                  "gradient"])
+                                  "gradient", "chunked forward", "chunked backward", "decode", "prologue",
+                                  "prologue and forward"])
 def test_memory_still_in_use_on_the_current_stream(name):
     call = operators()[name]
     want = call(None)

@@ -54,6 +54,7 @@ def world(monkeypatch):
     monkeypatch.setattr(gdn, "_empty_like", torch.empty_like)
     monkeypatch.setattr(gdn, "_raw_stream", lambda device: w["now"].cuda_stream)
     monkeypatch.setattr(gdn, "_need_cuda", lambda *a: None)
+    monkeypatch.setattr(gdn, "load_library", lambda: w["lib"])
     w["lib"] = FakeLibrary()
     monkeypatch.setattr(gdn, "_lib", w["lib"])
     return w
@@ -71,14 +72,25 @@ AROUND = {
     "loss": lambda s: gdn.linear_cross_entropy_fwd(I, I, T, stream=s),
     "gradient": lambda s: gdn.linear_cross_entropy_bwd(I, I, T, V[:2], V[:2], stream=s),
 }
+Q, G, M = torch.zeros(1, 4, 2, 8), torch.zeros(1, 4, 2), torch.zeros(1, 2, 8, 8)
+F, P = torch.zeros(2, 8, 4), torch.zeros(2)
+LAYER = {
+    "chunked forward": lambda s: gdn.chunk_fwd(Q, Q, Q, G, G, stream=s),
+    "chunked backward": lambda s: gdn.chunk_bwd(Q, Q, Q, G, G, Q, stream=s),
+    "decode": lambda s: gdn.decode_step(M, Q[:, 0], Q[:, 0], Q[:, 0], G[:, 0], G[:, 0], stream=s),
+    "tokens of decode": lambda s: gdn.decode_multi(M, Q, Q, Q, G, G, stream=s),
+    "prologue": lambda s: gdn.prologue(Q, Q, Q, F, F, F, G, G, P, P, stream=s),
+    "prologue and forward": lambda s: gdn.prologue_chunk_fwd(*[Q.bfloat16()] * 3, F, F, F, G, G, P, P, stream=s),
+}
+CALLS = {**AROUND, **LAYER}
 
 
-@pytest.mark.parametrize("name", AROUND)
+@pytest.mark.parametrize("name", CALLS)
 def test_memory_comes_from_the_named_stream(world, name):
     """What a kernel on the named stream writes is taken from that stream's memory and kept until the caller's stream,
     which uses it next, has done so."""
     stream = FakeStream()
-    got = AROUND[name](stream)
+    got = CALLS[name](stream)
     got = got if isinstance(got, tuple) else (got,)
     assert world["lib"].streams == [77] and world["now"] is world["here"]
     assert world["made"] and all(s is stream for _, s in world["made"])
@@ -91,9 +103,13 @@ def test_what_the_caller_gave_is_the_callers(world):
     world["made"].clear()
     got = gdn.gated_scan_fwd(X, X, out=out, final_state=state, stream=FakeStream())
     assert got[0] is out and got[1] is state and not world["made"] and not world["recorded"]
+    five = tuple(torch.zeros_like(t) for t in (Q, Q, Q, G, G))
+    world["made"].clear()
+    assert gdn.prologue(Q, Q, Q, F, F, F, G, G, P, P, out=five, stream=FakeStream()) is not None
+    assert not world["made"] and not world["recorded"]
 
 
-@pytest.mark.parametrize("name", AROUND)
+@pytest.mark.parametrize("name", CALLS)
 def test_without_a_name_the_current_stream_it_is(world, name):
-    AROUND[name](None)
+    CALLS[name](None)
     assert world["lib"].streams == [5] and all(s is world["here"] for _, s in world["made"]) and not world["recorded"]
