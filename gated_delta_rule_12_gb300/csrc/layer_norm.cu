@@ -306,7 +306,7 @@ rows_fwd_kernel(const LayerNormArgs a, int team)
         stage = (stage + 1) & (kStages - 1);
         float s[1] = {total(add2(p, q))};
         sum(s);
-        const float mean = s[0] * inv;
+        const float mean = s[0] / (float)a.D;   // times 1 / D, a row of one value could miss its mean by an ulp, and x - mean 0
         p = q = 0;
 #pragma unroll
         for (int i = 0; i < NP; ++i) x[i] = add2(x[i], both(-mean));

@@ -1,4 +1,4 @@
-"""Layer norm where its buffers alias."""
+"""Layer norm where its buffers alias, its rows are constant or very long."""
 import pytest
 import torch
 
@@ -44,3 +44,16 @@ def test_dx_in_the_place_of_dout(rows, D, dtype):
     dw, db = bwd_into(buf, buf, x, mean, rstd, w)
     assert torch.equal(buf, want[0])
     assert torch.equal(dw, want[1]) and torch.equal(db, want[2])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [13, 49, 98, 255, 509, 1000, 1501, 2049, 3001, 7001, 10000, 16383, 20000])
+@pytest.mark.parametrize("value", [3.0, 1000.0])
+def test_constant_rows_of_any_length(value, D, dtype):
+    """Partial sums of whole numbers below 2^24 are exact, so the mean is the value itself, no deviation is left and the
+    row becomes its bias, of however many elements it consists."""
+    x = torch.full((5, D), value, dtype=DT[dtype]).cuda()
+    b = torch.randn(D).cuda()
+    y, mean, rstd = gdn.layer_norm_fwd(x, None, b, eps=1e-5)
+    assert (mean == value).all()
+    assert torch.equal(y, b.to(DT[dtype]).expand_as(y))
