@@ -92,8 +92,10 @@ __device__ __forceinline__ uint2 pack(const Pair (&v)[kPairs<T>])
     }
 }
 
-// One stretch of the recurrence maps a carry c to H + A c.  A = exp(S), S the sum of the stretch's g, is kept finite,
-// so that growth beyond fp32's range leaves a carry of 0 at 0.
+// One stretch of the recurrence maps a carry c to H + exp(S) c, S the sum of the stretch's g.  exp(S) leaves fp32 from
+// |S| = 88 on, although its product with the carry may not; so A is exp(S / 2), and the carry is multiplied by it twice (a
+// test for such sums instead cost up to 30 % of the kernel's time).  A is kept finite, so that growth beyond fp32's range
+// leaves a carry of 0 at 0; the square of fp32's largest number makes infinity of every other carry that is not subnormal.
 template <typename T> struct Map { Pair A[kPairs<T>], H[kPairs<T>]; };
 
 template <typename T>
@@ -102,16 +104,19 @@ __device__ __forceinline__ void set_decay(Map<T> &m, const Pair (&sum)[kPairs<T>
 #pragma unroll
     for (int v = 0; v < kPairs<T>; ++v) {
         float a, b;
-        split(decay<T>(sum[v]), a, b);
+        split(decay<T>(mul2(sum[v], both(0.5f))), a, b);
         m.A[v] = pair(fminf(a, 3.402823466e38f), fminf(b, 3.402823466e38f));
     }
 }
+
+// H + A A c
+__device__ __forceinline__ Pair through(Pair A, Pair c, Pair H) { return fma2(A, mul2(A, c), H); }
 
 template <typename T>
 __device__ __forceinline__ void apply(const Map<T> &m, Pair (&c)[kPairs<T>])
 {
 #pragma unroll
-    for (int v = 0; v < kPairs<T>; ++v) c[v] = fma2(m.A[v], c[v], m.H[v]);
+    for (int v = 0; v < kPairs<T>; ++v) c[v] = through(m.A[v], c[v], m.H[v]);
 }
 
 __device__ __forceinline__ void cluster_sync()
@@ -185,7 +190,7 @@ struct Exchange {
             for (int v = 0; v < NP; ++v) {
                 const Pair so = __shfl_up_sync(0xffffffffu, s[v], o * L), ho = __shfl_up_sync(0xffffffffu, h[v], o * L);
                 if (group >= o) {
-                    h[v] = fma2(m.A[v], ho, h[v]);
+                    h[v] = through(m.A[v], ho, h[v]);
                     s[v] = add2(s[v], so);
                 }
             }
