@@ -115,15 +115,15 @@ __device__ __forceinline__ bool kept(const LinearCeArgs &a, int row)
     return t >= 0 && t < a.V;
 }
 
-// Logits of rows blockIdx.y * 128 .. and columns v0 + blockIdx.x * 128 ..; BACK: G of the piece, else the tile's
+// Logits of rows row0 + blockIdx.y * 128 .. and columns v0 + blockIdx.x * 128 ..; BACK: G of the piece, else the tile's
 // (max, sum) of each row and the target's logit where the tile holds it.
 template <typename T, bool BACK>
-__global__ void __launch_bounds__(kThreads, 2) ce_logits_kernel(LinearCeArgs a, CeWorkspace ws, int v0, int cols)
+__global__ void __launch_bounds__(kThreads, 2) ce_logits_kernel(LinearCeArgs a, CeWorkspace ws, int v0, int cols, int row0)
 {
-    const int m0 = blockIdx.y * kTile, n0 = v0 + blockIdx.x * kTile;
+    const int m0 = row0 + blockIdx.y * kTile, n0 = v0 + blockIdx.x * kTile;
     const T *h = (const T *)a.h, *w = (const T *)a.w;
     // the device error word in front of the workspace: these kernels have nothing to report
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *((unsigned *)a.workspace - 64) = kDevErrNone;
+    if (blockIdx.x == 0 && m0 == 0 && threadIdx.x == 0) *((unsigned *)a.workspace - 64) = kDevErrNone;
     float acc[8][8];
     tile_product<false, false>(
         [&](int m, int64_t k) { return m0 + m < a.N ? to_f32(h[(int64_t)(m0 + m) * a.D + k]) : 0.f; },
@@ -193,9 +193,9 @@ __global__ void __launch_bounds__(256) ce_join_kernel(LinearCeArgs a, CeWorkspac
 
 // dh (+)= G W over one piece; the last piece writes the gradient.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) ce_dh_kernel(LinearCeArgs a, CeWorkspace ws, int v0, int cols)
+__global__ void __launch_bounds__(kThreads, 2) ce_dh_kernel(LinearCeArgs a, CeWorkspace ws, int v0, int cols, int row0)
 {
-    const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
+    const int m0 = row0 + blockIdx.y * kTile, n0 = blockIdx.x * kTile;
     const float *G = (const float *)((const char *)a.workspace + ws.g);
     float *sofar = (float *)((char *)a.workspace + ws.acc);
     const T *w = (const T *)a.w;
@@ -222,9 +222,9 @@ __global__ void __launch_bounds__(kThreads, 2) ce_dh_kernel(LinearCeArgs a, CeWo
 
 // dW of one piece: G^T h over the kept rows.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) ce_dw_kernel(LinearCeArgs a, CeWorkspace ws, int v0, int cols)
+__global__ void __launch_bounds__(kThreads, 2) ce_dw_kernel(LinearCeArgs a, CeWorkspace ws, int v0, int cols, int row0)
 {
-    const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
+    const int m0 = row0 + blockIdx.y * kTile, n0 = blockIdx.x * kTile;
     const float *G = (const float *)((const char *)a.workspace + ws.g);
     const T *h = (const T *)a.h;
     float acc[8][8];
@@ -243,11 +243,24 @@ __global__ void __launch_bounds__(kThreads, 2) ce_dw_kernel(LinearCeArgs a, CeWo
     }
 }
 
+// launch(grid, row0) over the tiles of rows x columns: a grid's second index ends at 65535, so more rows of tiles than that
+// are several launches.
+template <class Launch>
+void over_tiles(int rows, int columns, Launch launch)
+{
+    constexpr int kMost = 65535;
+    const int down = ceil_div(rows, kTile);
+    for (int first = 0; first < down; first += kMost)
+        launch(dim3(ceil_div(columns, kTile), down - first < kMost ? down - first : kMost), first * kTile);
+}
+
 template <typename T>
 cudaError_t fwd(const LinearCeArgs &a, cudaStream_t st)
 {
     const CeWorkspace ws = layout(a.N, a.D, a.V, false);
-    ce_logits_kernel<T, false><<<dim3(ws.tiles, ceil_div(a.N, kTile)), kThreads, 0, st>>>(a, ws, 0, a.V);
+    over_tiles(a.N, a.V, [&](dim3 grid, int row0) {
+        ce_logits_kernel<T, false><<<grid, kThreads, 0, st>>>(a, ws, 0, a.V, row0);
+    });
     ce_join_kernel<<<ceil_div(a.N, 8), 256, 0, st>>>(a, ws);
     return cudaGetLastError();
 }
@@ -256,12 +269,19 @@ template <typename T>
 cudaError_t bwd(const LinearCeArgs &a, cudaStream_t st)
 {
     const CeWorkspace ws = layout(a.N, a.D, a.V, true);
-    const int mt = ceil_div(a.N, kTile), dt = ceil_div(a.D, kTile);
     for (int v0 = 0; v0 < a.V; v0 += ws.piece) {
-        const int cols = a.V - v0 < ws.piece ? a.V - v0 : ws.piece, vt = ceil_div(cols, kTile);
-        ce_logits_kernel<T, true><<<dim3(vt, mt), kThreads, 0, st>>>(a, ws, v0, cols);
-        if (a.dh) ce_dh_kernel<T><<<dim3(dt, mt), kThreads, 0, st>>>(a, ws, v0, cols);
-        if (a.dw) ce_dw_kernel<T><<<dim3(dt, vt), kThreads, 0, st>>>(a, ws, v0, cols);
+        const int cols = a.V - v0 < ws.piece ? a.V - v0 : ws.piece;
+        over_tiles(a.N, cols, [&](dim3 grid, int row0) {
+            ce_logits_kernel<T, true><<<grid, kThreads, 0, st>>>(a, ws, v0, cols, row0);
+        });
+        if (a.dh)
+            over_tiles(a.N, a.D, [&](dim3 grid, int row0) {
+                ce_dh_kernel<T><<<grid, kThreads, 0, st>>>(a, ws, v0, cols, row0);
+            });
+        if (a.dw)
+            over_tiles(cols, a.D, [&](dim3 grid, int row0) {
+                ce_dw_kernel<T><<<grid, kThreads, 0, st>>>(a, ws, v0, cols, row0);
+            });
     }
     return cudaGetLastError();
 }
