@@ -32,7 +32,8 @@ struct Geometry {
     int nct;             // chunks per row when cu == null
 };
 
-__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// a >= 0, b > 0; the sum of any two ints fits an unsigned one
+__host__ __device__ inline int ceil_div(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1u) / (unsigned)b); }
 
 __host__ inline int64_t num_slots(int B, int T, int N, bool varlen)
 {

@@ -108,7 +108,7 @@ cudaError_t launch_layer_norm_bwd(const LayerNormArgs &a, cudaStream_t st);
 size_t layer_norm_bwd_workspace_bytes(int64_t rows, int D, int dt);
 cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st);
 cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st);
-// bf16 with D a multiple of 8 (rows that TMA can address): the tensor cores
+// bf16 with D a multiple of 8 (rows that TMA can address) up to 2^24: the tensor cores
 bool linear_ce_tc_supported(int dt, int D);
 size_t linear_ce_tc_workspace_bytes(int N, int D, int V, bool backward);
 cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st);

@@ -397,8 +397,8 @@ gdn_status gdn_layer_norm_bwd(const void *dout, const void *x, const float *mean
  *   workspace     at least gdn_linear_cross_entropy_workspace_size(..., backward = 0) bytes, 256-byte aligned (about
  *                 N V / 32 bytes); its first 256 bytes hold the device error word read by gdn_check_device_error (a
  *                 call with N = 0 leaves it as it is).
- * Logits and sums are fp32.  bf16 with D a multiple of 8 runs on the tensor cores, other sizes and fp32 on the CUDA
- * cores.  Results do not depend on timing.
+ * Logits and sums are fp32.  bf16 with D a multiple of 8, up to 2^24, runs on the tensor cores, other sizes and fp32 on the
+ * CUDA cores.  Results do not depend on timing.
  * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_CUDA.
  */
 size_t gdn_linear_cross_entropy_workspace_size(int32_t N, int32_t D, int32_t V, gdn_dtype dt, int32_t backward);

@@ -1,4 +1,4 @@
-"""The gated scan where runs of rows grow or decay beyond what fp32 holds."""
+"""The gated scan where runs of rows grow or decay beyond what fp32 holds, and at the ends of its sizes."""
 import pytest
 import torch
 
@@ -74,3 +74,27 @@ def test_zero_states_stay_zero_and_new_inputs_decay(T, D, dtype):
     assert (out[:, :T // 2] == 0).all()
     ref.check(out, ro, bo, "out")
     ref.check(fin, rf, bf, "final state")
+
+
+def test_the_longest_sequence():
+    T = 2 ** 31 - 1
+    x = torch.zeros((1, T, 1), dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros_like(x)
+    x[0, 5], x[0, -1], g[0, 1 << 30] = 3.0, 1.0, float("-inf")
+    out, fin = gdn.gated_scan_fwd(x, g)
+    assert (out[0, :5] == 0).all() and (out[0, 5:1 << 30] == 3).all() and (out[0, 1 << 30:-1] == 0).all()
+    assert out[0, -1] == 1 and fin.item() == 1
+    del out
+    dfin = torch.full((1, 1), 2.0, device="cuda")
+    dx, dg, di = gdn.gated_scan_bwd(None, g, x, torch.zeros_like(x), dfinal_state=dfin)
+    assert (dx[0, 1 << 30:] == 2).all() and (dx[0, :1 << 30] == 0).all() and di.item() == 0
+    # h_{t-1} is 3 behind token 5 alone, where nothing comes back any more; behind the last token there is none
+    assert (dg == 0).all()
+
+
+def test_the_widest_row():
+    D = 2 ** 31 - 1
+    x = torch.full((1, 1, D), 2.0, dtype=torch.bfloat16, device="cuda")
+    x[0, 0, -3:] = 5.0
+    out, fin = gdn.gated_scan_fwd(x, torch.zeros_like(x))
+    assert torch.equal(out, x) and (fin[0, -3:] == 5).all() and (fin[0, :-3] == 2).all()

@@ -1,4 +1,4 @@
-"""The linear cross entropy at the ends of its sizes: many tokens, many words."""
+"""The linear cross entropy at the ends of its sizes: many tokens, many words, long rows."""
 import pytest
 import torch
 
@@ -58,3 +58,27 @@ def test_more_word_tiles_than_a_grid_has_rows(dtype, D):
     rv, bd = ref.ce_bwd(h, w, t, lse, dl, low_bits=False)
     ref.check(dh, rv[0], bd[0], "dh")
     ref.check(dw, rv[1], bd[1], "dweight")
+
+
+@pytest.mark.parametrize("D", [1 << 24, (1 << 24) + 8])
+def test_very_long_rows(D):
+    """The last length of the tensor cores and the first that they leave; sums of a few whole numbers are exact."""
+    h = torch.ones((2, D), dtype=torch.bfloat16, device="cuda")
+    h[1] = -1
+    w = torch.zeros((3, D), dtype=torch.bfloat16, device="cuda")
+    w[0, [0, 5, D // 2, D - 1]], w[1, [7, D - 2, D - 1]], w[2, D - 1] = 1.0, 1.0, -1.0
+    t = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    loss, lse = gdn.linear_cross_entropy_fwd(h, w, t)
+    l = torch.tensor([[4.0, 3.0, -1.0], [-4.0, -3.0, 1.0]], dtype=torch.float64)
+    r = torch.logsumexp(l, -1)
+    assert ((ref.f64(lse) - r).abs() <= 1e-6 * (1 + r.abs())).all()
+    assert ((ref.f64(loss) - (r - l[[0, 1], [0, 2]])).abs() <= 1e-6 * (1 + r.abs())).all()
+    dh, dw = gdn.linear_cross_entropy_bwd(h, w, t, lse, torch.ones(2, device="cuda"))
+    G = torch.softmax(l, -1)
+    G[0, 0] -= 1
+    G[1, 2] -= 1
+    at = torch.tensor([0, 1, 5, 7, D // 2, D - 2, D - 1])
+    rh, rw = G @ ref.f64(w[:, at]), G.T @ ref.f64(h[:, at])
+    # G in bfloat16 and the result's own rounding; three terms of magnitude 1 at most
+    assert ((ref.f64(dh[:, at]) - rh).abs() <= 2 * ref.BF16 * (G.abs() @ ref.f64(w[:, at]).abs())).all()
+    assert ((ref.f64(dw[:, at]) - rw).abs() <= 2 * ref.BF16 * (G.abs().T @ ref.f64(h[:, at]).abs())).all()
