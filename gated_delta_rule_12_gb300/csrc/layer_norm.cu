@@ -564,19 +564,20 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) long_fwd_kernel(const LayerNormArgs a)
 {
     __shared__ float sh[kThreads / 32];
+    const unsigned D = a.D;   // i + kThreads may pass 2^31
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const T *x = (const T *)a.x + r * a.D;
         float s = 0.f;
-        for (int i = threadIdx.x; i < a.D; i += kThreads) s += to_f32(x[i]);
+        for (unsigned i = threadIdx.x; i < D; i += kThreads) s += to_f32(x[i]);
         const float mean = block_sum(s, sh) / a.D;
         s = 0.f;
-        for (int i = threadIdx.x; i < a.D; i += kThreads) {
+        for (unsigned i = threadIdx.x; i < D; i += kThreads) {
             const float d = to_f32(x[i]) - mean;
             s = fmaf(d, d, s);
         }
         const float rstd = 1.f / sqrtf(block_sum(s, sh) / a.D + a.eps);
         T *y = (T *)a.out + r * a.D;
-        for (int i = threadIdx.x; i < a.D; i += kThreads) {
+        for (unsigned i = threadIdx.x; i < D; i += kThreads) {
             const float xh = (to_f32(x[i]) - mean) * rstd;
             y[i] = from_f32<T>(fmaf(xh, a.weight ? a.weight[i] : 1.f, a.bias ? a.bias[i] : 0.f));
         }
@@ -591,18 +592,19 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) long_dx_kernel(const LayerNormArgs a)
 {
     __shared__ float sh[kThreads / 32];
+    const unsigned D = a.D;   // i + kThreads may pass 2^31
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const T *x = (const T *)a.x + r * a.D, *dy = (const T *)a.dout + r * a.D;
         const float mean = a.mean[r], rstd = a.rstd[r];
         float s1 = 0.f, s2 = 0.f;
-        for (int i = threadIdx.x; i < a.D; i += kThreads) {
+        for (unsigned i = threadIdx.x; i < D; i += kThreads) {
             const float u = to_f32(dy[i]) * (a.weight ? a.weight[i] : 1.f);
             s1 += u;
             s2 = fmaf(u, (to_f32(x[i]) - mean) * rstd, s2);
         }
         const float c1 = block_sum(s1, sh) / a.D, c2 = block_sum(s2, sh) / a.D;
         T *dx = (T *)a.dx + r * a.D;
-        for (int i = threadIdx.x; i < a.D; i += kThreads) {
+        for (unsigned i = threadIdx.x; i < D; i += kThreads) {
             const float u = to_f32(dy[i]) * (a.weight ? a.weight[i] : 1.f);
             dx[i] = from_f32<T>(rstd * (u - c1 - (to_f32(x[i]) - mean) * rstd * c2));
         }
@@ -613,8 +615,8 @@ __global__ void __launch_bounds__(kThreads) long_dx_kernel(const LayerNormArgs a
 template <typename T>
 __global__ void __launch_bounds__(kThreads) long_dw_kernel(const LayerNormArgs a)
 {
-    const int ch = blockIdx.x * kThreads + threadIdx.x;
-    if (ch >= a.D) return;
+    const unsigned ch = blockIdx.x * kThreads + threadIdx.x;   // may pass 2^31
+    if (ch >= (unsigned)a.D) return;
     const int64_t per = (a.rows + kRowSplits - 1) / kRowSplits, r0 = blockIdx.y * per;
     const int64_t r1 = r0 + per < a.rows ? r0 + per : a.rows;
     float sw = 0.f, sb = 0.f;

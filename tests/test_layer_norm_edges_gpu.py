@@ -57,3 +57,12 @@ def test_constant_rows_of_any_length(value, D, dtype):
     y, mean, rstd = gdn.layer_norm_fwd(x, None, b, eps=1e-5)
     assert (mean == value).all()
     assert torch.equal(y, b.to(DT[dtype]).expand_as(y))
+
+
+def test_the_longest_row():
+    """2^31 - 1 elements of +-1: a thread's sums are whole numbers up to 2^23, and the mean is 2^-31."""
+    D = 2 ** 31 - 1
+    x = torch.ones((1, D), dtype=torch.bfloat16, device="cuda")
+    x[0, 1::2] = -1
+    y, mean, rstd = gdn.layer_norm_fwd(x)
+    assert torch.equal(y, x) and abs(mean.item()) < 1e-6 and abs(rstd.item() - (1 + 1e-5) ** -0.5) < 1e-6
