@@ -465,6 +465,13 @@ def _stream_of(t):
     return _raw_stream(t.get_device())
 
 
+_MOST = 2 ** 31 - 1   # what a size may be in the C ABI; ctypes would cut a larger one down to its low 32 bits
+
+
+def _too_large(**sizes):
+    raise ValueError("sizes go up to 2^31 - 1, not " + ", ".join(f"{k} = {v}" for k, v in sizes.items()))
+
+
 def _check_scan_args(x, g, cu_seqlens, dtype, states, same):
     """Shapes, dtypes, placement and contiguity of a gated-scan call; returns (B, T, D, N).  ``states`` are the
     [N,D] fp32 tensors, ``same`` further tensors that must match g."""
@@ -472,6 +479,8 @@ def _check_scan_args(x, g, cu_seqlens, dtype, states, same):
     if len(shape) != 3:
         raise ValueError("x and g must be [B,T,D]")
     B, T, D = shape
+    if B > _MOST or T > _MOST or D > _MOST:
+        _too_large(B=B, T=T, D=D)
     N = B
     if cu_seqlens is not None:
         if cu_seqlens.dtype is not torch.int32:
@@ -557,6 +566,9 @@ def gated_scan_step(state, x, g, input_gate=False, out=None, stream=None):
     shape, dtype = state.shape, x.dtype
     if len(shape) != 2 or x.shape != shape or g.shape != shape or (out is not None and out.shape != shape):
         raise ValueError("gated_scan_step: state, x, g and out must be [N,D]")
+    N, D = shape
+    if N > _MOST or D > _MOST:
+        _too_large(N=N, D=D)
     if state.dtype is not _F32:
         raise TypeError("state must be float32")
     if g.dtype is not dtype or (out is not None and out.dtype is not dtype):
@@ -564,7 +576,6 @@ def gated_scan_step(state, x, g, input_gate=False, out=None, stream=None):
     _need_cuda(state, x, g, out)
     if out is None:
         out = _empty_like(x)
-    N, D = shape
     rc = lib.gdn_gated_scan_step(state.data_ptr(), x.data_ptr(), g.data_ptr(), out.data_ptr(), N, D, _dt(x),
                                  1 if input_gate else 0, _stream_of(x))
     if rc != GDN_OK:
@@ -578,6 +589,8 @@ def _check_norm_args(x, params, stats, same):
     if not shape or shape[-1] < 1:
         raise ValueError("x must be [..., D] with D >= 1")
     D = shape[-1]
+    if D > _MOST:
+        _too_large(D=D)
     rows = x.numel() // D
     for t in params:
         if t is not None:
@@ -609,7 +622,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     # everything in order takes the short way; the long one says what is not
     shape = x.shape
     D = shape[-1] if shape else 0
-    if D > 0 and out is None and x.is_cuda and x.is_contiguous() and \
+    if 0 < D <= _MOST and out is None and x.is_cuda and x.is_contiguous() and \
             (weight is None or (_sound(weight, _F32) and weight.shape == (D,))) and \
             (bias is None or (_sound(bias, _F32) and bias.shape == (D,))):
         rows = x.numel() // D
@@ -630,6 +643,8 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
 
 def layer_norm_bwd_workspace_size(rows, D, dtype=torch.bfloat16) -> int:
     dt = GDN_BF16 if dtype == _BF16 else GDN_F32
+    if D > _MOST:
+        return 0
     return int(load_library().gdn_layer_norm_bwd_workspace_size(rows, D, dt))
 
 
@@ -674,6 +689,8 @@ def _check_ce_args(h, weight, targets, rows):
     if targets.dtype is not torch.int32:
         raise TypeError("targets must be int32")
     N = hs[0]
+    if N > _MOST or hs[1] > _MOST or ws[0] > _MOST:
+        _too_large(N=N, D=hs[1], V=ws[0])
     if targets.shape != (N,):
         raise ValueError("targets must be [N]")
     for t in rows:
@@ -687,6 +704,8 @@ def _check_ce_args(h, weight, targets, rows):
 
 def linear_cross_entropy_workspace_size(N, D, V, dtype=torch.bfloat16, backward=False) -> int:
     dt = GDN_BF16 if dtype == _BF16 else GDN_F32
+    if max(N, D, V) > _MOST:
+        return 0
     return int(load_library().gdn_linear_cross_entropy_workspace_size(N, D, V, dt, int(bool(backward))))
 
 
