@@ -510,20 +510,23 @@ def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, input_gate=False, out
     and c = 1, or 1 - a with ``input_gate``.
 
     x, g [B,T,D] (fp32 or bf16, one dtype); init_state [N,D] fp32 or None; cu_seqlens int32 [N+1] (device) or
-    None.  Returns ``(out, final_state)``; final_state is None if not requested.
+    None.  Returns ``(out, final_state)``; final_state is None if not requested.  B may be 0.
     """
     if stream is not None:
         return _elsewhere(stream, gated_scan_fwd, x, g, init_state, cu_seqlens, input_gate, out, final_state,
                           output_final_state)
     lib = _lib or load_library()
     B, T, D, N = _check_scan_args(x, g, cu_seqlens, x.dtype, (init_state, final_state), (out,))
+    dt = _dt(x)
     if out is None:
         out = _empty_like(x)
     if final_state is None and output_final_state:
         final_state = _empty((N, D), dtype=_F32, device=x.device)
+    if B == 0:
+        return out, final_state
     rc = lib.gdn_gated_scan_fwd(x.data_ptr(), g.data_ptr(), _ptr(init_state), _ptr(cu_seqlens),
                                 N if cu_seqlens is not None else 0, out.data_ptr(), _ptr(final_state), B, T, D,
-                                _dt(x), int(bool(input_gate)), _stream_of(g))
+                                dt, int(bool(input_gate)), _stream_of(g))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_gated_scan_fwd")
     return out, final_state
@@ -541,11 +544,14 @@ def gated_scan_bwd(x, g, out, dout, init_state=None, dfinal_state=None, cu_seqle
     if input_gate and x is None:
         raise ValueError("gated_scan_bwd: x is needed with the input gate")
     B, T, D, N = _check_scan_args(x, g, cu_seqlens, g.dtype, (init_state, dfinal_state), (out, dout))
+    dt = _dt(g)
     dx, dg = _empty_like(g), _empty_like(g)
     dinit = _empty((N, D), dtype=_F32, device=g.device) if want_dinit else None
+    if B == 0:
+        return dx, dg, dinit
     rc = lib.gdn_gated_scan_bwd(_ptr(x), g.data_ptr(), out.data_ptr(), dout.data_ptr(), _ptr(init_state),
                                 _ptr(dfinal_state), _ptr(cu_seqlens), N if cu_seqlens is not None else 0,
-                                dx.data_ptr(), dg.data_ptr(), _ptr(dinit), B, T, D, _dt(g), int(bool(input_gate)),
+                                dx.data_ptr(), dg.data_ptr(), _ptr(dinit), B, T, D, dt, int(bool(input_gate)),
                                 _stream_of(g))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_gated_scan_bwd")

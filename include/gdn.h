@@ -320,8 +320,8 @@ gdn_status gdn_prologue_chunk_fwd(const void *xq, const void *xk, const void *xv
  *   init_state    [N, D] fp32 or NULL for zeros; final_state [N, D] fp32 or NULL to skip (may alias init_state);
  *                 a sequence without tokens passes its initial state on.
  *   cu_seqlens    as gdn_chunk_fwd (NULL: N = B sequences of T tokens; else packed, B = 1, N = num_seqs).
- *   T >= 0, D >= 1, no other limit on either; every pointer aligned to its element size (rows that start on 16-byte
- *   boundaries take the fast path).  out must not overlap x or g.  The recurrence runs in fp32; out is rounded to dt
+ *   B >= 1, T >= 0, D >= 1, no other limit on T and D; every pointer aligned to its element size (rows that start on
+ *   16-byte boundaries take the fast path).  out must not overlap x or g.  The recurrence runs in fp32; out is rounded to dt
  *   once.  A state of exactly 0 stays 0 however much a run of rows grows; any other one is right as far as fp32 holds
  *   it and infinite beyond (subnormal numbers apart; an exp(g) below 2^-126 counts as 0).
  * No workspace.  Results do not depend on timing.

@@ -113,3 +113,16 @@ def test_what_the_caller_gave_is_the_callers(world):
 def test_without_a_name_the_current_stream_it_is(world, name):
     CALLS[name](None)
     assert world["lib"].streams == [5] and all(s is world["here"] for _, s in world["made"]) and not world["recorded"]
+
+
+def test_an_empty_batch_of_the_scan_needs_no_call(world):
+    """As the other operators around the layer have it: nothing to compute is no error."""
+    x = torch.zeros(0, 3, 8)
+    out, fin = gdn.gated_scan_fwd(x, x, init_state=torch.zeros(0, 8))
+    assert out.shape == x.shape and fin.shape == (0, 8)
+    dx, dg, dinit = gdn.gated_scan_bwd(x, x, out, x, input_gate=True)
+    assert dx.shape == dg.shape == x.shape and dinit.shape == (0, 8)
+    assert gdn.gated_scan_bwd(None, x, out, x, want_dinit=False)[2] is None
+    assert not world["lib"].streams
+    with pytest.raises(ValueError, match="states"):
+        gdn.gated_scan_fwd(x, x, init_state=torch.zeros(1, 8))
