@@ -132,6 +132,9 @@ def load_library(path: str = LIB_PATH, build_if_missing: bool = False) -> ctypes
         lib.gdn_linear_cross_entropy_workspace_size.restype = _sz
         lib.gdn_linear_cross_entropy_fwd.argtypes = [_vp] * 5 + [_i32] * 3 + [_ci, _vp, _sz, _vp]
         lib.gdn_linear_cross_entropy_bwd.argtypes = [_vp] * 7 + [_i32] * 3 + [_ci, _vp, _sz, _vp]
+        lib.gdn_selftest_linear_cross_entropy_timeout.argtypes = [_i32, ctypes.c_uint32] + [_vp] * 7 + [_i32] * 3 + \
+            [_vp, _sz, _vp]
+        lib.gdn_selftest_linear_cross_entropy_timeout.restype = _ci
         for name in ("gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "layer_norm_fwd", "layer_norm_bwd",
                      "linear_cross_entropy_fwd", "linear_cross_entropy_bwd"):
             getattr(lib, "gdn_" + name).restype = _ci
@@ -772,6 +775,19 @@ def selftest_wait_timeout(workspace, limit_us=20000, stream=None):
     rc = load_library().gdn_selftest_wait_timeout(_ptr(workspace), int(limit_us), _stream(stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_selftest_wait_timeout")
+
+
+def selftest_linear_cross_entropy_timeout(step, h, weight, targets, lse, dloss, out0, out1, workspace, limit_us=20000,
+                                          stream=None):
+    """``gdn_selftest_linear_cross_entropy_timeout``: a cross-entropy call (``step`` 0 forward, 1 and 2 backward) one of
+    whose kernels waits in vain, gives up after ``limit_us`` and leaves NaN in the results that it reaches."""
+    N, D, V = _check_ce_args(h, weight, targets, [t for t in (lse, dloss) if t is not None])
+    _need_cuda(out0, out1, workspace)
+    rc = load_library().gdn_selftest_linear_cross_entropy_timeout(
+        step, limit_us, _ptr(h), _ptr(weight), _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(out0), _ptr(out1), N, D, V,
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_selftest_linear_cross_entropy_timeout")
 
 
 def chunk_fwd_noalloc(q, k, v, g, beta, out, final_state=None, init_state=None, cu_seqlens=None, scale=None,

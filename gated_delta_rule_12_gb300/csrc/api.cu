@@ -534,6 +534,32 @@ gdn_status gdn_linear_cross_entropy_bwd(const void *h, const void *weight, const
     return launch_linear_ce_bwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+gdn_status gdn_selftest_linear_cross_entropy_timeout(int32_t step, uint32_t limit_us, const void *h, const void *weight,
+                                                     const int32_t *targets, const float *lse, const float *dloss,
+                                                     void *out0, void *out1, int32_t N, int32_t D, int32_t V,
+                                                     void *workspace, size_t workspace_bytes, void *stream)
+{
+    LinearCeArgs a;
+    if (step < 0 || step > 2 || limit_us < 1 || limit_us > 1000000u) return GDN_ERR_INVALID_ARG;
+    const gdn_status s = ce_args(a, h, weight, targets, N, D, V, GDN_BF16, step > 0, workspace, workspace_bytes);
+    if (s != GDN_OK) return s;
+    if (!linear_ce_tc_supported(1, D)) return GDN_ERR_UNSUPPORTED;
+    if (N < 1 || !out0 || !aligned16(out0) || !aligned16(out1)) return GDN_ERR_INVALID_ARG;
+    CeStall stall;
+    stall.step = step;
+    stall.limit_ns = (uint64_t)limit_us * 1000u;
+    cudaError_t e;
+    if (step == 0) {
+        a.loss = (float *)out0; a.lse = (float *)out1;
+        e = launch_linear_ce_tc_fwd(a, (cudaStream_t)stream, stall);
+    } else {
+        if (!lse || !dloss || !aligned_to(lse, 4) || !aligned_to(dloss, 4)) return GDN_ERR_INVALID_ARG;
+        a.lse_in = lse; a.dloss = dloss; a.dh = out0; a.dw = out1;
+        e = launch_linear_ce_tc_bwd(a, (cudaStream_t)stream, stall);
+    }
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 gdn_status gdn_check_device_error(void *workspace, void *stream)
 {
     if (!workspace || ((uintptr_t)workspace & 255u) != 0) return GDN_ERR_INVALID_ARG;

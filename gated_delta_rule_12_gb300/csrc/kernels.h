@@ -111,8 +111,14 @@ cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st);
 // bf16 with D a multiple of 8 (rows that TMA can address) up to 2^24: the tensor cores
 bool linear_ce_tc_supported(int dt, int D);
 size_t linear_ce_tc_workspace_bytes(int N, int D, int V, bool backward);
-cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st);
-cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st);
+// The self-test's: in this kernel (0 the logits, 1 E, 2 the gradients) the first CTA pair's loads never come, and waits give
+// up after limit_ns.
+struct CeStall {
+    int step = -1;
+    uint64_t limit_ns = 0;
+};
+cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, CeStall stall = CeStall());
+cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st, CeStall stall = CeStall());
 size_t linear_ce_workspace_bytes(int N, int D, int V, int dt, bool backward);
 
 cudaError_t launch_chunk_simt(const ChunkArgs &a, cudaStream_t st);

@@ -27,7 +27,8 @@
 // surrounds them.
 //
 // Every wait on an mbarrier is bounded (1 s); a timeout records kDevErrTimeout in the workspace's error word, and the
-// CTA's roles unwind to the common exit, where both CTAs meet before tensor memory is freed.
+// CTA's roles unwind to the common exit, where both CTAs meet before tensor memory is freed.  Most callers never see that
+// word, so a CTA that gave up then writes NaN over all its tiles: the loss, or the rows and words that they reach, are NaN.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -79,6 +80,10 @@ struct CeParams {
     float *at;                // kLogits: [N]
     unsigned *err;
     int clear_err;            // the call's first kernel
+    void *out[2];             // kProb: E; kGrads: dW of the piece, dh or its slices
+    int pitch;                // kProb: elements a row of E
+    uint64_t limit_ns;        // of a wait
+    int silent;               // the self-test: the pair whose loads never come, else -1
 };
 
 struct CeMaps {
@@ -116,7 +121,7 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity)
 }
 
 // Bounded wait; false once this wait or another one of the CTA has given up.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned *err)
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, const CeParams &p)
 {
     if (try_wait_cluster(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
@@ -124,9 +129,9 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
         for (int i = 0; i < 16; ++i)
             if (try_wait_cluster(bar, parity)) return true;
         if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        if (globaltimer_ns() - t0 > p.limit_ns) {
             *abort_flag = 1;
-            atomicExch(err, kDevErrTimeout);
+            atomicExch(p.err, kDevErrTimeout);
             return false;
         }
     }
@@ -244,6 +249,33 @@ __device__ __forceinline__ Tile tile_of(const CeParams &p, int t)
     return r;
 }
 
+// NaN in this CTA's half of each of the pair's tiles.
+template <int MODE>
+__device__ __noinline__ void spoil(const CeParams &p, int pair, int pairs, int rank)
+{
+    for (int t = pair; t < p.tiles; t += pairs) {
+        const Tile c = tile_of<MODE>(p, t);
+        if (c.k0 >= c.k1) continue;
+        const int row0 = c.m * kTile + rank * kHalf, col0 = c.n * kTile;
+        const int rows = min(kHalf, (MODE == kGrads && c.which == 0 ? p.cols : p.N) - row0);
+        const int cols = min(kTile, (MODE == kGrads ? p.D : p.cols) - col0);
+        for (int i = threadIdx.x; i < rows * cols; i += kThreads) {
+            const int64_t row = row0 + i / cols;
+            const int col = col0 + i % cols;
+            if (MODE == kLogits) {
+                const float nan = __uint_as_float(0x7fffffffu);
+                p.part[(int64_t)c.n * p.N + row] = make_float2(nan, nan);
+            } else if (MODE == kProb) {
+                static_cast<unsigned short *>(p.out[0])[row * p.pitch + col] = 0x7fff;
+            } else if (c.which == 0 || p.direct) {
+                static_cast<unsigned short *>(p.out[c.which])[row * p.D + col] = 0x7fff;
+            } else {
+                static_cast<unsigned *>(p.out[1])[((int64_t)c.s * p.N + row) * p.D + col] = 0x7fffffffu;
+            }
+        }
+    }
+}
+
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CeParams p)
@@ -296,7 +328,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int t = pair; t < p.tiles && ok; t += pairs) {
+            for (int t = pair == p.silent ? p.tiles : pair; t < p.tiles && ok; t += pairs) {
                 const Tile c = tile_of<MODE>(p, t);
                 const Product &q = p.p[c.which];
                 const CUtensorMap *ma = &maps.a[c.which], *mb = &maps.b[c.which];
@@ -304,7 +336,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 const int m0 = c.m * kTile + (int)rank * kHalf, n0 = c.n * kTile + (int)rank * kHalf;
                 for (int k = c.k0; k < c.k1; ++k, ++it) {
                     const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-                    if (!wait_bar(empty + 8 * s, ph ^ 1, abort_flag, p.err)) { ok = false; break; }
+                    if (!wait_bar(empty + 8 * s, ph ^ 1, abort_flag, p)) { ok = false; break; }
                     const uint32_t bar = map_to_rank(full + 8 * s, 0);
                     if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * kStageBytes);
                     const uint32_t sa = base + s * kStageBytes, sb = sa + kStageBytes / 2;
@@ -325,7 +357,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
             // no copy and no arrival may come after the CTA has left: the last fills of the stages are read first
             const uint32_t n = it < (uint32_t)kStages ? it : kStages;
             for (uint32_t j = it - n; j < it && ok; ++j)
-                ok = wait_bar(empty + 8 * (j % kStages), (j / kStages) & 1, abort_flag, p.err);
+                ok = wait_bar(empty + 8 * (j % kStages), (j / kStages) & 1, abort_flag, p);
             if (!ok) {   // given up: copies in flight get 10 ms to land
                 const uint64_t t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(1000);
@@ -342,13 +374,13 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 const uint32_t idesc = idesc_bf16(kTile, kTile, a_mn, b_mn);
                 const uint32_t buf = tiles & 1, use = tiles >> 1;
                 ++tiles;
-                if (!wait_bar(acc_empty + 8 * buf, (use & 1) ^ 1, abort_flag, p.err)) break;
+                if (!wait_bar(acc_empty + 8 * buf, (use & 1) ^ 1, abort_flag, p)) break;
                 fence_after_sync();
                 const uint32_t d = tmem + buf * 256;
                 const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
                 for (int k = c.k0; k < c.k1; ++k, ++it) {
                     const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-                    if (!wait_bar(full + 8 * s, ph, abort_flag, p.err)) { ok = false; break; }
+                    if (!wait_bar(full + 8 * s, ph, abort_flag, p)) { ok = false; break; }
                     fence_after_sync();
                     const uint32_t sa = base + s * kStageBytes, sb = sa + kStageBytes / 2;
 #pragma unroll
@@ -384,7 +416,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
             }
             if (MODE == kGrads && c.which == 0) scale = __ldg(p.scale);
             const bool keep = (MODE == kGrads && !direct) || (target >= 0 && target < p.V);
-            if (!__all_sync(0xffffffffu, wait_bar(acc_full + 8 * buf, use & 1, abort_flag, p.err))) break;
+            if (!__all_sync(0xffffffffu, wait_bar(acc_full + 8 * buf, use & 1, abort_flag, p))) break;
             fence_after_sync();
             const uint32_t src = tmem + buf * 256 + (quarter << 21);   // lane field: bits 16 and up
             float top = -INFINITY, sum = 0.f;
@@ -490,6 +522,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
     fence_after_sync();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512u) : "memory");
+    if (*abort_flag) spoil<MODE>(p, pair, pairs, (int)rank);
 }
 
 // Joins a row's (max, sum) pairs: 32 rows a block, each warp a share of the `words` pairs of each, first the largest maximum,
@@ -690,8 +723,10 @@ cudaError_t launch_early(Kernel kernel, unsigned grid, unsigned threads, int sme
 }
 
 template <int MODE>
-cudaError_t launch(const CeMaps &maps, const CeParams &p, cudaStream_t st)
+cudaError_t launch(const CeMaps &maps, CeParams p, cudaStream_t st, const CeStall &stall)
 {
+    p.silent = stall.step == MODE ? 0 : -1;
+    p.limit_ns = stall.step == MODE ? stall.limit_ns : kWaitLimitNs;
     const cudaError_t e = cudaFuncSetAttribute(ce_tc_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int pairs = p.tiles < kPairs ? p.tiles : kPairs;
@@ -712,7 +747,7 @@ bool linear_ce_tc_supported(int dt, int D) { return dt == 1 && D % 8 == 0 && D <
 
 size_t linear_ce_tc_workspace_bytes(int N, int D, int V, bool backward) { return tc_layout(N, D, V, backward).total; }
 
-cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st)
+cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, CeStall stall)
 {
     const TcWorkspace ws = tc_layout(a.N, a.D, a.V, false);
     char *w = (char *)a.workspace;
@@ -729,12 +764,12 @@ cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st)
     p.at = (float *)(w + ws.at);
     p.err = (unsigned *)w;
     p.clear_err = 1;
-    const cudaError_t e = launch<kLogits>(maps, p, st);
+    const cudaError_t e = launch<kLogits>(maps, p, st, stall);
     if (e != cudaSuccess) return e;
     return launch_early(ce_tc_join_kernel, ceil_div(a.N, 32), 32 * kJoinWarps, 0, st, p, p.p[0].nt, a.loss, a.lse);
 }
 
-cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st)
+cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st, CeStall stall)
 {
     const TcWorkspace ws = tc_layout(a.N, a.D, a.V, true);
     char *w = (char *)a.workspace;
@@ -775,15 +810,19 @@ cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st)
         p.clear_err = v0 == 0;
         p.p[0] = {mt, ceil_div(cols, kTile), ceil_div(a.D, kDepth), 1, v0};
         p.tiles0 = p.tiles = mt * p.p[0].nt;
-        cudaError_t e = launch<kProb>(mg, p, st);
+        p.out[0] = w + ws.e;
+        p.pitch = ws.piece;
+        cudaError_t e = launch<kProb>(mg, p, st, stall);
         if (e != cudaSuccess) return e;
         p.p[0] = {ceil_div(cols, kTile), dt, ceil_div(a.N, kDepth), 1, 0};
         p.p[1] = {mt, dt, ceil_div(cols, kDepth), ws.slices, v0};
         p.tiles0 = a.dw ? p.p[0].mt * dt : 0;
         p.tiles = p.tiles0 + (a.dh ? mt * dt * ws.slices : 0);
         p.accumulate = v0 > 0;
+        p.out[0] = a.dw ? (char *)a.dw + (int64_t)v0 * a.D * 2 : nullptr;
+        p.out[1] = ws.direct ? a.dh : w + ws.acc;
         p.clear_err = 0;
-        e = launch<kGrads>(md, p, st);
+        e = launch<kGrads>(md, p, st, stall);
         if (e != cudaSuccess) return e;
     }
     if (!a.dh || ws.direct) return cudaSuccess;

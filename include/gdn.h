@@ -397,6 +397,7 @@ gdn_status gdn_layer_norm_bwd(const void *dout, const void *x, const float *mean
  *   workspace     at least gdn_linear_cross_entropy_workspace_size(..., backward = 0) bytes, 256-byte aligned (about
  *                 N V / 32 bytes); its first 256 bytes hold the device error word read by gdn_check_device_error (a
  *                 call with N = 0 leaves it as it is).
+ * A tensor-core kernel that gives up a wait (after 1 s) leaves NaN in what it should have written, besides that word.
  * Logits and sums are fp32.  bf16 with D a multiple of 8, up to 2^24, runs on the tensor cores, other sizes and fp32 on the
  * CUDA cores.  Results do not depend on timing.
  * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_CUDA.
@@ -425,6 +426,18 @@ gdn_status gdn_linear_cross_entropy_bwd(const void *h, const void *weight, const
                                         void *dh, void *dweight,
                                         int32_t N, int32_t D, int32_t V, gdn_dtype dt,
                                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Self-test of the cross entropy's failure path: the bf16 call (step 0: forward, out0 = loss, out1 = lse; steps 1 and 2:
+ * backward, out0 = dh, out1 = dweight; out1 may be NULL) in whose logits (0), softmax (1) or gradient (2) kernel the data of one tile never
+ * comes.  Its waits give up after limit_us microseconds (1 .. 1e6), nothing faults, gdn_check_device_error returns
+ * GDN_ERR_DEVICE_TIMEOUT, and the results that the tile reaches are NaN.
+ * Errors: as the calls; GDN_ERR_UNSUPPORTED where they would not take the tensor cores.
+ */
+gdn_status gdn_selftest_linear_cross_entropy_timeout(int32_t step, uint32_t limit_us, const void *h, const void *weight,
+                                                     const int32_t *targets, const float *lse, const float *dloss,
+                                                     void *out0, void *out1, int32_t N, int32_t D, int32_t V,
+                                                     void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * gdn_chunk_fwd_noalloc -- gdn_chunk_fwd for callers that cannot allocate.

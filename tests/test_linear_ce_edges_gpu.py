@@ -1,4 +1,5 @@
-"""The linear cross entropy at the ends of its sizes: many tokens, many words, long rows."""
+"""The linear cross entropy at the ends of its sizes: many tokens, many words, long rows; and
+what a call leaves whose data never come."""
 import pytest
 import torch
 
@@ -82,3 +83,42 @@ def test_very_long_rows(D):
     # G in bfloat16 and the result's own rounding; three terms of magnitude 1 at most
     assert ((ref.f64(dh[:, at]) - rh).abs() <= 2 * ref.BF16 * (G.abs() @ ref.f64(w[:, at]).abs())).all()
     assert ((ref.f64(dw[:, at]) - rw).abs() <= 2 * ref.BF16 * (G.abs().T @ ref.f64(h[:, at]).abs())).all()
+
+
+@pytest.mark.parametrize("step,V,want_dw", [(0, 700, True), (1, 700, True), (1, 3000, True), (2, 700, True), (2, 3000, True),
+                                            (2, 3000, False)])
+def test_a_wait_that_gives_up_leaves_nan(step, V, want_dw):
+    """One tile's loads never come: its waits end at their limit, the error word says so, and what the tile reaches is NaN
+    for callers who never read that word; the rest is as always, and so is the next call."""
+    N, D = 300, 128
+    gen = torch.Generator().manual_seed(step)
+    h, w = torch.randn((N, D), generator=gen).bfloat16().cuda(), (torch.randn((V, D), generator=gen) * 0.1).bfloat16().cuda()
+    t = torch.randint(0, V, (N,), generator=gen).to(torch.int32).cuda()
+    t[10], t[290] = -1, -1
+    dl = torch.rand(N, generator=gen).cuda()
+    ws = torch.empty(gdn.linear_cross_entropy_workspace_size(N, D, V, backward=step > 0), dtype=torch.uint8, device="cuda")
+    loss, lse = gdn.linear_cross_entropy_fwd(h, w, t)
+    good = (loss, lse) if step == 0 else gdn.linear_cross_entropy_bwd(h, w, t, lse, dl)
+    got = tuple(torch.zeros_like(v) for v in good)
+    if not want_dw:
+        got = (got[0], None)
+    gdn.selftest_linear_cross_entropy_timeout(step, h, w, t, lse, dl, *got, ws, limit_us=50000)
+    with pytest.raises(gdn.GDNError) as err:
+        gdn.check_device_error(ws)
+    assert err.value.code == 5
+    # the first tile of 256: rows of the tokens (0 and 1), rows of the words (1 and 2, or tokens again without dweight)
+    first = (torch.arange(N) < 256).cuda() & (t >= 0)
+    for i, (a, b) in enumerate(zip(got, good)):
+        if a is None:
+            continue
+        if step == 2 and i == 0 and want_dw:
+            lost = torch.zeros(N, dtype=torch.bool, device="cuda")
+        elif step > 0 and i == 1:
+            lost = (torch.arange(V) < 256).cuda()
+        else:
+            lost = first
+        assert torch.isnan(a[lost]).all() and torch.equal(a[~lost], b[~lost]), (step, i)
+    again = gdn.linear_cross_entropy_fwd(h, w, t, workspace=ws) if step == 0 else \
+        gdn.linear_cross_entropy_bwd(h, w, t, lse, dl, workspace=ws)
+    gdn.check_device_error(ws)
+    assert all(torch.equal(a, b) for a, b in zip(again, good))

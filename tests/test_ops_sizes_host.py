@@ -1,4 +1,4 @@
-"""Sizes near the ends of their types; no GPU is needed."""
+"""Sizes near the ends of their types, and refusals of the cross entropy's self-test; no GPU is needed."""
 import pytest
 import torch
 
@@ -45,3 +45,16 @@ def test_sizes_beyond_32_bits_are_refused(call):
 def test_workspaces_of_sizes_beyond_32_bits():
     assert gdn.layer_norm_bwd_workspace_size(3, BIG) == 0
     assert gdn.linear_cross_entropy_workspace_size(BIG, 8, 5) == gdn.linear_cross_entropy_workspace_size(4, 8, BIG) == 0
+
+
+FAKE = 1 << 20
+STALL = dict(step=1, limit=1000, h=FAKE, w=FAKE, t=FAKE, lse=FAKE, dl=FAKE, out0=FAKE, out1=FAKE, N=4, D=16, V=32, ws=FAKE,
+             wsb=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("over,code", [(dict(step=-1), 1), (dict(step=3), 1), (dict(limit=0), 1), (dict(limit=1000001), 1),
+                                       (dict(h=None), 1), (dict(lse=None), 1), (dict(dl=FAKE + 2), 1), (dict(out0=None), 1),
+                                       (dict(out1=FAKE + 8), 1), (dict(N=0), 1), (dict(D=12), 2), (dict(ws=None), 3),
+                                       (dict(wsb=64), 3)])
+def test_selftest_refusals(over, code):
+    assert gdn.load_library().gdn_selftest_linear_cross_entropy_timeout(*{**STALL, **over}.values()) == code
