@@ -98,3 +98,26 @@ def test_the_widest_row():
     x[0, 0, -3:] = 5.0
     out, fin = gdn.gated_scan_fwd(x, torch.zeros_like(x))
     assert torch.equal(out, x) and (fin[0, -3:] == 5).all() and (fin[0, :-3] == 2).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D,gate", [(16, False), (13, True)])
+@pytest.mark.parametrize("cu", [[0, 0, 9000, 9007, 9007, 12000], [0, 4001, 4001, 4002, 11000], [0, 8577]])
+def test_packed_sequences_in_clusters(cu, D, dtype, gate):
+    """Few channels over a long time: the CTAs of a cluster share each sequence, those without a token and those shorter
+    than one CTA's rows among them."""
+    gen = torch.Generator().manual_seed(cu[-1] + D)
+    r = lambda *s: torch.randn(s, generator=gen)  # noqa: E731
+    T, N = cu[-1], len(cu) - 1
+    x, dout = r(1, T, D).to(DT[dtype]).cuda(), r(1, T, D).to(DT[dtype]).cuda()
+    g = (-0.1 * torch.nn.functional.softplus(r(1, T, D))).to(DT[dtype]).cuda()
+    init, dfin = r(N, D).cuda(), r(N, D).cuda()
+    c = torch.tensor(cu, dtype=torch.int32).cuda()
+    out, fin = gdn.gated_scan_fwd(x, g, init_state=init, cu_seqlens=c, input_gate=gate)
+    ro, rf, bo, bf = ref.scan_fwd(x, g, init, c, gate)
+    ref.check(out, ro, bo, "out")
+    ref.check(fin, rf, bf, "final state")
+    grads = gdn.gated_scan_bwd(x, g, out, dout, init_state=init, dfinal_state=dfin, cu_seqlens=c, input_gate=gate)
+    rg, bg = ref.scan_bwd(x, g, out, dout, init, dfin, c, gate)
+    for got, want, b, name in zip(grads, rg, bg, ("dx", "dg", "dinit")):
+        ref.check(got, want, b, name)

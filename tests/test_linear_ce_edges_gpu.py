@@ -1,5 +1,5 @@
-"""The linear cross entropy at the ends of its sizes: many tokens, many words, long rows; and
-what a call leaves whose data never come."""
+"""The linear cross entropy at the ends of its sizes: many tokens, many words in several
+pieces, long rows; and what a call leaves whose data never come."""
 import pytest
 import torch
 
@@ -122,3 +122,42 @@ def test_a_wait_that_gives_up_leaves_nan(step, V, want_dw):
         gdn.linear_cross_entropy_bwd(h, w, t, lse, dl, workspace=ws)
     gdn.check_device_error(ws)
     assert all(torch.equal(a, b) for a, b in zip(again, good))
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 20), ("bf16", 61), ("bf16", 64)])
+def test_several_pieces_of_the_vocabulary(dtype, D):
+    """More tokens times words than one piece of the backward pass takes, the last piece partial and odd."""
+    N, V = (700, 30011) if (dtype, D) != ("bf16", 64) else (3000, 23001)
+    gen = torch.Generator().manual_seed(3)
+    h = torch.randn((N, D), generator=gen).to(DT[dtype]).cuda()
+    w = (torch.randn((V, D), generator=gen) * (2 * D ** -0.5)).to(DT[dtype]).cuda()
+    t = torch.randint(-V // 10, V, (N,), generator=gen).to(torch.int32).cuda()
+    t[:4] = torch.tensor([0, V - 1, V, -1])
+    dl = (torch.rand(N, generator=gen) / N).cuda()
+    loss, lse = gdn.linear_cross_entropy_fwd(h, w, t)
+    dh, dw = gdn.linear_cross_entropy_bwd(h, w, t, lse, dl)
+    rv, bd = ref.ce_fwd(h, w, t)
+    ref.check(loss, rv[0], bd[0], "loss")
+    ref.check(lse, rv[1], bd[1], "lse")
+    rv, bd = ref.ce_bwd(h, w, t, lse, dl, low_bits=dtype == "bf16" and D == 64)
+    ref.check(dh, rv[0], bd[0], "dh")
+    ref.check(dw, rv[1], bd[1], "dweight")
+
+
+@pytest.mark.parametrize("N", [8193, 16700])
+def test_more_tokens_than_a_group_of_row_tiles(N):
+    """Beyond 8192 tokens the tensor cores' row tiles come in several groups, the last one smaller."""
+    D, V = 24, 700
+    gen = torch.Generator().manual_seed(N)
+    h = torch.randn((N, D), generator=gen).bfloat16().cuda()
+    w = (torch.randn((V, D), generator=gen) * (2 * D ** -0.5)).bfloat16().cuda()
+    t = torch.randint(-V // 10, V, (N,), generator=gen).to(torch.int32).cuda()
+    dl = (torch.rand(N, generator=gen) / N).cuda()
+    loss, lse = gdn.linear_cross_entropy_fwd(h, w, t)
+    dh, dw = gdn.linear_cross_entropy_bwd(h, w, t, lse, dl)
+    rv, bd = ref.ce_fwd(h, w, t)
+    ref.check(loss, rv[0], bd[0], "loss")
+    ref.check(lse, rv[1], bd[1], "lse")
+    rv, bd = ref.ce_bwd(h, w, t, lse, dl, low_bits=True)
+    ref.check(dh, rv[0], bd[0], "dh")
+    ref.check(dw, rv[1], bd[1], "dweight")
