@@ -9,8 +9,9 @@
 // Bound by memory: three tensors forward, five backward (six with the gate), at 3 and 6 operations an element.  What
 // keeps the kernel from that bound is the number of instructions an element and the latency of the joins along time,
 // hence pairs of channels in one instruction and few, long iterations.  Measured (GB300, bf16, device time): 4 x 2048 x
-// 2048 forward 23.8 us (4.2 TB/s), backward 32.5 us (5.2 TB/s); 19 x 2048 x 1024, which fills the SMs evenly, forward
-// 39.5 us (6.1 TB/s); 8 packed sequences, 32768 x 2048, forward 91.7 us (4.4 TB/s); a step of 256 x 2048 2.1 us.
+// 2048, 128 CTAs for 152 SMs, forward 23.5 us (4.3 TB/s), backward 32.5 us (5.2 TB/s); 19 x 2048 x 1024, which fills the
+// SMs evenly, forward 39.5 us (6.1 TB/s); 8 packed sequences, 32768 x 2048, forward 92 us (4.4 TB/s; by their lengths 90
+// to 100); a step of 256 x 2048 2.1 us.
 #include "common.cuh"
 #include "kernels.h"
 #include "pairs.cuh"
@@ -730,8 +731,9 @@ __global__ void __launch_bounds__(256) scan_step_kernel(float *state, const T *x
 // Rows of 128 bytes (16 lanes) come first; where they make fewer than 80 CTAs, narrower ones, whose groups in the warp
 // go along time instead, make more CTAs of more rows (device time of the forward pass, bf16, N x T x D, with 16, 8 and
 // 4 lanes a row: 64 x 2048 x 512 73, 76, 94 us; 11 x 3292 x 256 36, 21, 21 us; 2 x 4096 x 1024 44, 24, 15 us).  Packed
-// sequences of unequal lengths are held up by the longest and take more CTAs (8 sequences, 32768 x 2048: 185, 115, 108
-// before the rows were padded apart in shared memory).  16 warps a CTA measured slower throughout (2 x 4096 x 1024: 17).
+// sequences of unequal lengths are held up by the longest and take more CTAs (forward, 32768 x 2048 in 8 sequences 146, 99,
+// 92 us, in 16 85, 77, 99, in 30 80, 88, 117; 32768 x 1024 in 8 133, 83, 61; backward in 8 198, 141, 145, in 16 127, 110,
+// 147).  16 warps a CTA measured slower throughout (2 x 4096 x 1024: 17).
 //
 // A cluster's join adds 2 to 3 us an iteration (4 x 2048 x 2048 in clusters of two: 75 us instead of 24), so clusters
 // serve only where 32-byte rows still leave most SMs idle over a long time, and no more of them than the GPU holds at

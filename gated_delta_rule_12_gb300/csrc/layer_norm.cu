@@ -7,14 +7,15 @@
 // Bound by memory: x and y forward; dy, x and dx backward.  A team of threads holds a row in registers, so each row is
 // read once; the variance comes from the deviations in registers.  A thread keeps the same columns for every row of
 // its team: w and b are read once a thread, and dw and db gather in registers, join over the CTA's teams in shared
-// memory and leave one partial row a CTA, which a second kernel adds up.  Rows come four ahead through asynchronous
-// copies: 32 KB of them in flight on an SM, as registers one row ahead allow, held the backward pass to 3.9 TB/s and
-// the norm over heads (131072 x 128) to 2.6.  Rows of more than 16384 elements go through kernels that read them again.
+// memory and leave one partial row a CTA, which a second kernel adds up.  Rows come up to four ahead through asynchronous
+// copies (one at a time, overlapping nothing, where two stages do not fit: backward, fp32 rows beyond 11264): 32 KB of them in flight on an SM, as registers one row ahead allow, held the backward pass to 3.9 TB/s and
+// the norm over heads (131072 x 128) to 2.6.  Rows of more than 16384 elements go through
+// kernels that read them again, element by element (2000 x 32768 fp32 forward 225 us, 0.35 of the copy rate).
 // Rows of other lengths than 16-byte accesses fit go by the 16-byte chunks that they lie in (48841 x 687 bf16: forward
 // 32 us, backward 54 us; element by element 93 and 173), unless their tensors start elsewhere.
 //
-// Measured (GB300, bf16, device time): forward 8192 x 2048 15.1 us (4.4 TB/s); backward 25.2 us, 131072 x 128 backward
-// 24.0 us (4.0 and 4.2 TB/s), of which about 3 us are the second kernel and the gap before it.
+// Measured (GB300, bf16, device time): forward 8192 x 2048 14.8 us (4.5 TB/s); backward 25.7 us, 131072 x 128 backward
+// 24.2 us (3.9 and 4.2 TB/s), of which about 3 us are the second kernel and the gap before it.
 #include "common.cuh"
 #include "kernels.h"
 #include "pairs.cuh"
@@ -367,8 +368,8 @@ __global__ void __launch_bounds__(MAX, MAX == 512 && NV * VW <= 8 ? 2 : 1) rows_
     __shared__ __align__(16) float sh[2 * 32 * 2];
     using Rows = Ring<T, VW, NV, 2, MAX>;
     // Teams of more than 512 threads have 64 registers each.  They read a row from the ring again behind its sums, and
-    // the weight from shared memory, instead of keeping both (3581 x 9368 bf16: 76 us, 118 with
-    // them spilled).
+    // the weight from shared memory, instead of keeping both (3581 x 9368 bf16: 76 us, 118 with them spilled; some
+    // instances still spill 20 to 190 bytes).
     constexpr bool kAgain = MAX == 1024;
     const int stages = kAgain ? again_stages(Rows::stage_bytes(blockDim.x), blockDim.x) : Rows::kStages;
     const Rows ring(smem);

@@ -362,8 +362,8 @@ gdn_status gdn_gated_scan_step(float *state, const void *x, const void *g, void 
  *   x, out        [rows, D] dtype dt, contiguous; out may alias x.
  *   weight, bias  [D] fp32, or NULL for 1 and 0.
  *   mean, rstd    [rows] fp32, or NULL to skip; the backward pass needs them.
- *   rows >= 0, D >= 1, rows * D <= 2^48, eps >= 0; pointers aligned to their element size (x and out 16-byte
- *   aligned with D a multiple of 8 take the fast path).
+ *   rows >= 0, D >= 1, rows * D <= 2^48, eps >= 0; pointers aligned to their element size (x and out that start on
+ *   16-byte boundaries take the fast path up to D = 16384, whatever D is).
  * Statistics are fp32, the variance from the deviations from the mean.
  * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
  */
@@ -395,7 +395,7 @@ gdn_status gdn_layer_norm_bwd(const void *dout, const void *x, const float *mean
  *   loss          [N] fp32;  lse [N] fp32 or NULL to skip (the backward pass needs it).
  *   0 <= N <= 2^23, D >= 1, 1 <= V <= 2^30, N V <= 2^45 (beyond: GDN_ERR_UNSUPPORTED).
  *   workspace     at least gdn_linear_cross_entropy_workspace_size(..., backward = 0) bytes, 256-byte aligned (about
- *                 N V / 32 bytes); its first 256 bytes hold the device error word read by gdn_check_device_error (a
+ *                 N V / 32 bytes, on the CUDA cores N V / 16); its first 256 bytes hold the device error word read by gdn_check_device_error (a
  *                 call with N = 0 leaves it as it is).
  * A tensor-core kernel that gives up a wait (after 1 s) leaves NaN in what it should have written, besides that word.
  * Logits and sums are fp32.  bf16 with D a multiple of 8, up to 2^24, runs on the tensor cores, other sizes and fp32 on the
@@ -416,8 +416,8 @@ gdn_status gdn_linear_cross_entropy_fwd(const void *h, const void *weight, const
  *   dh            [N, D] dtype dt or NULL to skip;  dweight [V, D] dtype dt or NULL to skip.  Overwritten; both
  *                 16-byte aligned.
  * Ignored rows get a zero dh and add nothing to dweight, whatever their h and dloss hold.
- *   workspace     as the forward call, with backward = 1: up to 128 MB for a piece of the vocabulary, a copy of h and
- *                 fp32 sums of dh.
+ *   workspace     as the forward call, with backward = 1: a piece of the vocabulary (up to 128 MB, on the CUDA cores 64
+ *                 MB, but 512 bytes a token at least), fp32 sums of dh and, on the tensor cores, a copy of h.
  * On the tensor cores softmax - onehot enters the products rounded to bf16, and so does dloss h, in units of the largest
  * |dloss| (exact where all rows weigh the same); sums are fp32.  Errors as the forward call.
  */
