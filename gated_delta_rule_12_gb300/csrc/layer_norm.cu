@@ -8,9 +8,10 @@
 // read once; the variance comes from the deviations in registers.  A thread keeps the same columns for every row of
 // its team: w and b are read once a thread, and dw and db gather in registers, join over the CTA's teams in shared
 // memory and leave one partial row a CTA, which a second kernel adds up.  Rows come up to four ahead through asynchronous
-// copies (one at a time, overlapping nothing, where two stages do not fit: backward, fp32 rows beyond 11264): 32 KB of them in flight on an SM, as registers one row ahead allow, held the backward pass to 3.9 TB/s and
-// the norm over heads (131072 x 128) to 2.6.  Rows of more than 16384 elements go through
-// kernels that read them again, element by element (2000 x 32768 fp32 forward 225 us, 0.35 of the copy rate).
+// copies: 32 KB of them in flight on an SM, as registers one row ahead allow, held the backward pass to 3.9 TB/s and the
+// norm over heads (131072 x 128) to 2.6.  (Where two stages do not fit, backward with fp32 rows beyond 11264 elements, a
+// row's copies overlap nothing.)  Rows of more than 16384 elements go through kernels that read them again, element by
+// element (2000 x 32768 fp32 forward 225 us, 0.35 of the copy rate).
 // Rows of other lengths than 16-byte accesses fit go by the 16-byte chunks that they lie in (48841 x 687 bf16: forward
 // 32 us, backward 54 us; element by element 93 and 173), unless their tensors start elsewhere.
 //

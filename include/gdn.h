@@ -395,8 +395,8 @@ gdn_status gdn_layer_norm_bwd(const void *dout, const void *x, const float *mean
  *   loss          [N] fp32;  lse [N] fp32 or NULL to skip (the backward pass needs it).
  *   0 <= N <= 2^23, D >= 1, 1 <= V <= 2^30, N V <= 2^45 (beyond: GDN_ERR_UNSUPPORTED).
  *   workspace     at least gdn_linear_cross_entropy_workspace_size(..., backward = 0) bytes, 256-byte aligned (about
- *                 N V / 32 bytes, on the CUDA cores N V / 16); its first 256 bytes hold the device error word read by gdn_check_device_error (a
- *                 call with N = 0 leaves it as it is).
+ *                 N V / 32 bytes, on the CUDA cores N V / 16); its first 256 bytes hold the device error word read by
+ *                 gdn_check_device_error (a call with N = 0 leaves it as it is).
  * A tensor-core kernel that gives up a wait (after 1 s) leaves NaN in what it should have written, besides that word.
  * Logits and sums are fp32.  bf16 with D a multiple of 8, up to 2^24, runs on the tensor cores, other sizes and fp32 on the
  * CUDA cores.  Results do not depend on timing.
@@ -429,9 +429,9 @@ gdn_status gdn_linear_cross_entropy_bwd(const void *h, const void *weight, const
 
 /*
  * Self-test of the cross entropy's failure path: the bf16 call (step 0: forward, out0 = loss, out1 = lse; steps 1 and 2:
- * backward, out0 = dh, out1 = dweight; out1 may be NULL) in whose logits (0), softmax (1) or gradient (2) kernel the data of one tile never
- * comes.  Its waits give up after limit_us microseconds (1 .. 1e6), nothing faults, gdn_check_device_error returns
- * GDN_ERR_DEVICE_TIMEOUT, and the results that the tile reaches are NaN.
+ * backward, out0 = dh, out1 = dweight; out1 may be NULL) in whose logits (0), softmax (1) or gradient (2) kernel the data
+ * of one tile never comes.  Its waits give up after limit_us microseconds (1 .. 1e6), nothing faults,
+ * gdn_check_device_error returns GDN_ERR_DEVICE_TIMEOUT, and the results that the tile reaches are NaN.
  * Errors: as the calls; GDN_ERR_UNSUPPORTED where they would not take the tensor cores.
  */
 gdn_status gdn_selftest_linear_cross_entropy_timeout(int32_t step, uint32_t limit_us, const void *h, const void *weight,
