@@ -25,6 +25,11 @@ Entry points (same names as the C ABI, without the ``gdn_`` prefix):
     gated_scan_step(state, x, g)          -> out            (state updated in place)
     layer_norm_fwd(x, weight, bias, eps)  -> (out, mean, rstd)
     layer_norm_bwd(dout, x, mean, rstd, weight) -> (dx, dweight, dbias)
+    rms_norm_fwd(x, weight, residual, eps) -> (out, residual_out, rstd)   residual_out = x + residual
+    rms_norm_bwd(dout, x, rstd, weight, dresidual) -> (dx, dweight)
+    rms_norm_fp8(x, weight, residual, eps) -> (q, scales, residual_out)   the norm, its output in 8 bits
+    fp8_quantize(x, block_rows)           -> (q, scales)    e4m3 with a scale for each block of 128
+    fp8_linear(x, x_scales, weight, weight_scales) -> out [M,N] bf16
     linear_cross_entropy_fwd(h, weight, targets) -> (loss, lse)   no logits array
     linear_cross_entropy_bwd(h, weight, targets, lse, dloss) -> (dh, dweight)
     check_device_error(workspace)         -> None or raises
@@ -51,6 +56,8 @@ EXPORTS = ["gdn_status_string", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd_k
            "gdn_check_device_error", "gdn_chunk_fwd_noalloc", "gdn_prologue_chunk_fwd_workspace_size",
            "gdn_prologue_chunk_fwd", "gdn_gated_scan_fwd", "gdn_gated_scan_bwd", "gdn_gated_scan_step",
            "gdn_layer_norm_fwd", "gdn_layer_norm_bwd_workspace_size", "gdn_layer_norm_bwd",
+           "gdn_rms_norm_fwd", "gdn_rms_norm_fp8", "gdn_rms_norm_bwd_workspace_size", "gdn_rms_norm_bwd",
+           "gdn_fp8_quantize", "gdn_fp8_linear_workspace_size", "gdn_fp8_linear",
            "gdn_linear_cross_entropy_workspace_size", "gdn_linear_cross_entropy_fwd",
            "gdn_linear_cross_entropy_bwd"]
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -128,6 +135,16 @@ def load_library(path: str = LIB_PATH, build_if_missing: bool = False) -> ctypes
         lib.gdn_layer_norm_bwd_workspace_size.argtypes = [ctypes.c_int64, _i32, _ci]
         lib.gdn_layer_norm_bwd_workspace_size.restype = _sz
         lib.gdn_layer_norm_bwd.argtypes = [_vp] * 8 + [ctypes.c_int64, _i32, _ci, _vp, _sz, _vp]
+        _i64 = ctypes.c_int64
+        lib.gdn_rms_norm_fwd.argtypes = [_vp] * 6 + [_i64, _i32, _ci, _f32, _vp]
+        lib.gdn_rms_norm_fp8.argtypes = [_vp] * 6 + [_i64, _i32, _ci, _f32, _vp]
+        lib.gdn_rms_norm_bwd_workspace_size.argtypes = [_i64, _i32, _ci]
+        lib.gdn_rms_norm_bwd_workspace_size.restype = _sz
+        lib.gdn_rms_norm_bwd.argtypes = [_vp] * 7 + [_i64, _i32, _ci, _vp, _sz, _vp]
+        lib.gdn_fp8_quantize.argtypes = [_vp] * 3 + [_i64, _i32, _i32, _ci, _vp]
+        lib.gdn_fp8_linear_workspace_size.argtypes = [_i32] * 3
+        lib.gdn_fp8_linear_workspace_size.restype = _sz
+        lib.gdn_fp8_linear.argtypes = [_vp] * 5 + [_i32] * 3 + [_vp, _sz, _vp]
         lib.gdn_linear_cross_entropy_workspace_size.argtypes = [_i32] * 3 + [_ci, _i32]
         lib.gdn_linear_cross_entropy_workspace_size.restype = _sz
         lib.gdn_linear_cross_entropy_fwd.argtypes = [_vp] * 5 + [_i32] * 3 + [_ci, _vp, _sz, _vp]
@@ -136,6 +153,7 @@ def load_library(path: str = LIB_PATH, build_if_missing: bool = False) -> ctypes
             [_vp, _sz, _vp]
         lib.gdn_selftest_linear_cross_entropy_timeout.restype = _ci
         for name in ("gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "layer_norm_fwd", "layer_norm_bwd",
+                     "rms_norm_fwd", "rms_norm_fp8", "rms_norm_bwd", "fp8_quantize", "fp8_linear",
                      "linear_cross_entropy_fwd", "linear_cross_entropy_bwd"):
             getattr(lib, "gdn_" + name).restype = _ci
         _lib = lib
@@ -459,7 +477,7 @@ def prologue_chunk_fwd(xq, xk, xv, wq, wk, wv, a, b, A_log, dt_bias, conv_state_
 
 # Calls of a few microseconds are held up by what surrounds them, so the wrappers below look torch's attributes up once
 # and take the current stream as the raw handle (0.1 us; the stream object takes 3).
-_F32, _BF16 = torch.float32, torch.bfloat16
+_F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
 _empty, _empty_like = torch.empty, torch.empty_like
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -686,6 +704,195 @@ def layer_norm_bwd(dout, x, mean, rstd, weight=None, workspace=None, stream=None
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_layer_norm_bwd")
     return dx, dw, db
+
+
+def _check_rms_args(x, weight, stats, same):
+    """Shapes, dtypes, placement and contiguity of a root-mean-square norm's call; returns (rows, D)."""
+    shape = x.shape
+    if not shape or shape[-1] < 1:
+        raise ValueError("x must be [..., D] with D >= 1")
+    D = shape[-1]
+    if D > _MOST:
+        _too_large(D=D)
+    rows = x.numel() // D
+    if weight is not None:
+        if weight.dtype is not _F32:
+            raise TypeError("weight must be float32")
+        if weight.shape != (D,):
+            raise ValueError("weight must be [D]")
+    for t in stats:
+        if t.dtype is not _F32:
+            raise TypeError("rstd must be float32")
+        if t.numel() != rows:
+            raise ValueError("rstd must hold one value a row")
+    for t in same:
+        if t is not None:
+            if t.dtype is not x.dtype:
+                raise TypeError("x and the other row tensors must share one dtype")
+            if t.shape != shape:
+                raise ValueError("x and the other row tensors must share one shape")
+    _need_cuda(x, weight, *stats, *same)
+    return rows, D
+
+
+def _rms_rows(x, weight, residual, residual_out, out=None):
+    """What the two forward calls check alike: (rows, D, residual_out).  Everything in order takes the short way."""
+    shape = x.shape
+    D = shape[-1] if shape else 0
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out goes with a residual")
+    if 0 < D <= _MOST and out is None and residual_out is None and x.is_cuda and x.is_contiguous() and \
+            (weight is None or (_sound(weight, _F32) and weight.shape == (D,))) and \
+            (residual is None or (_sound(residual, x.dtype) and residual.shape == shape)):
+        rows = x.numel() // D
+    else:
+        rows, D = _check_rms_args(x, weight, (), (residual, residual_out, out))
+    if residual is not None and residual_out is None:
+        residual_out = _empty_like(x)
+    return rows, D, residual_out
+
+
+def rms_norm_fwd(x, weight=None, residual=None, eps=1e-5, out=None, residual_out=None, stream=None):
+    """Root-mean-square norm over the last axis, the residual added first (``gdn_rms_norm_fwd``).
+
+    x, residual [..., D] (fp32 or bf16, one dtype); weight [D] fp32 or None.  Returns ``(out, residual_out, rstd)``:
+    residual_out is x + residual in their dtype (None without a residual; it may be given, and may be ``residual``
+    itself), out its norm, rstd fp32 of shape ``x.shape[:-1]``."""
+    if stream is not None:
+        return _elsewhere(stream, rms_norm_fwd, x, weight, residual, eps, out, residual_out)
+    lib = _lib or load_library()
+    rows, D, residual_out = _rms_rows(x, weight, residual, residual_out, out)
+    dt = _dt(x)
+    if out is None:
+        out = _empty_like(x)
+    rstd = _empty(x.shape[:-1], dtype=_F32, device=x.device)
+    rc = lib.gdn_rms_norm_fwd(x.data_ptr(), _ptr(residual), None if weight is None else weight.data_ptr(), out.data_ptr(),
+                              _ptr(residual_out), rstd.data_ptr(), rows, D, dt, eps, _stream_of(x))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_rms_norm_fwd")
+    return out, residual_out, rstd
+
+
+def rms_norm_fp8(x, weight=None, residual=None, eps=1e-5, residual_out=None, stream=None):
+    """``rms_norm_fwd`` with an output in 8 bits for ``fp8_linear`` (``gdn_rms_norm_fp8``).
+
+    Returns ``(q, scales, residual_out)``: q [..., D] float8_e4m3fn in units of scales [..., ceil(D / 128)] fp32."""
+    if stream is not None:
+        return _elsewhere(stream, rms_norm_fp8, x, weight, residual, eps, residual_out)
+    lib = _lib or load_library()
+    rows, D, residual_out = _rms_rows(x, weight, residual, residual_out)
+    dt = _dt(x)
+    q = _empty_like(x, dtype=_E4M3)
+    scales = _empty((*x.shape[:-1], -(-D // 128)), dtype=_F32, device=x.device)
+    rc = lib.gdn_rms_norm_fp8(x.data_ptr(), _ptr(residual), None if weight is None else weight.data_ptr(), q.data_ptr(),
+                              scales.data_ptr(), _ptr(residual_out), rows, D, dt, eps, _stream_of(x))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_rms_norm_fp8")
+    return q, scales, residual_out
+
+
+def rms_norm_bwd_workspace_size(rows, D, dtype=torch.bfloat16) -> int:
+    dt = GDN_BF16 if dtype == _BF16 else GDN_F32
+    if D > _MOST:
+        return 0
+    return int(load_library().gdn_rms_norm_bwd_workspace_size(rows, D, dt))
+
+
+def rms_norm_bwd(dout, x, rstd, weight=None, dresidual=None, workspace=None, stream=None):
+    """Backward of ``rms_norm_fwd`` (``gdn_rms_norm_bwd``): returns ``(dx, dweight)``, the second [D] fp32.
+
+    ``x`` is what was normed, the forward's residual_out where a residual was added; ``dresidual`` the gradient that comes
+    to residual_out from elsewhere, or None.  dx is the gradient of the forward's x and of its residual alike."""
+    if stream is not None:
+        return _elsewhere(stream, rms_norm_bwd, dout, x, rstd, weight, dresidual, workspace)
+    lib = _lib or load_library()
+    rows, D = _check_rms_args(x, weight, (rstd,), (dout, dresidual))
+    dt = _dt(x)
+    device = x.device
+    dx = _empty_like(x)
+    dw = _empty(D, dtype=_F32, device=device)
+    ws, size = _workspace(workspace, 0 if workspace is not None else lib.gdn_rms_norm_bwd_workspace_size(rows, D, dt),
+                          device)
+    rc = lib.gdn_rms_norm_bwd(dout.data_ptr(), x.data_ptr(), rstd.data_ptr(), _ptr(weight), _ptr(dresidual),
+                              dx.data_ptr(), dw.data_ptr(), rows, D, dt, ws.data_ptr(), size, _stream_of(x))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_rms_norm_bwd")
+    return dx, dw
+
+
+def fp8_quantize(x, block_rows=1, stream=None):
+    """Values to e4m3 in units of a scale for each block of 128 columns (``gdn_fp8_quantize``).
+
+    x [..., D] (fp32 or bf16).  Returns ``(q, scales)``: q float8_e4m3fn of x's shape; scales fp32 [..., ceil(D / 128)]
+    with ``block_rows`` 1 (activations), or [ceil(R / 128), ceil(D / 128)] with 128 (weights, x [R, D])."""
+    if stream is not None:
+        return _elsewhere(stream, fp8_quantize, x, block_rows)
+    lib = _lib or load_library()
+    shape = x.shape
+    if not shape or shape[-1] < 1:
+        raise ValueError("x must be [..., D] with D >= 1")
+    if block_rows not in (1, 128) or (block_rows == 128 and len(shape) != 2):
+        raise ValueError("block_rows must be 1, or 128 with x [R, D]")
+    D = shape[-1]
+    if D > _MOST:
+        _too_large(D=D)
+    rows = x.numel() // D
+    dt = _dt(x)
+    _need_cuda(x)
+    q = _empty_like(x, dtype=_E4M3)
+    lead = shape[:-1] if block_rows == 1 else (-(-rows // 128),)
+    scales = _empty((*lead, -(-D // 128)), dtype=_F32, device=x.device)
+    rc = lib.gdn_fp8_quantize(x.data_ptr(), q.data_ptr(), scales.data_ptr(), rows, D, block_rows, dt, _stream_of(x))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_fp8_quantize")
+    return q, scales
+
+
+def fp8_linear_workspace_size(M, N, K) -> int:
+    if max(M, N, K) > _MOST:
+        return 0
+    return int(load_library().gdn_fp8_linear_workspace_size(M, N, K))
+
+
+def fp8_linear(x, x_scales, weight, weight_scales, out=None, workspace=None, stream=None):
+    """Product ``x @ weight.T`` of 8-bit operands with scales (``gdn_fp8_linear``).
+
+    x [..., K] float8_e4m3fn with x_scales [..., ceil(K / 128)] fp32 (``rms_norm_fp8``, ``fp8_quantize``); weight [N, K]
+    float8_e4m3fn with weight_scales [ceil(N / 128), ceil(K / 128)] fp32 (``fp8_quantize`` with block_rows 128).  Returns
+    out [..., N] bf16."""
+    if stream is not None:
+        return _elsewhere(stream, fp8_linear, x, x_scales, weight, weight_scales, out, workspace)
+    lib = _lib or load_library()
+    xs, ws = x.shape, weight.shape
+    if len(xs) < 1 or len(ws) != 2 or xs[-1] != ws[1]:
+        raise ValueError("x must be [..., K] and weight [N, K]")
+    N, K = ws
+    if N < 1 or K < 1:
+        raise ValueError("N and K must be 1 or more")
+    M = x.numel() // K
+    if max(M, N, K) > _MOST:
+        _too_large(M=M, N=N, K=K)
+    blocks = -(-K // 128)
+    if x.dtype is not _E4M3 or weight.dtype is not _E4M3:
+        raise TypeError("x and weight must be float8_e4m3fn")
+    if x_scales.dtype is not _F32 or weight_scales.dtype is not _F32:
+        raise TypeError("scales must be float32")
+    if x_scales.shape != (*xs[:-1], blocks) or weight_scales.shape != (-(-N // 128), blocks):
+        raise ValueError("x_scales must be [..., ceil(K / 128)], weight_scales [ceil(N / 128), ceil(K / 128)]")
+    shape = (*xs[:-1], N)
+    if out is None:
+        out = _empty(shape, dtype=_BF16, device=x.device)
+    elif out.dtype is not _BF16:
+        raise TypeError("out must be bfloat16")
+    elif out.shape != shape:
+        raise ValueError("out must be [..., N]")
+    _need_cuda(x, x_scales, weight, weight_scales, out)
+    work, size = _workspace(workspace, 0 if workspace is not None else lib.gdn_fp8_linear_workspace_size(M, N, K), x.device)
+    rc = lib.gdn_fp8_linear(x.data_ptr(), x_scales.data_ptr(), weight.data_ptr(), weight_scales.data_ptr(), out.data_ptr(),
+                            M, N, K, work.data_ptr(), size, _stream_of(x))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_fp8_linear")
+    return out
 
 
 def _check_ce_args(h, weight, targets, rows):

@@ -471,6 +471,126 @@ gdn_status gdn_layer_norm_bwd(const void *dout, const void *x, const float *mean
     return launch_layer_norm_bwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+static gdn_status rms_args(RmsNormArgs &a, const void *x, const void *residual, const float *weight, void *out,
+                           void *residual_out, int64_t rows, int32_t D, gdn_dtype dt, float eps, unsigned out_size)
+{
+    if (rows < 0 || D < 1 || !(eps >= 0.f)) return GDN_ERR_INVALID_ARG;
+    if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (rows > ((int64_t)1 << 48) / D) return GDN_ERR_INVALID_ARG;
+    if (!residual != !residual_out && rows > 0) return GDN_ERR_INVALID_ARG;
+    const unsigned esz = (dt == GDN_BF16) ? 2u : 4u;
+    if (rows > 0 && (!x || !out)) return GDN_ERR_INVALID_ARG;
+    if (!aligned_to(x, esz) || !aligned_to(residual, esz) || !aligned_to(residual_out, esz) || !aligned_to(out, out_size) ||
+        !aligned_to(weight, 4))
+        return GDN_ERR_INVALID_ARG;
+    a = RmsNormArgs();
+    a.x = x; a.residual = residual; a.weight = weight; a.out = out; a.residual_out = residual_out;
+    a.rows = rows; a.D = D; a.dt = (dt == GDN_BF16) ? 1 : 0; a.eps = eps;
+    return GDN_OK;
+}
+
+gdn_status gdn_rms_norm_fwd(const void *x, const void *residual, const float *weight, void *out, void *residual_out,
+                            float *rstd, int64_t rows, int32_t D, gdn_dtype dt, float eps, void *stream)
+{
+    RmsNormArgs a;
+    const gdn_status s = rms_args(a, x, residual, weight, out, residual_out, rows, D, dt, eps, (dt == GDN_BF16) ? 2u : 4u);
+    if (s != GDN_OK) return s;
+    if (!aligned_to(rstd, 4) || (rows > 0 && out == residual_out)) return GDN_ERR_INVALID_ARG;
+    if (rows == 0) return GDN_OK;
+    a.rstd = rstd;
+    return launch_rms_norm_fwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_rms_norm_fp8(const void *x, const void *residual, const float *weight, void *q, float *scales,
+                            void *residual_out, int64_t rows, int32_t D, gdn_dtype dt, float eps, void *stream)
+{
+    RmsNormArgs a;
+    const gdn_status s = rms_args(a, x, residual, weight, q, residual_out, rows, D, dt, eps, 1u);
+    if (s != GDN_OK) return s;
+    if ((rows > 0 && !scales) || !aligned_to(scales, 4)) return GDN_ERR_INVALID_ARG;
+    if (rows == 0) return GDN_OK;
+    a.scales = scales;
+    return launch_rms_norm_fwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_rms_norm_bwd_workspace_size(int64_t rows, int32_t D, gdn_dtype dt)
+{
+    if (rows < 0 || D < 1 || (dt != GDN_F32 && dt != GDN_BF16) || rows > ((int64_t)1 << 48) / D) return 0;
+    return rms_norm_bwd_workspace_bytes(D);
+}
+
+gdn_status gdn_rms_norm_bwd(const void *dout, const void *x, const float *rstd, const float *weight, const void *dresidual,
+                            void *dx, float *dweight, int64_t rows, int32_t D, gdn_dtype dt, void *workspace,
+                            size_t workspace_bytes, void *stream)
+{
+    if (rows < 0 || D < 1) return GDN_ERR_INVALID_ARG;
+    if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (rows > ((int64_t)1 << 48) / D) return GDN_ERR_INVALID_ARG;
+    const unsigned esz = (dt == GDN_BF16) ? 2u : 4u;
+    if (rows > 0 && (!dout || !x || !rstd)) return GDN_ERR_INVALID_ARG;
+    if (!aligned_to(dout, esz) || !aligned_to(x, esz) || !aligned_to(dresidual, esz) || !aligned_to(dx, esz) ||
+        !aligned_to(rstd, 4) || !aligned_to(weight, 4) || !aligned_to(dweight, 4))
+        return GDN_ERR_INVALID_ARG;
+    if (!workspace || ((uintptr_t)workspace & 255u) != 0) return GDN_ERR_WORKSPACE;
+    if (workspace_bytes < gdn_rms_norm_bwd_workspace_size(rows, D, dt)) return GDN_ERR_WORKSPACE;
+    if (!dx && !dweight) return GDN_OK;
+    if (rows == 0) {
+        if (!dweight) return GDN_OK;
+        return cudaMemsetAsync(dweight, 0, (size_t)D * 4, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    }
+    RmsNormArgs a = RmsNormArgs();
+    a.dout = dout; a.x = x; a.rstd = const_cast<float *>(rstd); a.weight = weight; a.dresidual = dx ? dresidual : nullptr;
+    a.dx = dx; a.dweight = dweight;
+    a.rows = rows; a.D = D; a.dt = (dt == GDN_BF16) ? 1 : 0;
+    a.workspace = workspace;
+    return launch_rms_norm_bwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_fp8_quantize(const void *x, void *q, float *scales, int64_t rows, int32_t D, int32_t block_rows,
+                            gdn_dtype dt, void *stream)
+{
+    if (rows < 0 || D < 1 || (block_rows != 1 && block_rows != kFp8Block)) return GDN_ERR_INVALID_ARG;
+    if (dt != GDN_F32 && dt != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (rows > ((int64_t)1 << 48) / D) return GDN_ERR_INVALID_ARG;
+    if (rows > 0 && (!x || !q || !scales)) return GDN_ERR_INVALID_ARG;
+    if (!aligned_to(x, (dt == GDN_BF16) ? 2u : 4u) || !aligned_to(scales, 4)) return GDN_ERR_INVALID_ARG;
+    if (block_rows > 1 && (rows + kFp8Block - 1) / kFp8Block * ceil_div(D, kFp8Block) > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if (rows == 0) return GDN_OK;
+    Fp8QuantArgs a = Fp8QuantArgs();
+    a.x = x; a.q = (unsigned char *)q; a.scales = scales;
+    a.rows = rows; a.D = D; a.dt = (dt == GDN_BF16) ? 1 : 0; a.block_rows = block_rows;
+    return launch_fp8_quantize(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+// launch grids and tile counts stay within 32 bits
+static bool fp8_size_supported(int32_t M, int32_t N, int32_t K)
+{
+    return M <= (1 << 23) && N <= (1 << 23) && (int64_t)M * N <= (int64_t)1 << 42 && K <= (1 << 20);
+}
+
+size_t gdn_fp8_linear_workspace_size(int32_t M, int32_t N, int32_t K)
+{
+    if (M < 0 || N < 1 || K < 1 || !fp8_size_supported(M, N, K)) return 0;
+    return fp8_linear_workspace_bytes(M, N, K);
+}
+
+gdn_status gdn_fp8_linear(const void *x, const float *x_scales, const void *w, const float *w_scales, void *out, int32_t M,
+                          int32_t N, int32_t K, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (M < 0 || N < 1 || K < 1) return GDN_ERR_INVALID_ARG;
+    if (!fp8_size_supported(M, N, K)) return GDN_ERR_UNSUPPORTED;
+    if (M > 0 && (!x || !x_scales || !out)) return GDN_ERR_INVALID_ARG;
+    if (!w || !w_scales || !aligned_to(x_scales, 4) || !aligned_to(w_scales, 4) || !aligned_to(out, 2)) return GDN_ERR_INVALID_ARG;
+    if (!workspace || ((uintptr_t)workspace & 255u) != 0) return GDN_ERR_WORKSPACE;
+    if (workspace_bytes < gdn_fp8_linear_workspace_size(M, N, K)) return GDN_ERR_WORKSPACE;
+    if (M == 0) return GDN_OK;
+    Fp8LinearArgs a = Fp8LinearArgs();
+    a.x = (const unsigned char *)x; a.w = (const unsigned char *)w; a.xs = x_scales; a.ws = w_scales; a.out = out;
+    a.M = M; a.N = N; a.K = K;
+    a.workspace = workspace;
+    return launch_fp8_linear(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 // launch grids and tile counts stay within 32 bits
 static bool ce_size_supported(int32_t N, int32_t V)
 {

@@ -21,6 +21,11 @@ namespace gdn {
 constexpr int kChunk = 64;
 constexpr float kL2Eps = 1e-6f;
 
+// 8-bit operands: e4m3 values in units of a scale for each block of 128
+constexpr int kFp8Block = 128;
+constexpr float kFp8Max = 448.f;
+constexpr float kFp8Tiny = 0x1p-100f;   // the least magnitude a block is scaled to, so that no scale is 0
+
 // Device error word codes (first 4 bytes of the workspace header).
 constexpr unsigned kDevErrNone = 0u;
 constexpr unsigned kDevErrTimeout = 1u;

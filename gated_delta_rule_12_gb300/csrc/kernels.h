@@ -89,6 +89,36 @@ struct LayerNormArgs {
     void *workspace;
 };
 
+struct RmsNormArgs {
+    const void *x, *residual;                 // [rows, D], dtype dt; residual null or added, the sum going to residual_out
+    const void *dout, *dresidual;             // backward: dtype dt, dresidual null or added to dx
+    const float *weight;                      // [D] fp32 or null
+    void *out, *residual_out, *dx;            // [rows, D], dtype dt; out e4m3 where scales is given
+    float *scales;                            // [rows, ceil(D / 128)] fp32 or null
+    float *rstd;                              // [rows] fp32: written by the forward (or null), read by the backward
+    float *dweight;                           // [D] fp32 or null
+    int64_t rows;
+    int D, dt;
+    float eps;
+    void *workspace;
+};
+
+struct Fp8QuantArgs {
+    const void *x;                            // [rows, D], dtype dt
+    unsigned char *q;                         // [rows, D] e4m3
+    float *scales;                            // [ceil(rows / block_rows), ceil(D / 128)]
+    int64_t rows;
+    int D, dt, block_rows;                    // 1 or 128
+};
+
+struct Fp8LinearArgs {
+    const unsigned char *x, *w;               // [M, K], [N, K] e4m3
+    const float *xs, *ws;                     // [M, ceil(K / 128)], [ceil(N / 128), ceil(K / 128)]
+    void *out;                                // [M, N] bf16
+    int M, N, K;
+    void *workspace;
+};
+
 struct LinearCeArgs {
     const void *h, *w;                        // [N, D], [V, D], dtype dt
     const int32_t *targets;                   // [N]
@@ -106,6 +136,12 @@ cudaError_t launch_gated_scan_step(float *state, const void *x, const void *g, v
 cudaError_t launch_layer_norm_fwd(const LayerNormArgs &a, cudaStream_t st);
 cudaError_t launch_layer_norm_bwd(const LayerNormArgs &a, cudaStream_t st);
 size_t layer_norm_bwd_workspace_bytes(int64_t rows, int D, int dt);
+cudaError_t launch_rms_norm_fwd(const RmsNormArgs &a, cudaStream_t st);
+cudaError_t launch_rms_norm_bwd(const RmsNormArgs &a, cudaStream_t st);
+size_t rms_norm_bwd_workspace_bytes(int D);
+cudaError_t launch_fp8_quantize(const Fp8QuantArgs &a, cudaStream_t st);
+cudaError_t launch_fp8_linear(const Fp8LinearArgs &a, cudaStream_t st);
+size_t fp8_linear_workspace_bytes(int M, int N, int K);
 cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st);
 cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st);
 // bf16 with D a multiple of 8 (rows that TMA can address) up to 2^24: the tensor cores

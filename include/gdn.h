@@ -388,6 +388,88 @@ gdn_status gdn_layer_norm_bwd(const void *dout, const void *x, const float *mean
                               void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Root-mean-square norm over the last axis with the residual's addition: the norm in front of a block of a pre-norm
+ * residual stream ("Gated Delta Networks: Improving Mamba2 with Delta Rule", §3.4; the norm itself is the textbook one):
+ *     s = x + residual,  out = s rstd weight,  rstd = 1 / sqrt(mean(s^2) + eps).
+ *   x, out        [rows, D] dtype dt, contiguous; out may alias x or residual.
+ *   residual, residual_out  [rows, D] dtype dt, both or neither (then s = x).  s is rounded to dt, stored in residual_out
+ *                 and normed as it is stored.  residual_out may alias x or residual, not out.
+ *   weight        [D] fp32, or NULL for 1.
+ *   rstd          [rows] fp32, or NULL to skip; the backward pass needs it.
+ *   rows >= 0, D >= 1, rows * D <= 2^48, eps >= 0; pointers aligned to their element size (tensors that start on
+ *   16-byte boundaries take the fast path up to D = 16384, whatever D is).
+ * Statistics are fp32.
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
+ */
+gdn_status gdn_rms_norm_fwd(const void *x, const void *residual, const float *weight,
+                            void *out, void *residual_out, float *rstd,
+                            int64_t rows, int32_t D, gdn_dtype dt, float eps, void *stream);
+
+/*
+ * gdn_rms_norm_fwd with an output in 8 bits, as gdn_fp8_linear takes it: y = s rstd weight in fp32, then as
+ * gdn_fp8_quantize with block_rows = 1.
+ *   q             [rows, D] e4m3 bytes;  scales [rows, ceil(D / 128)] fp32.  Neither may overlap an input.
+ * Other arguments and errors as gdn_rms_norm_fwd (the fast path: D a multiple of 8 for bf16, of 4 for fp32).
+ */
+gdn_status gdn_rms_norm_fp8(const void *x, const void *residual, const float *weight,
+                            void *q, float *scales, void *residual_out,
+                            int64_t rows, int32_t D, gdn_dtype dt, float eps, void *stream);
+
+/*
+ * Backward pass of gdn_rms_norm_fwd, with x the normed rows (residual_out where a residual was added), xhat = x rstd and
+ * u = dout weight:
+ *     dx = rstd (u - xhat mean(u xhat)) + dresidual,  dweight = sum_rows dout xhat.
+ * dx is the gradient of x and of residual alike, which entered by their sum.
+ *   dout, x, dx   [rows, D] dtype dt (dx may alias dout or dresidual; NULL skips it).
+ *   dresidual     [rows, D] dtype dt, the gradient that comes to residual_out from elsewhere, or NULL for zeros.
+ *   dweight       [D] fp32, overwritten (NULL skips it); rows = 0 leaves zeros in it.
+ *   workspace     at least gdn_rms_norm_bwd_workspace_size() bytes, 256-byte aligned.
+ * The sums over rows are joined in a fixed order: the same inputs give the same bits.
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_WORKSPACE, GDN_ERR_CUDA.
+ */
+size_t gdn_rms_norm_bwd_workspace_size(int64_t rows, int32_t D, gdn_dtype dt);
+
+gdn_status gdn_rms_norm_bwd(const void *dout, const void *x, const float *rstd, const float *weight,
+                            const void *dresidual, void *dx, float *dweight,
+                            int64_t rows, int32_t D, gdn_dtype dt,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Values to e4m3 (4 exponent bits, 3 of the fraction, up to 448) in units of a scale for each block of 128 columns of
+ * block_rows rows:  c = max(|x|, 2^-100) / 448 over the block,  q = e4m3(x / c), to the nearest, ties to even.
+ *   x             [rows, D] dtype dt, contiguous;  q [rows, D] bytes.
+ *   scales        [ceil(rows / block_rows), ceil(D / 128)] fp32.  The last blocks may be partial.
+ *   block_rows    1 (activations) or 128 (weights).
+ * NaN stays NaN in its place and does not enter its block's scale.  An infinity makes its block's scale infinite, itself
+ * NaN and the block's finite values 0.
+ *   rows >= 0, D >= 1, rows * D <= 2^48, and for block_rows = 128 fewer than 2^31 blocks (else GDN_ERR_UNSUPPORTED);
+ *   pointers aligned to their element size (the fast path: 16 bytes, D a multiple of 8 for bf16, of 4 for fp32).
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA.
+ */
+gdn_status gdn_fp8_quantize(const void *x, void *q, float *scales, int64_t rows, int32_t D, int32_t block_rows,
+                            gdn_dtype dt, void *stream);
+
+/*
+ * Product of 8-bit operands with scales, the projections of a served layer:
+ *     out_mn = sum_b x_scales_mb w_scales_{n / 128, b} sum_{k in block b} x_mk w_nk,   blocks of 128 along K.
+ *   x             [M, K] e4m3 bytes;  x_scales [M, ceil(K / 128)] fp32   (gdn_fp8_quantize with block_rows 1, gdn_rms_norm_fp8)
+ *   w             [N, K] e4m3 bytes;  w_scales [ceil(N / 128), ceil(K / 128)] fp32   (gdn_fp8_quantize with block_rows 128)
+ *   out           [M, N] bf16; must not overlap an input.
+ *   0 <= M <= 2^23, 1 <= N <= 2^23, M N <= 2^42, 1 <= K <= 2^20 (beyond: GDN_ERR_UNSUPPORTED); scales 4-byte, out 2-byte
+ *   aligned.  K a multiple of 16, with x, w and out on 16-byte boundaries, runs on the tensor cores, the rest on the CUDA
+ *   cores.
+ *   workspace     at least gdn_fp8_linear_workspace_size() bytes, 256-byte aligned; its first 256 bytes hold the device
+ *                 error word read by gdn_check_device_error.
+ * Sums are fp32, rounded once to bf16.  Results do not depend on timing.  A tensor-core kernel that gives up a wait (after
+ * 1 s) leaves NaN in what it should have written, besides the error word.
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_CUDA.
+ */
+size_t gdn_fp8_linear_workspace_size(int32_t M, int32_t N, int32_t K);
+
+gdn_status gdn_fp8_linear(const void *x, const float *x_scales, const void *w, const float *w_scales, void *out,
+                          int32_t M, int32_t N, int32_t K, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Softmax cross entropy of a linear head, without an [N, V] array of logits:
  *     lse_i = log sum_v exp(h_i . w_v),   loss_i = lse_i - h_i . w_{targets_i}.
  *   h             [N, D] dtype dt;  weight [V, D] dtype dt;  both 16-byte aligned and contiguous.
