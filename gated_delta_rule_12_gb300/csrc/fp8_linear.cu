@@ -78,6 +78,7 @@ size_t fp8_linear_workspace_bytes(int, int, int) { return 256; }
 
 cudaError_t launch_fp8_linear(const Fp8LinearArgs &a, cudaStream_t st)
 {
+    if (fp8_linear_tc_supported(a)) return launch_fp8_linear_tc(a, st);
     const int mt = ceil_div(a.M, kTile), nt = ceil_div(a.N, kTile);
     simt_kernel<<<(unsigned)((int64_t)mt * nt), kThreads, 0, st>>>(a, nt);
     return cudaGetLastError();

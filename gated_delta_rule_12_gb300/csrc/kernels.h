@@ -141,6 +141,9 @@ cudaError_t launch_rms_norm_bwd(const RmsNormArgs &a, cudaStream_t st);
 size_t rms_norm_bwd_workspace_bytes(int D);
 cudaError_t launch_fp8_quantize(const Fp8QuantArgs &a, cudaStream_t st);
 cudaError_t launch_fp8_linear(const Fp8LinearArgs &a, cudaStream_t st);
+// K a multiple of 16, tensors on 16-byte boundaries
+bool fp8_linear_tc_supported(const Fp8LinearArgs &a);
+cudaError_t launch_fp8_linear_tc(const Fp8LinearArgs &a, cudaStream_t st);
 size_t fp8_linear_workspace_bytes(int M, int N, int K);
 cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st);
 cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st);
