@@ -8,7 +8,7 @@
 //   pair_kernel   many tokens: 256 tokens x 256 words a pair of CTAs (cta_group::2, each holds 128 rows of both operands,
 //                 five stages of 32 KB); persistent, one pair's tile after another.  Eight epilogue warps, a thread 128
 //                 sums of its token: reading 128 x 256 values back takes 256 cycles a block, its multiplication 512.
-//                 Results go to memory by TMA.
+//                 Results go to memory by TMA, rows that it cannot address (words no multiple of 8) by plain stores.
 //   few_kernel    few tokens: the words are the rows of the tile (128), 16 to 128 tokens its columns, so the weights'
 //                 bytes, which such a call is bound by, take the whole width.  A cluster of up to eight CTAs shares a
 //                 tile's K; their partial sums meet in shared memory and are added in the CTAs' order.
@@ -71,11 +71,54 @@ __device__ __forceinline__ void mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64
         :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
+// These kernels' barriers order tensor memory, by tcgen05 fences, and what the asynchronous proxy wrote, so their waits
+// and arrivals need no wider ordering: a release to the cluster waits for the warp's loads in flight, GPU-wide latency on
+// the chain of every block.
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned *err)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            atomicExch(err, kDevErrTimeout);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
 {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+
+// Waits for the loads from tensor memory, of which `r` is the last: nothing that uses it may come before.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31]) :: "memory");
+}
+
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :: "memory");
 }
 
 __device__ __forceinline__ Pair pair_of(uint32_t lo, uint32_t hi) { return pair(__uint_as_float(lo), __uint_as_float(hi)); }
@@ -112,12 +155,11 @@ pair_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Par
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + (abort_addr - base));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_cluster(bar, parity, abort_flag, p.err, kWaitLimitNs); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_here(bar, parity, abort_flag, p.err); };
 
     if (threadIdx.x == 32) {
         prefetch_tmap(&maps.x);
         prefetch_tmap(&maps.w);
-        prefetch_tmap(&maps.out);
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -212,12 +254,19 @@ pair_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Par
             Pair acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0;
-            float x_next = __ldg(xs), w_next = __ldg(ws);
+            // the scales come two blocks ahead
+            float x_now = __ldg(xs), w_now = __ldg(ws), x_next = 0.f, w_next = 0.f;
+            if (p.kb > 1) {
+                x_next = __ldg(xs + 1);
+                w_next = __ldg(ws + 1);
+            }
             for (int k = 0; k < p.kb; ++k, ++it) {
-                const Pair scale = both(x_next * w_next);
-                if (k + 1 < p.kb) {
-                    x_next = __ldg(xs + k + 1);
-                    w_next = __ldg(ws + k + 1);
+                const Pair scale = both(x_now * w_now);
+                x_now = x_next;
+                w_now = w_next;
+                if (k + 2 < p.kb) {
+                    x_next = __ldg(xs + k + 2);
+                    w_next = __ldg(ws + k + 2);
                 }
                 const uint32_t buf = it & 1;
                 ok = __all_sync(0xffffffffu, wait(acc_full + 8 * buf, (it >> 1) & 1));
@@ -228,11 +277,11 @@ pair_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Par
                 for (int ch = 0; ch < 8; ++ch) {
                     uint32_t r[16];
                     tmem_ld16(src + ch * 16, r);
-                    tmem_wait_ld();
+                    wait_ld(r);
                     if (ch == 7) {   // the accumulator is in registers: the next block but one may have it
                         fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) arrive_remote(leader_empty + 8 * buf);
+                        if (lane == 0) arrive_remote_relaxed(leader_empty + 8 * buf);
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) acc[8 * ch + i] = fma2(pair_of(r[2 * i], r[2 * i + 1]), scale, acc[8 * ch + i]);
@@ -252,6 +301,20 @@ pair_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Par
                     w[i] = pack_bf16(a, b);
                 }
                 st_shared16(buf_s + (j >> 3) * 4096 + lane * 128 + (((j & 7) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+            }
+            if (p.N % 8 != 0) {   // rows that TMA cannot address: 64 bytes of a row at a time
+                __syncwarp();
+                const int rows = min(32, p.M - row0);
+#pragma unroll 1
+                for (int i = lane; i < rows * 128; i += 32) {
+                    const int r = i >> 7, c = i & 127;
+                    unsigned short v;
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v)
+                                 : "r"(buf_s + (c >> 6) * 4096 + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2));
+                    if (col0 + c < p.N) p.out[(int64_t)(row0 + r) * p.N + col0 + c] = __ushort_as_bfloat16(v);
+                }
+                __syncwarp();
+                continue;
             }
             fence_proxy_async();
             __syncwarp();
@@ -319,7 +382,7 @@ __device__ __forceinline__ int ld_cluster_int(uint32_t addr)
 
 // TN tokens a tile.  The grid: clusters of p.splits CTAs, one a tile, the tiles of the same words next to each other.
 template <int TN>
-__global__ void __launch_bounds__(few_threads<TN>(), 1) few_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Params p)
+__global__ void __launch_bounds__(few_threads<TN>(), TN == 128 ? 1 : 2) few_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Params p)
 {
     constexpr int kWarps = few_warps<TN>(), kThreads = few_threads<TN>();
     constexpr int kMine = TN * 4 / kWarps;             // tokens that an epilogue thread sums
@@ -339,7 +402,7 @@ __global__ void __launch_bounds__(few_threads<TN>(), 1) few_kernel(const __grid_
     const int splits = p.splits, rank = (int)(blockIdx.x % (unsigned)splits), tile = (int)(blockIdx.x / (unsigned)splits);
     const int m0 = tile % p.mt * TN, n0 = tile / p.mt * kRows;
     const int k0 = (int)((int64_t)p.kb * rank / splits), k1 = (int)((int64_t)p.kb * (rank + 1) / splits);
-    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_cluster(bar, parity, abort_flag, p.err, kWaitLimitNs); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_here(bar, parity, abort_flag, p.err); };
 
     if (threadIdx.x == 32) {
         prefetch_tmap(&maps.x);
@@ -431,7 +494,7 @@ __global__ void __launch_bounds__(few_threads<TN>(), 1) few_kernel(const __grid_
                 uint32_t r[kChunk];
                 if constexpr (kChunk == 32) tmem_ld32(src + ch * 32, r);
                 else tmem_ld16(src + ch * 16, r);
-                tmem_wait_ld();
+                wait_ld(r);
                 if (ch == kMine / kChunk - 1) {
                     fence_before_sync();
                     __syncwarp();
@@ -524,17 +587,34 @@ struct Plan {
     int splits, stages;
 };
 
+// The kernel, the tile's tokens and the cut of K that take the least time by a model fitted to measurements (microseconds;
+// 512 to 16384 words, K 512 to 6144, 1 to 1024 tokens): a kernel's start and end, more with more tokens a tile and for every
+// CTA of a cluster whose sums are joined, and the blocks one after another, once for each round of CTAs.  2048 x 6144 on one
+// box: 1 token 5.3 (16 tokens a tile, K in 4; uncut 9.3, pairs 9.5), 64 tokens 8.5 (32, 2; 128 tokens a tile 9.1), 256 tokens
+// 10.5 (pairs; 13.5 uncut, 19 to 24 where the CTAs need a second round).
 Plan plan(int M, int N, int kb)
 {
-    const int pair_tiles = ceil_div(M, kTile) * ceil_div(N, kTile);
-    if (N % 8 == 0 && M > 128 && pair_tiles >= kPairs / 2) return {0, 1, kStages};
-    Plan r = {M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128, 1, 1};
-    const int64_t tiles = (int64_t)ceil_div(M, r.tn) * ceil_div(N, kRows);
-    const int room = 100 * 1024;   // two CTAs an SM
-    while (r.splits < kMostSplits && tiles * r.splits * 2 <= 304 && kb / (r.splits * 2) >= 2) r.splits *= 2;
-    const int most = (tiles * r.splits <= 152 ? 2 * room : room) / few_stage_bytes(r.tn), need = ceil_div(kb, r.splits);
-    r.stages = need < most ? need : most;
-    return r;
+    Plan best = {0, 1, kStages};
+    const int64_t rounds = ((int64_t)ceil_div(M, kTile) * ceil_div(N, kTile) + kPairs - 1) / kPairs;
+    float least = 4.5f + rounds * kb * 0.4f;
+    for (int tn = 16; tn <= 128; tn *= 2) {
+        if (tn < 128 && (M > 4 * tn || (tn > 16 && M <= tn / 2))) continue;
+        const int64_t tiles = (int64_t)ceil_div(M, tn) * ceil_div(N, kRows);
+        for (int splits = 1; splits <= (tn == 128 ? kMostSplits / 2 : kMostSplits) && splits <= kb; splits *= 2) {
+            const int64_t ctas = tiles * splits;
+            // two CTAs an SM, but for 128 tokens; clusters of 4 and 8 do not fill every GPC
+            const int at_once = (tn == 128 ? 152 : 304) * (splits == 8 ? 27 : splits == 4 ? 30 : 32) / 32;
+            const float waves = (float)((ctas + at_once - 1) / at_once);
+            const float start = tn == 16 ? 4.f : tn == 32 ? 4.6f : tn == 64 ? 5.4f : 6.2f;
+            const float t = waves * (start + ceil_div(kb, splits) * (ctas > 152 ? 0.41f : 0.34f)) + 0.006f * tn * (splits > 1 ? splits : 0);
+            if (t >= least) continue;
+            least = t;
+            const int room = (tn == 128 || (ctas <= 120 && splits <= 4) ? 180 : 88) * 1024;
+            const int most = room / few_stage_bytes(tn), need = ceil_div(kb, splits);
+            best = {tn, splits, need < most ? need : most};
+        }
+    }
+    return best;
 }
 
 template <int TN>
@@ -589,7 +669,7 @@ cudaError_t launch_fp8_linear_tc(const Fp8LinearArgs &a, cudaStream_t st)
     case 64: return launch_few<64>(maps, p, st);
     case 128: return launch_few<128>(maps, p, st);
     }
-    if (!out_map(&maps.out, a.out, a.N, a.M)) return cudaErrorInvalidValue;
+    if (a.N % 8 == 0 && !out_map(&maps.out, a.out, a.N, a.M)) return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
     if (e != cudaSuccess) return e;
     const int tiles = p.mt * p.nt, pairs = tiles < kPairs ? tiles : kPairs;

@@ -108,7 +108,7 @@ def test_linear_against_the_definition(M, N, K):
 
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (5, 1, 16), (1, 7, 100), (40, 130, 17), (70, 70, 200), (130, 129, 999),
                                    (64, 2048, 2048), (1, 6144, 2048), (3, 16, 8192), (129, 15, 4112), (700, 1030, 400),
-                                   (1025, 515, 1040), (2, 16384, 144), (600, 2000, 2048), (20, 3, 20000)])
+                                   (1025, 515, 1040), (2, 16384, 144), (600, 2000, 2048), (20, 3, 20000), (1000, 3001, 256), (515, 2047, 272)])
 def test_linear_odd_and_larger_sizes(M, N, K):
     check_linear(M, N, K, seed=M)
 
