@@ -32,6 +32,8 @@ Entry points (same names as the C ABI, without the ``gdn_`` prefix):
     fp8_linear(x, x_scales, weight, weight_scales) -> out [M,N] bf16
     linear_cross_entropy_fwd(h, weight, targets) -> (loss, lse)   no logits array
     linear_cross_entropy_bwd(h, weight, targets, lse, dloss) -> (dh, dweight)
+    linear_log_probs_fwd(h, weight, targets, top_k) -> (logp, entropy, lse, top_ids, top_logps)   no logits array
+    linear_log_probs_bwd(h, weight, targets, lse, entropy, dlogp, dentropy) -> (dh, dweight)
     check_device_error(workspace)         -> None or raises
 """
 from __future__ import annotations
@@ -59,7 +61,8 @@ EXPORTS = ["gdn_status_string", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd_k
            "gdn_rms_norm_fwd", "gdn_rms_norm_fp8", "gdn_rms_norm_bwd_workspace_size", "gdn_rms_norm_bwd",
            "gdn_fp8_quantize", "gdn_fp8_linear_workspace_size", "gdn_fp8_linear",
            "gdn_linear_cross_entropy_workspace_size", "gdn_linear_cross_entropy_fwd",
-           "gdn_linear_cross_entropy_bwd"]
+           "gdn_linear_cross_entropy_bwd", "gdn_linear_log_probs_workspace_size", "gdn_linear_log_probs_fwd",
+           "gdn_linear_log_probs_bwd"]
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -149,12 +152,16 @@ def load_library(path: str = LIB_PATH, build_if_missing: bool = False) -> ctypes
         lib.gdn_linear_cross_entropy_workspace_size.restype = _sz
         lib.gdn_linear_cross_entropy_fwd.argtypes = [_vp] * 5 + [_i32] * 3 + [_ci, _vp, _sz, _vp]
         lib.gdn_linear_cross_entropy_bwd.argtypes = [_vp] * 7 + [_i32] * 3 + [_ci, _vp, _sz, _vp]
+        lib.gdn_linear_log_probs_workspace_size.argtypes = [_i32] * 4 + [_ci, _i32]
+        lib.gdn_linear_log_probs_workspace_size.restype = _sz
+        lib.gdn_linear_log_probs_fwd.argtypes = [_vp] * 8 + [_i32] * 4 + [_ci, _vp, _sz, _vp]
+        lib.gdn_linear_log_probs_bwd.argtypes = [_vp] * 9 + [_i32] * 3 + [_ci, _vp, _sz, _vp]
         lib.gdn_selftest_linear_cross_entropy_timeout.argtypes = [_i32, ctypes.c_uint32] + [_vp] * 7 + [_i32] * 3 + \
             [_vp, _sz, _vp]
         lib.gdn_selftest_linear_cross_entropy_timeout.restype = _ci
         for name in ("gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "layer_norm_fwd", "layer_norm_bwd",
                      "rms_norm_fwd", "rms_norm_fp8", "rms_norm_bwd", "fp8_quantize", "fp8_linear",
-                     "linear_cross_entropy_fwd", "linear_cross_entropy_bwd"):
+                     "linear_cross_entropy_fwd", "linear_cross_entropy_bwd", "linear_log_probs_fwd", "linear_log_probs_bwd"):
             getattr(lib, "gdn_" + name).restype = _ci
         _lib = lib
         return lib
@@ -965,6 +972,71 @@ def linear_cross_entropy_bwd(h, weight, targets, lse, dloss, workspace=None, str
                                           size, _stream_of(h))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_linear_cross_entropy_bwd")
+    return dh, dw
+
+
+MOST_TOP = 20   # the most alternatives of linear_log_probs_fwd
+
+
+def linear_log_probs_workspace_size(N, D, V, top_k=0, dtype=torch.bfloat16, backward=False) -> int:
+    dt = GDN_BF16 if dtype == _BF16 else GDN_F32
+    if max(N, D, V, top_k) > _MOST:
+        return 0
+    return int(load_library().gdn_linear_log_probs_workspace_size(N, D, V, top_k, dt, int(bool(backward))))
+
+
+def linear_log_probs_fwd(h, weight, targets, top_k=0, workspace=None, stream=None):
+    """Log probabilities of the given tokens under the logits ``h @ weight.T``, with the entropy of each row's
+    distribution and its ``top_k`` most probable words, without forming the logits (``gdn_linear_log_probs_fwd``).
+
+    h [N,D], weight [V,D] (fp32 or bf16); targets int32 [N], rows with a target outside [0,V) are ignored; top_k from 0 to
+    20.  Returns ``(logp, entropy, lse, top_ids, top_logps)``: the first three [N] fp32 and 0 in ignored rows; top_ids
+    int32 and top_logps fp32 [N,top_k], best first and equal ones by the lower index, -1 and 0 in ignored rows (None with
+    top_k = 0).
+    """
+    if stream is not None:
+        return _elsewhere(stream, linear_log_probs_fwd, h, weight, targets, top_k, workspace)
+    lib = _lib or load_library()
+    N, D, V = _check_ce_args(h, weight, targets, ())
+    dt = _dt(h)
+    if not 0 <= top_k <= min(MOST_TOP, V):
+        raise ValueError(f"top_k must be from 0 to {MOST_TOP} and at most V")
+    device = h.device
+    logp = _empty(N, dtype=_F32, device=device)
+    entropy, lse = _empty_like(logp), _empty_like(logp)
+    ids = top = None
+    if top_k:
+        ids = _empty((N, top_k), dtype=torch.int32, device=device)
+        top = _empty((N, top_k), dtype=_F32, device=device)
+    ws, size = _workspace(workspace, 0 if workspace is not None else
+                          lib.gdn_linear_log_probs_workspace_size(N, D, V, top_k, dt, 0), device)
+    rc = lib.gdn_linear_log_probs_fwd(h.data_ptr(), weight.data_ptr(), targets.data_ptr(), logp.data_ptr(),
+                                      entropy.data_ptr(), lse.data_ptr(), _ptr(ids), _ptr(top), N, D, V, top_k, dt,
+                                      ws.data_ptr(), size, _stream_of(h))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_linear_log_probs_fwd")
+    return logp, entropy, lse, ids, top
+
+
+def linear_log_probs_bwd(h, weight, targets, lse, entropy, dlogp, dentropy=None, workspace=None, stream=None):
+    """Gradient of ``linear_log_probs_fwd`` (``gdn_linear_log_probs_bwd``) for the gradients ``dlogp`` and ``dentropy``
+    [N] fp32 (the second None for zeros): returns ``(dh, dweight)`` in the dtype of h.  ``lse`` and ``entropy`` are the
+    forward's; entropy may be None where dentropy is."""
+    if stream is not None:
+        return _elsewhere(stream, linear_log_probs_bwd, h, weight, targets, lse, entropy, dlogp, dentropy, workspace)
+    lib = _lib or load_library()
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy goes with the forward's entropy")
+    N, D, V = _check_ce_args(h, weight, targets, [t for t in (lse, dlogp, entropy, dentropy) if t is not None])
+    dt = _dt(h)
+    dh, dw = _empty_like(h), _empty_like(weight)
+    ws, size = _workspace(workspace, 0 if workspace is not None else
+                          lib.gdn_linear_log_probs_workspace_size(N, D, V, 0, dt, 1), h.device)
+    rc = lib.gdn_linear_log_probs_bwd(h.data_ptr(), weight.data_ptr(), targets.data_ptr(), lse.data_ptr(), _ptr(entropy),
+                                      dlogp.data_ptr(), _ptr(dentropy), dh.data_ptr(), dw.data_ptr(), N, D, V, dt,
+                                      ws.data_ptr(), size, _stream_of(h))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_linear_log_probs_bwd")
     return dh, dw
 
 

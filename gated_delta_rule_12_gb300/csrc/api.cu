@@ -654,6 +654,54 @@ gdn_status gdn_linear_cross_entropy_bwd(const void *h, const void *weight, const
     return launch_linear_ce_bwd(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+size_t gdn_linear_log_probs_workspace_size(int32_t N, int32_t D, int32_t V, int32_t top_k, gdn_dtype dt, int32_t backward)
+{
+    if (N < 0 || D < 1 || V < 1 || top_k < 0 || top_k > GDN_MOST_TOP || top_k > V || (dt != GDN_F32 && dt != GDN_BF16) ||
+        !ce_size_supported(N, V))
+        return 0;
+    return linear_ce_workspace_bytes(N, D, V, (dt == GDN_BF16) ? 1 : 0, backward != 0, backward ? -1 : top_k);
+}
+
+gdn_status gdn_linear_log_probs_fwd(const void *h, const void *weight, const int32_t *targets, float *logp, float *entropy,
+                                    float *lse, int32_t *top_ids, float *top_logps, int32_t N, int32_t D, int32_t V,
+                                    int32_t top_k, gdn_dtype dt, void *workspace, size_t workspace_bytes, void *stream)
+{
+    LinearCeArgs a;
+    if (top_k < 0 || top_k > GDN_MOST_TOP || top_k > V) return GDN_ERR_INVALID_ARG;
+    const gdn_status s = ce_args(a, h, weight, targets, N, D, V, dt, false, workspace, SIZE_MAX);
+    if (s != GDN_OK) return s;
+    if (workspace_bytes < gdn_linear_log_probs_workspace_size(N, D, V, top_k, dt, 0)) return GDN_ERR_WORKSPACE;
+    if (N > 0 && (!logp || !entropy || (top_k > 0 && (!top_ids || !top_logps)))) return GDN_ERR_INVALID_ARG;
+    const void *ptrs4[] = {logp, entropy, lse, top_ids, top_logps};
+    for (const void *p : ptrs4)
+        if (!aligned_to(p, 4)) return GDN_ERR_INVALID_ARG;
+    if (N == 0) return GDN_OK;
+    const LogProbs out = {logp, entropy, lse, top_ids, top_logps, top_k};
+    return launch_linear_ce_fwd(a, (cudaStream_t)stream, &out) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_linear_log_probs_bwd(const void *h, const void *weight, const int32_t *targets, const float *lse,
+                                    const float *entropy, const float *dlogp, const float *dentropy, void *dh,
+                                    void *dweight, int32_t N, int32_t D, int32_t V, gdn_dtype dt, void *workspace,
+                                    size_t workspace_bytes, void *stream)
+{
+    LinearCeArgs a;
+    const gdn_status s = ce_args(a, h, weight, targets, N, D, V, dt, true, workspace, workspace_bytes);
+    if (s != GDN_OK) return s;
+    if (N > 0 && (!lse || !dlogp || (dentropy && !entropy))) return GDN_ERR_INVALID_ARG;
+    if (!aligned_to(lse, 4) || !aligned_to(entropy, 4) || !aligned_to(dlogp, 4) || !aligned_to(dentropy, 4) ||
+        !aligned16(dh) || !aligned16(dweight))
+        return GDN_ERR_INVALID_ARG;
+    if (!dh && !dweight) return GDN_OK;
+    if (N == 0) {
+        if (!dweight) return GDN_OK;
+        const size_t bytes = (size_t)V * D * (dt == GDN_BF16 ? 2 : 4);
+        return cudaMemsetAsync(dweight, 0, bytes, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    }
+    a.lse_in = lse; a.dloss = dlogp; a.dh = dh; a.dw = dweight;
+    return launch_linear_ce_bwd(a, (cudaStream_t)stream, {dentropy, entropy, -1.f}) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 gdn_status gdn_selftest_linear_cross_entropy_timeout(int32_t step, uint32_t limit_us, const void *h, const void *weight,
                                                      const int32_t *targets, const float *lse, const float *dloss,
                                                      void *out0, void *out1, int32_t N, int32_t D, int32_t V,
@@ -671,11 +719,11 @@ gdn_status gdn_selftest_linear_cross_entropy_timeout(int32_t step, uint32_t limi
     cudaError_t e;
     if (step == 0) {
         a.loss = (float *)out0; a.lse = (float *)out1;
-        e = launch_linear_ce_tc_fwd(a, (cudaStream_t)stream, stall);
+        e = launch_linear_ce_tc_fwd(a, (cudaStream_t)stream, nullptr, stall);
     } else {
         if (!lse || !dloss || !aligned_to(lse, 4) || !aligned_to(dloss, 4)) return GDN_ERR_INVALID_ARG;
         a.lse_in = lse; a.dloss = dloss; a.dh = out0; a.dw = out1;
-        e = launch_linear_ce_tc_bwd(a, (cudaStream_t)stream, stall);
+        e = launch_linear_ce_tc_bwd(a, (cudaStream_t)stream, LogProbsGrad(), stall);
     }
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

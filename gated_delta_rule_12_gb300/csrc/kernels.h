@@ -119,6 +119,14 @@ struct Fp8LinearArgs {
     void *workspace;
 };
 
+// What the log probabilities' forward call writes in place of loss and lse.
+struct LogProbs {
+    float *logp, *entropy, *lse;              // [N] fp32; lse may be null
+    int32_t *top_ids;                         // [N, top_k]
+    float *top_logps;                         // [N, top_k] fp32
+    int top_k;
+};
+
 struct LinearCeArgs {
     const void *h, *w;                        // [N, D], [V, D], dtype dt
     const int32_t *targets;                   // [N]
@@ -127,6 +135,13 @@ struct LinearCeArgs {
     void *dh, *dw;                            // backward only: [N, D], [V, D], dtype dt
     int N, D, V, dt;
     void *workspace;
+};
+
+// The log probabilities' backward call, beside dlogp in dloss: dloss counts with the sign -1, and a gradient of the entropy
+// (else null) comes with the entropy, [N] fp32.
+struct LogProbsGrad {
+    const float *dentropy = nullptr, *entropy = nullptr;
+    float sign = 1.f;
 };
 
 cudaError_t launch_gated_scan_fwd(const GatedScanArgs &a, cudaStream_t st);
@@ -145,20 +160,23 @@ cudaError_t launch_fp8_linear(const Fp8LinearArgs &a, cudaStream_t st);
 bool fp8_linear_tc_supported(const Fp8LinearArgs &a);
 cudaError_t launch_fp8_linear_tc(const Fp8LinearArgs &a, cudaStream_t st);
 size_t fp8_linear_workspace_bytes(int M, int N, int K);
-cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st);
-cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st);
+// out, grad: the log probabilities' calls
+cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st, const LogProbs *out = nullptr);
+cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st, LogProbsGrad grad = LogProbsGrad());
 // bf16 with D a multiple of 8 (rows that TMA can address) up to 2^24: the tensor cores
 bool linear_ce_tc_supported(int dt, int D);
-size_t linear_ce_tc_workspace_bytes(int N, int D, int V, bool backward);
+size_t linear_ce_tc_workspace_bytes(int N, int D, int V, bool backward, int top = -1);   // top: of log probabilities
 // The self-test's: in this kernel (0 the logits, 1 E, 2 the gradients) the first CTA pair's loads never come, and waits give
 // up after limit_ns.
 struct CeStall {
     int step = -1;
     uint64_t limit_ns = 0;
 };
-cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, CeStall stall = CeStall());
-cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st, CeStall stall = CeStall());
-size_t linear_ce_workspace_bytes(int N, int D, int V, int dt, bool backward);
+cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, const LogProbs *out = nullptr,
+                                    CeStall stall = CeStall());
+cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st, LogProbsGrad grad = LogProbsGrad(),
+                                    CeStall stall = CeStall());
+size_t linear_ce_workspace_bytes(int N, int D, int V, int dt, bool backward, int top = -1);
 
 cudaError_t launch_chunk_simt(const ChunkArgs &a, cudaStream_t st);
 cudaError_t launch_chunk_bwd(const BwdArgs &a, cudaStream_t st);

@@ -14,6 +14,7 @@
 // the workspace, then read by the two products.  All sums run in a fixed order.
 #include "common.cuh"
 #include "kernels.h"
+#include "log_probs.cuh"
 
 namespace gdn {
 namespace {
@@ -23,20 +24,23 @@ constexpr int kTile = 128, kDepth = 16, kThreads = 256;
 struct CeWorkspace {
     size_t part;     // forward: float2 [N][tiles]   (max, sum) of each row over each 128 columns
     size_t at;       // forward: float [N]           the target's logit
+    size_t best;     // log probabilities, forward: float2 [N][tiles][top]   a tile's best words, part being RowStat then
     size_t g;        // backward: float [N][piece]   G of one piece of the vocabulary
     size_t acc;      // backward: float [N][D]       dh so far
     size_t total;
     int tiles, piece;
 };
 
-CeWorkspace layout(int N, int D, int V, bool backward)
+// top: the best words of a log-probability call, -1 for the cross entropy
+CeWorkspace layout(int N, int D, int V, bool backward, int top = -1)
 {
     CeWorkspace w = {};
     size_t off = 0;
     w.tiles = ceil_div(V, kTile);
     if (!backward) {
-        w.part = off; off = align256(off + (size_t)N * w.tiles * 8);
+        w.part = off; off = align256(off + (size_t)N * w.tiles * (top < 0 ? sizeof(float2) : sizeof(RowStat)));
         w.at = off;   off = align256(off + (size_t)N * 4);
+        w.best = off; off = align256(off + (top > 0 ? (size_t)N * w.tiles * top * sizeof(float2) : 0));
     } else {
         // a piece's G in about 64 MB
         const int64_t fit = ((int64_t)16 << 20) / (N > 0 ? N : 1) / kTile;
@@ -115,10 +119,14 @@ __device__ __forceinline__ bool kept(const LinearCeArgs &a, int row)
     return t >= 0 && t < a.V;
 }
 
-// Logits of rows row0 + blockIdx.y * 128 .. and columns v0 + blockIdx.x * 128 ..; BACK: G of the piece, else the tile's
-// (max, sum) of each row and the target's logit where the tile holds it.
-template <typename T, bool BACK>
-__global__ void __launch_bounds__(kThreads, 2) ce_logits_kernel(LinearCeArgs a, CeWorkspace ws, int v0, int cols, int row0)
+// Logits of rows row0 + blockIdx.y * 128 .. and columns v0 + blockIdx.x * 128 ..; kBack: G of the piece (kBackEnt: with the
+// entropy's gradient), else the tile's (max, sum) of each row and the target's logit where the tile holds it (kStats: what
+// the entropy takes, and the tile's best words too).
+enum { kLoss, kBack, kStats, kBackEnt };
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kThreads, 2) ce_logits_kernel(LinearCeArgs a, CeWorkspace ws, int v0, int cols, int row0,
+                                                                LogProbsGrad grad, int top_k)
 {
     const int m0 = row0 + blockIdx.y * kTile, n0 = v0 + blockIdx.x * kTile;
     const T *h = (const T *)a.h, *w = (const T *)a.w;
@@ -134,9 +142,19 @@ __global__ void __launch_bounds__(kThreads, 2) ce_logits_kernel(LinearCeArgs a, 
         const bool in = row < a.N;   // the same for the 16 lanes that share the row
         const int t = in ? a.targets[row] : -1;
         const bool keep = t >= 0 && t < a.V;
-        if (BACK) {
+        if (MODE == kBackEnt) {
             if (!in) continue;
-            const float lse = a.lse_in[row], dl = a.dloss[row];
+            const float lse = a.lse_in[row], da = a.dloss[row], de = grad.dentropy[row], entropy = grad.entropy[row];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int v = n0 + col_of(j);
+                if (v - v0 >= cols) continue;
+                const float z = acc[i][j] - lse, g = expf(z) * fmaf(de, fmaxf(z, -1e4f) + entropy, da);   // 0 times -inf is 0 here
+                ((float *)((char *)a.workspace + ws.g))[(int64_t)row * cols + (v - v0)] = keep ? (v == t ? da : 0.f) - g : 0.f;
+            }
+        } else if (MODE == kBack) {
+            if (!in) continue;
+            const float lse = a.lse_in[row], dl = grad.sign * a.dloss[row];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int v = n0 + col_of(j);
@@ -152,16 +170,54 @@ __global__ void __launch_bounds__(kThreads, 2) ce_logits_kernel(LinearCeArgs a, 
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const float base = isinf(top) ? 0.f : top;   // keeps infinities and NaN in the sum
+            float u = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int v = n0 + col_of(j);
                 if (v >= a.V) continue;
-                sum += expf(acc[i][j] - base);
+                const float d = acc[i][j] - base, e = expf(d);
+                sum += e;
+                if (MODE == kStats) u = fmaf(e, fmaxf(d, -1e4f), u);   // 0 times -inf is 0 here
                 if (in && v == t) ((float *)((char *)a.workspace + ws.at))[row] = acc[i][j];
             }
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (in && (threadIdx.x & 15) == 0)
+            if (MODE == kStats) {
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+                const int64_t at = (int64_t)row * ws.tiles + blockIdx.x;
+                int count = 0;
+                // a word a turn, the best one left among the 16 lanes' (most tiles of a row have few of its best, but which
+                // is known only behind them all)
+                for (; count < top_k; ++count) {
+                    float x = -INFINITY;
+                    int word = INT32_MAX;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (n0 + col_of(j) < a.V && acc[i][j] > x) {
+                            x = acc[i][j];
+                            word = n0 + col_of(j);
+                        }
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) {
+                        const float y = __shfl_xor_sync(0xffffffffu, x, o);
+                        const int other = __shfl_xor_sync(0xffffffffu, word, o);
+                        if (y > x || (y == x && other < word)) {
+                            x = y;
+                            word = other;
+                        }
+                    }
+                    if (word == INT32_MAX) x = -INFINITY;   // no more: the turns go on, as the warp's other rows may have some
+                    if (in && (threadIdx.x & 15) == 0)
+                        ((float2 *)((char *)a.workspace + ws.best))[at * top_k + count] =
+                            make_float2(x, __int_as_float(word == INT32_MAX ? -1 : word));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (n0 + col_of(j) == word) acc[i][j] = -INFINITY;
+                }
+                if (in && (threadIdx.x & 15) == 0)
+                    ((RowStat *)((char *)a.workspace + ws.part))[at] = {top == -INFINITY ? top : base, sum, u, count};
+            } else if (in && (threadIdx.x & 15) == 0)
                 ((float2 *)((char *)a.workspace + ws.part))[(int64_t)row * ws.tiles + blockIdx.x] =
                     make_float2(top == -INFINITY ? top : base, sum);
         }
@@ -189,6 +245,45 @@ __global__ void __launch_bounds__(256) ce_join_kernel(LinearCeArgs a, CeWorkspac
         if (a.loss) a.loss[row] = keep ? lse - ((const float *)((const char *)a.workspace + ws.at))[row] : 0.f;
         if (a.lse) a.lse[row] = keep ? lse : 0.f;
     }
+}
+
+// The same for kStats, with the entropy and the row's K best words.
+template <int K>
+__global__ void __launch_bounds__(256) logp_join_kernel(LinearCeArgs a, CeWorkspace ws, LogProbs out)
+{
+    const int lane = threadIdx.x & 31;
+    const int row = (blockIdx.x * 256 + threadIdx.x) >> 5;
+    if (row >= a.N) return;
+    const RowStat *p = (const RowStat *)((const char *)a.workspace + ws.part) + (int64_t)row * ws.tiles;
+    const float2 *words = (const float2 *)((const char *)a.workspace + ws.best) + (int64_t)row * ws.tiles * out.top_k;
+    float top = -INFINITY;
+    for (int i = lane; i < ws.tiles; i += 32) top = fmaxf(top, p[i].top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = isinf(top) ? 0.f : top;
+    float sum = 0.f, u = 0.f;
+    BestWords<K ? K : 1> best;
+    for (int i = lane; i < ws.tiles; i += 32) {
+        const RowStat v = p[i];
+        const float d = v.top - base, f = expf(d);
+        sum = fmaf(v.sum, f, sum);
+        u = fmaf(f, fmaf(v.top == -INFINITY ? 0.f : d, v.sum, v.u), u);
+        for (int c = 0; c < (K ? v.count : 0); ++c) {
+            const float2 w = words[(int64_t)i * out.top_k + c];
+            if (!(w.x > best.v[K ? K - 1 : 0])) break;   // nor do the worse ones of the tile
+            best.add(w.x, __float_as_int(w.y));
+        }
+    }
+    sum = warp_sum(sum);
+    u = warp_sum(u);
+    const bool keep = kept(a, row);
+    const float ls = logf(sum), lse = base + ls;
+    if (lane == 0) {
+        out.logp[row] = keep ? (((const float *)((const char *)a.workspace + ws.at))[row] - base) - ls : 0.f;
+        out.entropy[row] = keep ? ls - u / sum : 0.f;
+        if (out.lse) out.lse[row] = keep ? lse : 0.f;
+    }
+    if (K) write_best(best, out.top_k, lse, keep, out.top_ids + (int64_t)row * out.top_k, out.top_logps + (int64_t)row * out.top_k);
 }
 
 // dh (+)= G W over one piece; the last piece writes the gradient.
@@ -255,24 +350,36 @@ void over_tiles(int rows, int columns, Launch launch)
 }
 
 template <typename T>
-cudaError_t fwd(const LinearCeArgs &a, cudaStream_t st)
+cudaError_t fwd(const LinearCeArgs &a, cudaStream_t st, const LogProbs *out)
 {
+    if (out) {
+        const CeWorkspace ws = layout(a.N, a.D, a.V, false, out->top_k);
+        over_tiles(a.N, a.V, [&](dim3 grid, int row0) {
+            ce_logits_kernel<T, kStats><<<grid, kThreads, 0, st>>>(a, ws, 0, a.V, row0, LogProbsGrad(), out->top_k);
+        });
+        const int blocks = ceil_div(a.N, 8);
+        if (out->top_k == 0) logp_join_kernel<0><<<blocks, 256, 0, st>>>(a, ws, *out);
+        else if (out->top_k <= 8) logp_join_kernel<8><<<blocks, 256, 0, st>>>(a, ws, *out);
+        else logp_join_kernel<kMostTop><<<blocks, 256, 0, st>>>(a, ws, *out);
+        return cudaGetLastError();
+    }
     const CeWorkspace ws = layout(a.N, a.D, a.V, false);
     over_tiles(a.N, a.V, [&](dim3 grid, int row0) {
-        ce_logits_kernel<T, false><<<grid, kThreads, 0, st>>>(a, ws, 0, a.V, row0);
+        ce_logits_kernel<T, kLoss><<<grid, kThreads, 0, st>>>(a, ws, 0, a.V, row0, LogProbsGrad(), 0);
     });
     ce_join_kernel<<<ceil_div(a.N, 8), 256, 0, st>>>(a, ws);
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t bwd(const LinearCeArgs &a, cudaStream_t st)
+cudaError_t bwd(const LinearCeArgs &a, cudaStream_t st, LogProbsGrad grad)
 {
     const CeWorkspace ws = layout(a.N, a.D, a.V, true);
     for (int v0 = 0; v0 < a.V; v0 += ws.piece) {
         const int cols = a.V - v0 < ws.piece ? a.V - v0 : ws.piece;
         over_tiles(a.N, cols, [&](dim3 grid, int row0) {
-            ce_logits_kernel<T, true><<<grid, kThreads, 0, st>>>(a, ws, v0, cols, row0);
+            (grad.dentropy ? ce_logits_kernel<T, kBackEnt> : ce_logits_kernel<T, kBack>)
+                <<<grid, kThreads, 0, st>>>(a, ws, v0, cols, row0, grad, 0);
         });
         if (a.dh)
             over_tiles(a.N, a.D, [&](dim3 grid, int row0) {
@@ -288,26 +395,26 @@ cudaError_t bwd(const LinearCeArgs &a, cudaStream_t st)
 
 }  // namespace
 
-size_t linear_ce_workspace_bytes(int N, int D, int V, int dt, bool backward)
+size_t linear_ce_workspace_bytes(int N, int D, int V, int dt, bool backward, int top)
 {
-    if (linear_ce_tc_supported(dt, D)) return linear_ce_tc_workspace_bytes(N, D, V, backward);
-    return 256 + layout(N, D, V, backward).total;
+    if (linear_ce_tc_supported(dt, D)) return linear_ce_tc_workspace_bytes(N, D, V, backward, top);
+    return 256 + layout(N, D, V, backward, top).total;
 }
 
-cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a0, cudaStream_t st)
+cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a0, cudaStream_t st, const LogProbs *out)
 {
-    if (linear_ce_tc_supported(a0.dt, a0.D)) return launch_linear_ce_tc_fwd(a0, st);
+    if (linear_ce_tc_supported(a0.dt, a0.D)) return launch_linear_ce_tc_fwd(a0, st, out);
     LinearCeArgs a = a0;
     a.workspace = (char *)a0.workspace + 256;
-    return a.dt ? fwd<__nv_bfloat16>(a, st) : fwd<float>(a, st);
+    return a.dt ? fwd<__nv_bfloat16>(a, st, out) : fwd<float>(a, st, out);
 }
 
-cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a0, cudaStream_t st)
+cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a0, cudaStream_t st, LogProbsGrad grad)
 {
-    if (linear_ce_tc_supported(a0.dt, a0.D)) return launch_linear_ce_tc_bwd(a0, st);
+    if (linear_ce_tc_supported(a0.dt, a0.D)) return launch_linear_ce_tc_bwd(a0, st, grad);
     LinearCeArgs a = a0;
     a.workspace = (char *)a0.workspace + 256;
-    return a.dt ? bwd<__nv_bfloat16>(a, st) : bwd<float>(a, st);
+    return a.dt ? bwd<__nv_bfloat16>(a, st, grad) : bwd<float>(a, st, grad);
 }
 
 }  // namespace gdn

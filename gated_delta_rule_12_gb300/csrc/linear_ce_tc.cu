@@ -3,6 +3,7 @@
 // One persistent kernel form serves the three products, each over 256 x 256 tiles of a pair of CTAs:
 //   logits   [h | w]     A = h  (K = D contiguous),     B = w (K contiguous):    a row's (max, sum) per tile
 //   E        same operands, recomputed for one piece of the vocabulary:          E = softmax - onehot, bf16
+//            (with an entropy's gradient: the gradient of the logits in units of the row's weight, below)
 //   gradients            dW: A = E^T, B = dloss h (both with K = tokens as rows),  dW of the piece
 //                        dh: A = E (K = words contiguous), B = w (K as rows),    fp32 sums over the pieces
 // Tile: tcgen05.mma cta_group::2, M = 256 (128 rows a CTA), N = 256, K = 16 a step; a CTA holds 128 rows of A and
@@ -38,6 +39,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "log_probs.cuh"
 #include "pair_mma.cuh"
 #include "umma.cuh"
 
@@ -58,7 +60,20 @@ constexpr int kSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kStore + 2
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr int kPairs = 76;                 // CTA pairs the GPU holds at once (152 SMs)
 
-enum { kLogits = 0, kProb = 1, kGrads = 2 };
+// kStats: kLogits with what the entropy takes, and a row's best words; kProbEnt: kProb with the entropy's gradient.
+enum { kLogits = 0, kProb = 1, kGrads = 2, kStats = 3, kProbEnt = 4 };
+
+// What a row's gradient of the logits is kept free of: the cross entropy's dloss (sign 1), minus the gradient of a token's
+// log probability (sign -1), or, with a gradient b of the entropy, the larger of the two's magnitudes.
+struct RowWeights {
+    const float *a, *b;
+    float sign;
+    __device__ __forceinline__ float operator()(int row) const
+    {
+        const float x = __ldg(a + row);
+        return b ? fmaxf(fabsf(x), fabsf(__ldg(b + row))) : sign * x;
+    }
+};
 
 // One product C[M, N] = A B^T over `kb` stages of K.
 struct Product {
@@ -76,10 +91,15 @@ struct CeParams {
     int accumulate;           // kGrads: dh adds to the earlier pieces' sums
     int direct;               // kGrads: the only piece, dh in one slice: its tiles are the result
     const int32_t *targets;
-    const float *lse_in, *dloss;
+    const float *lse_in, *entropy;
+    RowWeights weight;
     const float *scale;       // kGrads: s
     float2 *part;             // kLogits: [tiles of 256 words][N]
-    float *at;                // kLogits: [N]
+    RowStat *stat;            // kStats: the same
+    float2 *best;             // kStats: [tiles of 256 words][N][top], a logit and its word's bits
+    unsigned *cut;            // kStats: [N], order_of() of a logit that the row's best words do not fall below; or null
+    int top;
+    float *at;                // kLogits, kStats: [N]
     unsigned *err;
     int clear_err;            // the call's first kernel
     void *out[2];             // kProb: E; kGrads: dW of the piece, dh or its slices
@@ -144,10 +164,12 @@ __device__ __noinline__ void spoil(const CeParams &p, int pair, int pairs, int r
         for (int i = threadIdx.x; i < rows * cols; i += kThreads) {
             const int64_t row = row0 + i / cols;
             const int col = col0 + i % cols;
+            const float nan = __uint_as_float(0x7fffffffu);
             if (MODE == kLogits) {
-                const float nan = __uint_as_float(0x7fffffffu);
                 p.part[(int64_t)c.n * p.N + row] = make_float2(nan, nan);
-            } else if (MODE == kProb) {
+            } else if (MODE == kStats) {
+                p.stat[(int64_t)c.n * p.N + row] = {nan, nan, nan, 0};
+            } else if (MODE == kProb || MODE == kProbEnt) {
                 static_cast<unsigned short *>(p.out[0])[row * p.pitch + col] = 0x7fff;
             } else if (c.which == 0 || p.direct) {
                 static_cast<unsigned short *>(p.out[c.which])[row * p.D + col] = 0x7fff;
@@ -158,7 +180,8 @@ __device__ __noinline__ void spoil(const CeParams &p, int pair, int pairs, int r
     }
 }
 
-template <int MODE>
+// K: the best words that a thread keeps in kStats, at least p.top.
+template <int MODE, int K = 0>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CeParams p)
 {
@@ -293,15 +316,28 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
             const bool direct = MODE == kGrads && c.which == 1 && p.direct;
             if ((MODE != kGrads || direct) && in) {
                 target = __ldg(p.targets + row);
-                if (MODE == kProb) lse = __ldg(p.lse_in + row);
-                if (direct) scale = __ldg(p.dloss + row);
+                if (MODE == kProb || MODE == kProbEnt) lse = __ldg(p.lse_in + row);
+                if (direct) scale = p.weight(row);
+            }
+            float ca = 0.f, cb = 0.f, entropy = 0.f;   // kProbEnt: the gradients in units of the row's weight
+            if (MODE == kProbEnt && in) {
+                const float r = p.weight(row), inv = r != 0.f ? 1.f / r : 0.f;
+                ca = __ldg(p.weight.a + row) * inv;
+                cb = __ldg(p.weight.b + row) * inv;
+                entropy = __ldg(p.entropy + row);
             }
             if (MODE == kGrads && c.which == 0) scale = __ldg(p.scale);
             const bool keep = (MODE == kGrads && !direct) || (target >= 0 && target < p.V);
             if (!__all_sync(0xffffffffu, wait_bar(acc_full + 8 * buf, use & 1, abort_flag, p))) break;
             fence_after_sync();
             const uint32_t src = tmem + buf * 256 + (quarter << 21);   // lane field: bits 16 and up
-            float top = -INFINITY, sum = 0.f;
+            float top = -INFINITY, sum = 0.f, u = 0.f;
+            BestWords<K ? K : 1> best;
+            float cut = -INFINITY;                     // words at or below it are not among the row's best
+            if (K && in && p.cut) {
+                const unsigned c = *(volatile const unsigned *)(p.cut + row);
+                if (c) cut = below(c);   // words equal to it may be; 0: no such logit yet
+            }
 #pragma unroll 1
             for (int ch = 0; ch < chunks; ++ch) {
                 uint32_t r[32];
@@ -313,7 +349,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                     if (lane == 0) arrive_remote(leader_empty + 8 * buf);
                 }
                 const int c0 = col0 + ch * 32;   // within the piece for kProb
-                if (MODE == kLogits) {
+                if (MODE == kLogits || MODE == kStats) {
                     if (c0 + 32 > p.V) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -328,15 +364,47 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(r[j]));
-                    const float higher = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                    const float here = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), higher = fmaxf(top, here);
                     // the base keeps infinities and NaN in the sum instead of making them NaN by themselves
                     const float was = isinf(top) ? 0.f : top, now = isinf(higher) ? 0.f : higher;
-                    if (top != -INFINITY) sum *= __expf(was - now);
+                    if (top != -INFINITY) {
+                        const float f = __expf(was - now);
+                        if (MODE == kStats) u = f * fmaf(was - now, sum, u);
+                        sum *= f;
+                    }
                     top = higher;
-                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+                    float s4[4] = {0.f, 0.f, 0.f, 0.f}, u4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) s4[j & 3] += __expf(__uint_as_float(r[j]) - now);
+                    for (int j = 0; j < 32; ++j) {
+                        const float d = __uint_as_float(r[j]) - now, e = __expf(d);
+                        s4[j & 3] += e;
+                        if (MODE == kStats) u4[j & 3] = fmaf(e, fmaxf(d, -1e4f), u4[j & 3]);   // 0 times -inf is 0 here
+                    }
                     sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    if (MODE == kStats) u += (u4[0] + u4[1]) + (u4[2] + u4[3]);
+                    if (K && __any_sync(0xffffffffu, in && here > cut)) {
+                        // Words that may be among the best come out one at a time, each lane its own: found by their bits,
+                        // then read back from the warp's buffer, as registers have no variable index.
+                        const uint32_t row_s = buf0 + lane * 128;
+                        unsigned some = 0u;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            st_shared16(row_s + ((j ^ (lane & 7)) << 4), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) some |= (__uint_as_float(r[j]) > cut ? 1u : 0u) << j;
+                        if (!in) some = 0u;
+                        while (__any_sync(0xffffffffu, some != 0u)) {
+                            if (some) {
+                                const int j = __ffs((int)some) - 1;
+                                some &= some - 1u;
+                                float x;
+                                asm volatile("ld.shared.f32 %0, [%1];"
+                                             : "=f"(x) : "r"(row_s + (((j >> 2) ^ (lane & 7)) << 4) + (j & 3) * 4) : "memory");
+                                best.add(x, c0 + j);
+                            }
+                        }
+                        cut = fmaxf(cut, best.value(p.top - 1));
+                    }
                 } else {
                     // 128-byte rows of the warp's buffer: 64 bf16, two chunks of 32 columns, or 32 fp32
                     const bool fp32 = MODE == kGrads && c.which == 1 && !direct;
@@ -359,6 +427,14 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                                 const float e = __expf(__uint_as_float(r[j]) - lse);
                                 r[j] = __float_as_uint(keep ? e - (j == hot ? 1.f : 0.f) : 0.f);
                             }
+                        } else if (MODE == kProbEnt) {
+                            const int hot = target - p.v0 - c0;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float z = __uint_as_float(r[j]) - lse, e = __expf(z);
+                                const float g = e * fmaf(cb, fmaxf(z, -1e4f) + entropy, ca);   // 0 times -inf is 0 here
+                                r[j] = __float_as_uint(keep ? (j == hot ? ca : 0.f) - g : 0.f);
+                            }
                         } else {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(keep ? __uint_as_float(r[j]) * scale : 0.f);
@@ -378,7 +454,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                         if (lane == 0) {
                             const uint32_t from = buf0;
                             const int x = fp32 ? c0 : c0 - 32;
-                            if (MODE == kProb) {
+                            if (MODE == kProb || MODE == kProbEnt) {
                                 if (x < p.cols && row0 < p.N) store_2d(&maps.out[0], from, x, row0);
                             } else if (c.which == 0) {
                                 if (x < p.D && row0 < p.cols) store_2d(&maps.out[0], from, x, p.v0 + row0);
@@ -394,8 +470,19 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
             }
             if (MODE == kLogits && in)
                 p.part[(int64_t)c.n * p.N + row] = make_float2(top == -INFINITY ? top : (isinf(top) ? 0.f : top), sum);
+            if (MODE == kStats && in) {
+                const int64_t at = (int64_t)c.n * p.N + row;
+                const int count = K ? best.count(p.top) : 0;
+                p.stat[at] = {top == -INFINITY ? top : (isinf(top) ? 0.f : top), sum, u, count};
+                if (K) {
+#pragma unroll
+                    for (int i = 0; i < K; ++i)
+                        if (i < count) p.best[at * p.top + i] = make_float2(best.v[i], __int_as_float(best.id[i]));
+                    if (p.cut && count == p.top) atomicMax(p.cut + row, order_of(best.value(p.top - 1)));
+                }
+            }
         }
-        if (MODE != kLogits && lane == 0) bulk_wait_all();
+        if (MODE != kLogits && MODE != kStats && lane == 0) bulk_wait_all();
     }
     __syncwarp();
     fence_before_sync();
@@ -445,14 +532,78 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_tc_join_kernel(const CePar
     }
 }
 
+// The same for kStats, with the entropy; K: the row's best words, a warp a row.
+template <int K>
+__global__ void __launch_bounds__(32 * kJoinWarps) logp_tc_join_kernel(const CeParams p, int words, LogProbs out)
+{
+    __shared__ float tops[kJoinWarps][32], sums[kJoinWarps][32], us[kJoinWarps][32], lses[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x * 32 + lane;
+    wait_previous();
+    const RowStat *stat = p.stat + (row < p.N ? row : 0);
+    float top = -INFINITY, sum = 0.f, u = 0.f;
+#pragma unroll 8
+    for (int i = warp; i < words; i += kJoinWarps) top = fmaxf(top, stat[(int64_t)i * p.N].top);
+    tops[warp][lane] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, tops[i][lane]);
+    const float base = isinf(top) ? 0.f : top;   // keeps infinities and NaN in the sum
+#pragma unroll 8
+    for (int i = warp; i < words; i += kJoinWarps) {
+        const float4 v = *reinterpret_cast<const float4 *>(stat + (int64_t)i * p.N);
+        const float d = v.x - base, f = expf(d);
+        sum = fmaf(v.y, f, sum);
+        u = fmaf(f, fmaf(v.x == -INFINITY ? 0.f : d, v.y, v.z), u);
+    }
+    sums[warp][lane] = sum;
+    us[warp][lane] = u;
+    __syncthreads();
+    if (warp == 0) {
+        sum = u = 0.f;
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) {
+            sum += sums[i][lane];
+            u += us[i][lane];
+        }
+        const float ls = logf(sum);
+        lses[lane] = base + ls;
+        if (row < p.N) {
+            const int t = p.targets[row];
+            const bool keep = t >= 0 && t < p.V;
+            out.logp[row] = keep ? (p.at[row] - base) - ls : 0.f;
+            out.entropy[row] = keep ? ls - u / sum : 0.f;
+            if (out.lse) out.lse[row] = keep ? base + ls : 0.f;
+        }
+    }
+    if (K == 0) return;
+    __syncthreads();
+    for (int i = warp; i < 32; i += kJoinWarps) {
+        const int r = blockIdx.x * 32 + i;
+        if (r >= p.N) break;
+        BestWords<K ? K : 1> best;
+        for (int n = lane; n < words; n += 32) {
+            const int64_t at = (int64_t)n * p.N + r;
+            const int count = p.stat[at].count;
+            for (int c = 0; c < count; ++c) {
+                const float2 v = p.best[at * p.top + c];
+                if (!(v.x > best.v[K ? K - 1 : 0])) break;   // nor do the worse ones of the tile
+                best.add(v.x, __float_as_int(v.y));
+            }
+        }
+        const int t = p.targets[r];
+        write_best(best, p.top, lses[i], t >= 0 && t < p.V, out.top_ids + (int64_t)r * p.top, out.top_logps + (int64_t)r * p.top);
+    }
+}
+
 // s = max |dloss| over the kept rows, finite, and 1 where that is 0; the same in every thread of the block.
-__device__ __forceinline__ float largest_weight(const float *dloss, const int32_t *targets, int N, int V)
+__device__ __forceinline__ float largest_weight(RowWeights weight, const int32_t *targets, int N, int V)
 {
     __shared__ float sh[32];
     float m = 0.f;
     for (int i = threadIdx.x; i < N; i += blockDim.x) {
         const int t = __ldg(targets + i);
-        if (t >= 0 && t < V) m = fmaxf(m, fabsf(__ldg(dloss + i)));
+        if (t >= 0 && t < V) m = fmaxf(m, fabsf(weight(i)));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -463,10 +614,10 @@ __device__ __forceinline__ float largest_weight(const float *dloss, const int32_
     return m > 0.f ? fminf(m, 3.402823466e38f) : 1.f;
 }
 
-__global__ void __launch_bounds__(1024) ce_scale_kernel(const float *dloss, const int32_t *targets, int N, int V,
+__global__ void __launch_bounds__(1024) ce_scale_kernel(RowWeights weight, const int32_t *targets, int N, int V,
                                                         float *scale)
 {
-    const float s = largest_weight(dloss, targets, N, V);
+    const float s = largest_weight(weight, targets, N, V);
     if (threadIdx.x == 0) *scale = s;
 }
 
@@ -481,15 +632,15 @@ constexpr int kOwnScale = 4096;
 
 template <bool OWN>
 __global__ void __launch_bounds__(256) ce_weighted_rows_kernel(const uint4 *h, uint4 *out, const int32_t *targets,
-                                                               const float *dloss, float *scale, int N, int D8, int V)
+                                                               RowWeights weight, float *scale, int N, int D8, int V)
 {
-    const float s = OWN ? largest_weight(dloss, targets, N, V) : *scale;
+    const float s = OWN ? largest_weight(weight, targets, N, V) : *scale;
     if (OWN && blockIdx.x == 0 && threadIdx.x == 0) *scale = s;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)N * D8; i += (int64_t)gridDim.x * 256) {
         const int row = (int)(i / D8), t = __ldg(targets + row);
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (t >= 0 && t < V) {
-            const float f = __ldg(dloss + row) / s;
+            const float f = weight(row) / s;
             v = h[i];
             v = make_uint4(scale_bf16x2(v.x, f), scale_bf16x2(v.y, f), scale_bf16x2(v.z, f), scale_bf16x2(v.w, f));
         }
@@ -499,13 +650,13 @@ __global__ void __launch_bounds__(256) ce_weighted_rows_kernel(const uint4 *h, u
 
 // dh = dloss times the sum of its slices, in order, rounded; 0 in the ignored rows.
 __global__ void __launch_bounds__(256) ce_dh_finish_kernel(const float4 *acc, uint2 *dh, const int32_t *targets,
-                                                           const float *dloss, int N, int D4, int V, int slices)
+                                                           RowWeights weight, int N, int D4, int V, int slices)
 {
     const int64_t n = (int64_t)N * D4;
     wait_previous();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int row = (int)(i / D4), t = __ldg(targets + row);
-        const float f = __ldg(dloss + row);
+        const float f = weight(row);
         float4 s = acc[i];
         for (int j = 1; j < slices; ++j) {
             const float4 v = acc[i + j * n];
@@ -535,6 +686,7 @@ bool make_map(CUtensorMap *m, const void *base, int cols, int rows, int64_t pitc
 
 struct TcWorkspace {
     size_t part, at;          // forward
+    size_t best, cut;         // log probabilities, forward: [tiles of words][N][top], [N]
     // backward: E of a piece [N][piece], h dloss / s of the kept rows [N][D], dh's slices [.][N][D], s
     size_t e, hk, acc, scale;
     size_t total;
@@ -542,13 +694,17 @@ struct TcWorkspace {
     bool direct;              // one piece, one slice: dh needs no sums
 };
 
-TcWorkspace tc_layout(int N, int D, int V, bool backward)
+// top: the best words of a log-probability call, -1 for the cross entropy
+TcWorkspace tc_layout(int N, int D, int V, bool backward, int top = -1)
 {
     TcWorkspace w = {};
     size_t off = 256;
     if (!backward) {
-        w.part = off; off = align256(off + (size_t)N * ceil_div(V, kTile) * 8);
+        const size_t parts = (size_t)N * ceil_div(V, kTile);
+        w.part = off; off = align256(off + parts * (top < 0 ? sizeof(float2) : sizeof(RowStat)));
         w.at = off;   off = align256(off + (size_t)N * 4);
+        w.best = off; off = align256(off + (top > 0 ? parts * top * sizeof(float2) : 0));
+        w.cut = off;  off = align256(off + (top > 0 ? (size_t)N * 4 : 0));
     } else {
         // pieces of equal size whose E takes up to 128 MB (8192 x 2048 x 65536: 32 MB 4.39 ms, 64 MB 3.99, 128 MB 3.67,
         // 512 MB 3.55)
@@ -574,15 +730,15 @@ TcWorkspace tc_layout(int N, int D, int V, bool backward)
     return w;
 }
 
-template <int MODE>
+template <int MODE, int K = 0>
 cudaError_t launch(const CeMaps &maps, CeParams p, cudaStream_t st, const CeStall &stall)
 {
     p.silent = stall.step == MODE ? 0 : -1;
     p.limit_ns = stall.step == MODE ? stall.limit_ns : kWaitLimitNs;
-    const cudaError_t e = cudaFuncSetAttribute(ce_tc_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(ce_tc_kernel<MODE, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int pairs = p.tiles < kPairs ? p.tiles : kPairs;
-    return launch_early(ce_tc_kernel<MODE>, 2 * pairs, kThreads, kSmem, st, maps, p);
+    return launch_early(ce_tc_kernel<MODE, K>, 2 * pairs, kThreads, kSmem, st, maps, p);
 }
 
 unsigned grid_for(int64_t items)
@@ -597,11 +753,22 @@ unsigned grid_for(int64_t items)
 // after which the epilogue's wait gives up before 2^28.
 bool linear_ce_tc_supported(int dt, int D) { return dt == 1 && D % 8 == 0 && D <= 1 << 24; }
 
-size_t linear_ce_tc_workspace_bytes(int N, int D, int V, bool backward) { return tc_layout(N, D, V, backward).total; }
-
-cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, CeStall stall)
+size_t linear_ce_tc_workspace_bytes(int N, int D, int V, bool backward, int top)
 {
-    const TcWorkspace ws = tc_layout(a.N, a.D, a.V, false);
+    return tc_layout(N, D, V, backward, top).total;
+}
+
+template <int K>
+static cudaError_t run_stats(const CeMaps &maps, const CeParams &p, const LogProbs &out, cudaStream_t st)
+{
+    const cudaError_t e = launch<kStats, K>(maps, p, st, CeStall());
+    if (e != cudaSuccess) return e;
+    return launch_early(logp_tc_join_kernel<K>, ceil_div(p.N, 32), 32 * kJoinWarps, 0, st, p, p.p[0].nt, out);
+}
+
+cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, const LogProbs *out, CeStall stall)
+{
+    const TcWorkspace ws = tc_layout(a.N, a.D, a.V, false, out ? out->top_k : -1);
     char *w = (char *)a.workspace;
     CeMaps maps;
     memset(&maps, 0, sizeof(maps));
@@ -616,28 +783,42 @@ cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, CeSt
     p.at = (float *)(w + ws.at);
     p.err = (unsigned *)w;
     p.clear_err = 1;
+    if (out) {
+        p.stat = (RowStat *)(w + ws.part);
+        p.best = (float2 *)(w + ws.best);
+        p.top = out->top_k;
+        // Tiles tell later ones of their rows what need not be kept, where there are rounds of them to tell.
+        if (p.top > 0 && p.tiles > 4 * kPairs) {
+            p.cut = (unsigned *)(w + ws.cut);
+            const cudaError_t e = cudaMemsetAsync(p.cut, 0, (size_t)a.N * 4, st);
+            if (e != cudaSuccess) return e;
+        }
+        return p.top == 0 ? run_stats<0>(maps, p, *out, st) : p.top <= 8 ? run_stats<8>(maps, p, *out, st)
+                                                                      : run_stats<kMostTop>(maps, p, *out, st);
+    }
     const cudaError_t e = launch<kLogits>(maps, p, st, stall);
     if (e != cudaSuccess) return e;
     return launch_early(ce_tc_join_kernel, ceil_div(a.N, 32), 32 * kJoinWarps, 0, st, p, p.p[0].nt, a.loss, a.lse);
 }
 
-cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st, CeStall stall)
+cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st, LogProbsGrad grad, CeStall stall)
 {
     const TcWorkspace ws = tc_layout(a.N, a.D, a.V, true);
     char *w = (char *)a.workspace;
     const int mt = ceil_div(a.N, kTile), dt = ceil_div(a.D, kTile);
     CeParams p = {};
     p.N = a.N; p.V = a.V; p.D = a.D;
-    p.targets = a.targets; p.lse_in = a.lse_in; p.dloss = a.dloss;
+    p.targets = a.targets; p.lse_in = a.lse_in; p.entropy = grad.entropy;
+    p.weight = {a.dloss, grad.dentropy, grad.sign};
     p.direct = ws.direct;
     p.scale = (float *)(w + ws.scale);
     p.err = (unsigned *)w;
     if (a.dw) {
         const bool own = a.N <= kOwnScale;
-        if (!own) ce_scale_kernel<<<1, 1024, 0, st>>>(a.dloss, a.targets, a.N, a.V, (float *)(w + ws.scale));
+        if (!own) ce_scale_kernel<<<1, 1024, 0, st>>>(p.weight, a.targets, a.N, a.V, (float *)(w + ws.scale));
         (own ? ce_weighted_rows_kernel<true> : ce_weighted_rows_kernel<false>)
             <<<grid_for((int64_t)a.N * a.D / 8), 256, 0, st>>>((const uint4 *)a.h, (uint4 *)(w + ws.hk), a.targets,
-                                                               a.dloss, (float *)(w + ws.scale), a.N, a.D / 8, a.V);
+                                                               p.weight, (float *)(w + ws.scale), a.N, a.D / 8, a.V);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -664,7 +845,7 @@ cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st, CeSt
         p.tiles0 = p.tiles = mt * p.p[0].nt;
         p.out[0] = w + ws.e;
         p.pitch = ws.piece;
-        cudaError_t e = launch<kProb>(mg, p, st, stall);
+        cudaError_t e = grad.dentropy ? launch<kProbEnt>(mg, p, st, stall) : launch<kProb>(mg, p, st, stall);
         if (e != cudaSuccess) return e;
         p.p[0] = {ceil_div(cols, kTile), dt, ceil_div(a.N, kDepth), 1, 0};
         p.p[1] = {mt, dt, ceil_div(cols, kDepth), ws.slices, v0};
@@ -679,7 +860,7 @@ cudaError_t launch_linear_ce_tc_bwd(const LinearCeArgs &a, cudaStream_t st, CeSt
     }
     if (!a.dh || ws.direct) return cudaSuccess;
     return launch_early(ce_dh_finish_kernel, grid_for((int64_t)a.N * a.D / 4), 256, 0, st, (const float4 *)(w + ws.acc),
-                        (uint2 *)a.dh, a.targets, a.dloss, a.N, a.D / 4, a.V, ws.slices);
+                        (uint2 *)a.dh, a.targets, p.weight, a.N, a.D / 4, a.V, ws.slices);
 }
 
 }  // namespace gdn

@@ -510,6 +510,46 @@ gdn_status gdn_linear_cross_entropy_bwd(const void *h, const void *weight, const
                                         void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Log probabilities of given tokens under a linear head, with the entropy of each row's distribution and its most probable
+ * words, without an [N, V] array of logits; l_iv = h_i . w_v:
+ *     lse_i = log sum_v exp(l_iv),  logp_i = l_{i,targets_i} - lse_i,  entropy_i = lse_i - sum_v exp(l_iv - lse_i) l_iv.
+ *   h, weight, targets  as gdn_linear_cross_entropy_fwd.  A row whose target lies outside [0, V) is ignored: its results
+ *                 are 0, its top_ids -1.
+ *   logp, entropy [N] fp32;  lse [N] fp32 or NULL to skip (the backward pass needs it).
+ *   top_ids, top_logps  [N, top_k] int32 and fp32: the words of the largest logits and their log probabilities, equal
+ *                 logits by the lower index.  0 <= top_k <= GDN_MOST_TOP, top_k <= V; NULL with top_k = 0.  Words whose
+ *                 logit is -inf or NaN are none; where too few others are left, ids are -1 and log probabilities -inf.
+ *   workspace     at least gdn_linear_log_probs_workspace_size(..., backward = 0) bytes, 256-byte aligned (about
+ *                 N V (2 + top_k) / 32 bytes, on the CUDA cores twice that); its first 256 bytes as those of the cross
+ *                 entropy's.
+ * Sizes, types, precision, waits and errors as gdn_linear_cross_entropy_fwd.
+ */
+#define GDN_MOST_TOP 20
+
+size_t gdn_linear_log_probs_workspace_size(int32_t N, int32_t D, int32_t V, int32_t top_k, gdn_dtype dt,
+                                           int32_t backward);
+
+gdn_status gdn_linear_log_probs_fwd(const void *h, const void *weight, const int32_t *targets,
+                                    float *logp, float *entropy, float *lse, int32_t *top_ids, float *top_logps,
+                                    int32_t N, int32_t D, int32_t V, int32_t top_k, gdn_dtype dt,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of gdn_linear_log_probs_fwd for the gradients dlogp and dentropy, with p_iv = exp(l_iv - lse_i):
+ *     G_iv = dlogp_i ([v = targets_i] - p_iv) - dentropy_i p_iv (log p_iv + entropy_i),  dh = G weight,  dweight = G^T h.
+ *   lse, entropy  [N] fp32 of the forward call (entropy may be NULL where dentropy is).
+ *   dlogp         [N] fp32;  dentropy [N] fp32 or NULL for zeros.
+ *   dh, dweight, workspace (its size with backward = 1, whatever top_k is), ignored rows and errors as
+ *                 gdn_linear_cross_entropy_bwd.
+ * On the tensor cores G enters the products as bf16 in units of each row's max(|dlogp|, |dentropy|) (of -dlogp without
+ * dentropy), and that times h as bf16 in units of the largest; sums are fp32.
+ */
+gdn_status gdn_linear_log_probs_bwd(const void *h, const void *weight, const int32_t *targets,
+                                    const float *lse, const float *entropy, const float *dlogp, const float *dentropy,
+                                    void *dh, void *dweight, int32_t N, int32_t D, int32_t V, gdn_dtype dt,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Self-test of the cross entropy's failure path: the bf16 call (step 0: forward, out0 = loss, out1 = lse; steps 1 and 2:
  * backward, out0 = dh, out1 = dweight; out1 may be NULL) in whose logits (0), softmax (1) or gradient (2) kernel the data
  * of one tile never comes.  Its waits give up after limit_us microseconds (1 .. 1e6), nothing faults,

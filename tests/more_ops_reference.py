@@ -69,3 +69,65 @@ def fp8_linear(x, xs, w, ws):
     a = f64(x.float()) * spread(xs, M, K, 1)
     b = f64(w.float()) * spread(ws, N, K, 128)
     return a @ b.T, 2 * (128 + -(-K // 128) + 4) * U * (a.abs() @ b.abs().T)
+
+
+def _logits(h, w):
+    # fp32 sums of D products in any order, an accumulator that truncates counted double
+    return h @ w.T, 2 * U * (h.shape[1] + 2) * (h.abs() @ w.abs().T)
+
+
+def _kept(targets, V):
+    t = targets.cpu().long()
+    return t, (t >= 0) & (t < V)
+
+
+def log_probs_fwd(h, w, targets, k):
+    """(logp, entropy, lse, ids, top logps) and bounds; ids by the 64-bit logits, equal ones by the lower index."""
+    h, w = f64(h), f64(w)
+    V = w.shape[0]
+    t, keep = _kept(targets, V)
+    h = torch.where(keep[:, None], h, 0.0)
+    l, el = _logits(h, w)
+    el = el.max(-1, keepdim=True).values
+    top = l.max(-1, keepdim=True).values
+    lse = torch.logsumexp(l, -1, keepdim=True)
+    lp = l - lse
+    p, d = lp.exp(), l - top
+    H = -(p * lp).sum(-1)
+    # as the cross entropy's: the largest logit error, the sum's roundings, the logarithm's and the differences'
+    e = (el + (V / 128 + 40) * U + 4 * U * (lse.abs() + l.abs().max(-1, keepdim=True).values))[:, 0]
+    # entropy: an error of a logit counts p |log p + H|, that of an exponential's term (its argument's rounding, in units
+    # of log2 e too, and the sums') once in log S and, times |d| + U / S, in U / S
+    term = (V / 128 + 48) * U + 6 * U * d.abs()
+    eH = (p * term * (1 + d.abs() + (p * d).sum(-1, keepdim=True).abs())).sum(-1) + \
+        2 * (el * (p * (lp + H[:, None]).abs()).sum(-1, keepdim=True))[:, 0] + 6 * U * (H + (lse - top).abs()[:, 0])
+    z = torch.zeros_like(H)
+    v, ids = torch.sort(lp, dim=-1, descending=True, stable=True)
+    rows = [torch.where(keep, x, z) for x in (lp.gather(1, t.clamp(0, V - 1)[:, None])[:, 0], H, lse[:, 0])]
+    return (*rows, torch.where(keep[:, None], ids[:, :k], -1), torch.where(keep[:, None], v[:, :k], 0.0)), (2 * e, eH, e, 2 * e)
+
+
+def log_probs_bwd(h, w, targets, lse, H, da, db, low_bits):
+    """(dh, dweight) and bounds, for the given lse and H.  ``low_bits``: the logits' gradient enters the products rounded to
+    bfloat16 in units of its row's weight, and dweight's other factor, that weight times h, is rounded too."""
+    h, w, lse, da = f64(h), f64(w), f64(lse), f64(da)
+    N, V = h.shape[0], w.shape[0]
+    t, keep = _kept(targets, V)
+    h = torch.where(keep[:, None], h, 0.0)
+    a = torch.where(keep, da, 0.0)[:, None]
+    b = torch.where(keep, f64(db), 0.0)[:, None] if db is not None else torch.zeros_like(a)
+    H = torch.where(keep, f64(H), 0.0)[:, None] if db is not None else torch.zeros_like(a)
+    lse = torch.where(keep, lse, 0.0)[:, None]
+    l, el = _logits(h, w)
+    lp = l - lse
+    p = lp.exp()
+    hot = torch.nn.functional.one_hot(t.clamp(0, V - 1), V).double()
+    G = a * (hot - p) - b * p * (lp + H)
+    ep = (el + 4 * U * (l.abs() + lse.abs()) + 4 * U) * 1.01          # relative, of p
+    eG = p * (a.abs() * ep + b.abs() * (ep * (lp + H).abs() + el + 4 * U * (l.abs() + lse.abs() + H.abs())))
+    eG = eG + 6 * U * (a.abs() * (hot + p) + b.abs() * p * (lp + H).abs())
+    if low_bits:
+        eG = eG + BF16 * G.abs()
+    edh = eG @ w.abs() + 2 * U * (V + 64) * (G.abs() @ w.abs())
+    edw = (eG + (BF16 if low_bits else 0.0) * G.abs()).T @ h.abs() + 2 * U * (N + 64) * (G.abs().T @ h.abs())
+    return (G @ w, G.T @ h), (edh, edw)

@@ -1,5 +1,5 @@
-"""Refusals of the root-mean-square norm, the 8-bit quantising and the product of 8-bit operands; no GPU is needed (the
-pointers below are never dereferenced: validation fails first)."""
+"""Refusals of the root-mean-square norm, the 8-bit quantising, the product of 8-bit operands and the token log
+probabilities; no GPU is needed (the pointers below are never dereferenced: validation fails first)."""
 import pytest
 import torch
 
@@ -27,6 +27,10 @@ RMS_BWD = dict(dout=FAKE, x=FAKE, rstd=FAKE, w=FAKE, dres=FAKE, dx=FAKE, dw=FAKE
                wsb=1 << 40, stream=None)
 QUANT = dict(x=FAKE, q=FAKE, c=FAKE, rows=4, D=16, br=1, dt=0, stream=None)
 LINEAR = dict(x=FAKE, xs=FAKE, w=FAKE, ws=FAKE, out=FAKE, M=4, N=16, K=32, work=FAKE, size=1 << 40, stream=None)
+LOGP = dict(h=FAKE, w=FAKE, t=FAKE, logp=FAKE, ent=FAKE, lse=FAKE, ids=FAKE, top=FAKE, N=4, D=16, V=32, k=3, dt=0,
+            work=FAKE, size=1 << 40, stream=None)
+LOGP_BWD = dict(h=FAKE, w=FAKE, t=FAKE, lse=FAKE, ent=FAKE, da=FAKE, db=FAKE, dh=FAKE, dw=FAKE, N=4, D=16, V=32, dt=0,
+                work=FAKE, size=1 << 40, stream=None)
 
 
 @pytest.mark.parametrize("over", [dict(rows=-1), dict(D=0), dict(dt=5), dict(x=None), dict(out=None), dict(eps=-1.0),
@@ -69,6 +73,25 @@ def test_linear_refusals(lib, over, code):
     assert call(lib.gdn_fp8_linear, LINEAR, over) == code
 
 
+@pytest.mark.parametrize("over,code", [(dict(N=-1), 1), (dict(D=0), 1), (dict(V=0, k=0), 1), (dict(dt=3), 1), (dict(k=-1), 1),
+                                       (dict(k=21), 1), (dict(V=2), 1), (dict(h=None), 1), (dict(w=None), 1),
+                                       (dict(t=None), 1), (dict(logp=None), 1), (dict(ent=None), 1), (dict(ids=None), 1),
+                                       (dict(top=None), 1), (dict(ids=FAKE + 2), 1), (dict(ent=FAKE + 1), 1),
+                                       (dict(h=FAKE + 8), 1), (dict(work=None), 3), (dict(work=FAKE + 64), 3),
+                                       (dict(size=256), 3), (dict(N=(1 << 23) + 1), 2), (dict(V=(1 << 30) + 1), 2)])
+def test_log_probs_fwd_refusals(lib, over, code):
+    assert call(lib.gdn_linear_log_probs_fwd, LOGP, over) == code
+
+
+@pytest.mark.parametrize("over,code", [(dict(N=-1), 1), (dict(dt=3), 1), (dict(h=None), 1), (dict(w=None), 1),
+                                       (dict(t=None), 1), (dict(lse=None), 1), (dict(da=None), 1), (dict(ent=None), 1),
+                                       (dict(db=FAKE + 2), 1), (dict(ent=FAKE + 2), 1), (dict(dh=FAKE + 8), 1),
+                                       (dict(dw=FAKE + 8), 1), (dict(work=None), 3), (dict(size=256), 3),
+                                       (dict(V=(1 << 30) + 1), 2)])
+def test_log_probs_bwd_refusals(lib, over, code):
+    assert call(lib.gdn_linear_log_probs_bwd, LOGP_BWD, over) == code
+
+
 def test_nothing_to_do(lib):
     """No rows: nothing is enqueued, and no pointer to rows is needed."""
     assert call(lib.gdn_rms_norm_fwd, RMS, dict(rows=0, x=None, out=None, res=None, sum=None)) == 0
@@ -76,6 +99,8 @@ def test_nothing_to_do(lib):
     assert call(lib.gdn_rms_norm_bwd, RMS_BWD, dict(dx=None, dw=None)) == 0
     assert call(lib.gdn_fp8_quantize, QUANT, dict(rows=0, x=None, q=None, c=None)) == 0
     assert call(lib.gdn_fp8_linear, LINEAR, dict(M=0, x=None, xs=None, out=None)) == 0
+    assert call(lib.gdn_linear_log_probs_fwd, LOGP, dict(N=0, h=None, t=None, logp=None, ent=None, ids=None, top=None)) == 0
+    assert call(lib.gdn_linear_log_probs_bwd, LOGP_BWD, dict(dh=None, dw=None)) == 0
 
 
 def test_workspace_sizes(lib):
@@ -83,13 +108,25 @@ def test_workspace_sizes(lib):
     assert gdn.rms_norm_bwd_workspace_size(8, 512) >= 512 * 4
     assert gdn.fp8_linear_workspace_size(1 << 32, 8, 8) == 0 and gdn.fp8_linear_workspace_size(8, 8, 0) == 0
     assert gdn.fp8_linear_workspace_size(0, 8, 8) >= 256
+    size = gdn.linear_log_probs_workspace_size
+    assert size(4, 8, 4, 5) == 0 and size(4, 8, 40, 21) == 0 and size(4, 8, 40, -1) == 0 and size(1 << 33, 8, 40) == 0
+    assert 0 < size(4, 8, 40) < size(4, 8, 40, 5) < size(4, 8, 40, 20)
 
 
 def test_python_refusals(lib):
     x, w = torch.zeros(4, 128), torch.ones(128)
     e = torch.zeros(4, 128, dtype=torch.uint8).view(torch.float8_e4m3fn)
     c, cw = torch.ones(4, 1), torch.ones(1, 1)
+    h, t, z = torch.zeros(4, 16), torch.zeros(4, dtype=torch.int32), torch.zeros(4)
     wrong = [
+        (ValueError, lambda: gdn.linear_log_probs_fwd(h, h, t, top_k=5)),
+        (ValueError, lambda: gdn.linear_log_probs_fwd(h, h, t[:3])),
+        (TypeError, lambda: gdn.linear_log_probs_fwd(h, h, t.long())),
+        (TypeError, lambda: gdn.linear_log_probs_fwd(h, h.bfloat16(), t)),
+        (ValueError, lambda: gdn.linear_log_probs_fwd(h, h, t)),
+        (ValueError, lambda: gdn.linear_log_probs_bwd(h, h, t, z, None, z, z)),
+        (TypeError, lambda: gdn.linear_log_probs_bwd(h, h, t, z, z, z.double())),
+        (ValueError, lambda: gdn.linear_log_probs_bwd(h, h, t, z, z, z, z[:2])),
         (ValueError, lambda: gdn.rms_norm_fwd(x, w)),                                    # not on the GPU
         (ValueError, lambda: gdn.rms_norm_fwd(torch.zeros(()), None)),
         (ValueError, lambda: gdn.rms_norm_fwd(x, w[:100])),
