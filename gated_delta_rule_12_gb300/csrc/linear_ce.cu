@@ -247,45 +247,6 @@ __global__ void __launch_bounds__(256) ce_join_kernel(LinearCeArgs a, CeWorkspac
     }
 }
 
-// The same for kStats, with the entropy and the row's K best words.
-template <int K>
-__global__ void __launch_bounds__(256) logp_join_kernel(LinearCeArgs a, CeWorkspace ws, LogProbs out)
-{
-    const int lane = threadIdx.x & 31;
-    const int row = (blockIdx.x * 256 + threadIdx.x) >> 5;
-    if (row >= a.N) return;
-    const RowStat *p = (const RowStat *)((const char *)a.workspace + ws.part) + (int64_t)row * ws.tiles;
-    const float2 *words = (const float2 *)((const char *)a.workspace + ws.best) + (int64_t)row * ws.tiles * out.top_k;
-    float top = -INFINITY;
-    for (int i = lane; i < ws.tiles; i += 32) top = fmaxf(top, p[i].top);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float base = isinf(top) ? 0.f : top;
-    float sum = 0.f, u = 0.f;
-    BestWords<K ? K : 1> best;
-    for (int i = lane; i < ws.tiles; i += 32) {
-        const RowStat v = p[i];
-        const float d = v.top - base, f = expf(d);
-        sum = fmaf(v.sum, f, sum);
-        u = fmaf(f, fmaf(v.top == -INFINITY ? 0.f : d, v.sum, v.u), u);
-        for (int c = 0; c < (K ? v.count : 0); ++c) {
-            const float2 w = words[(int64_t)i * out.top_k + c];
-            if (!(w.x > best.v[K ? K - 1 : 0])) break;   // nor do the worse ones of the tile
-            best.add(w.x, __float_as_int(w.y));
-        }
-    }
-    sum = warp_sum(sum);
-    u = warp_sum(u);
-    const bool keep = kept(a, row);
-    const float ls = logf(sum), lse = base + ls;
-    if (lane == 0) {
-        out.logp[row] = keep ? (((const float *)((const char *)a.workspace + ws.at))[row] - base) - ls : 0.f;
-        out.entropy[row] = keep ? ls - u / sum : 0.f;
-        if (out.lse) out.lse[row] = keep ? lse : 0.f;
-    }
-    if (K) write_best(best, out.top_k, lse, keep, out.top_ids + (int64_t)row * out.top_k, out.top_logps + (int64_t)row * out.top_k);
-}
-
 // dh (+)= G W over one piece; the last piece writes the gradient.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) ce_dh_kernel(LinearCeArgs a, CeWorkspace ws, int v0, int cols, int row0)
@@ -357,10 +318,13 @@ cudaError_t fwd(const LinearCeArgs &a, cudaStream_t st, const LogProbs *out)
         over_tiles(a.N, a.V, [&](dim3 grid, int row0) {
             ce_logits_kernel<T, kStats><<<grid, kThreads, 0, st>>>(a, ws, 0, a.V, row0, LogProbsGrad(), out->top_k);
         });
+        const char *w = (const char *)a.workspace;
+        const LogProbParts p = {(const RowStat *)(w + ws.part), (const float2 *)(w + ws.best), (const float *)(w + ws.at),
+                                a.targets, 1, ws.tiles, a.N, a.V, ws.tiles, out->top_k};
         const int blocks = ceil_div(a.N, 8);
-        if (out->top_k == 0) logp_join_kernel<0><<<blocks, 256, 0, st>>>(a, ws, *out);
-        else if (out->top_k <= 8) logp_join_kernel<8><<<blocks, 256, 0, st>>>(a, ws, *out);
-        else logp_join_kernel<kMostTop><<<blocks, 256, 0, st>>>(a, ws, *out);
+        if (out->top_k == 0) logp_join_kernel<0><<<blocks, 256, 0, st>>>(p, *out);
+        else if (out->top_k <= 8) logp_join_kernel<8><<<blocks, 256, 0, st>>>(p, *out);
+        else logp_join_kernel<kMostTop><<<blocks, 256, 0, st>>>(p, *out);
         return cudaGetLastError();
     }
     const CeWorkspace ws = layout(a.N, a.D, a.V, false);

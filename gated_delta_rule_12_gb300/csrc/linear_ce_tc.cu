@@ -334,16 +334,21 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
             float top = -INFINITY, sum = 0.f, u = 0.f;
             BestWords<K ? K : 1> best;
             float cut = -INFINITY;                     // words at or below it are not among the row's best
-            if (K && in && p.cut) {
-                const unsigned c = *(volatile const unsigned *)(p.cut + row);
-                if (c) cut = below(c);   // words equal to it may be; 0: no such logit yet
-            }
+            auto told = [&] {                          // what other tiles have found: words equal to it may be
+                const unsigned c = in && p.cut ? *(volatile const unsigned *)(p.cut + row) : 0u;
+                if (c) cut = fmaxf(cut, below(c));
+            };
+            if (K) told();
+            unsigned hot = 0u;                         // chunks with words above it
+            float most[K ? 32 : 1];                    // the largest of every 32nd word
+#pragma unroll
+            for (int j = 0; j < (K ? 32 : 1); ++j) most[j] = -INFINITY;
 #pragma unroll 1
             for (int ch = 0; ch < chunks; ++ch) {
                 uint32_t r[32];
                 tmem_ld32(src + ch * 32, r);
                 tmem_wait_ld();
-                if (ch == chunks - 1) {   // the accumulator is in registers: the next tile but one may have it
+                if (!K && ch == chunks - 1) {   // the accumulator is in registers: the next tile but one may have it
                     fence_before_sync();
                     __syncwarp();
                     if (lane == 0) arrive_remote(leader_empty + 8 * buf);
@@ -382,28 +387,10 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                     }
                     sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
                     if (MODE == kStats) u += (u4[0] + u4[1]) + (u4[2] + u4[3]);
-                    if (K && __any_sync(0xffffffffu, in && here > cut)) {
-                        // Words that may be among the best come out one at a time, each lane its own: found by their bits,
-                        // then read back from the warp's buffer, as registers have no variable index.
-                        const uint32_t row_s = buf0 + lane * 128;
-                        unsigned some = 0u;
+                    if (K) {
+                        hot |= (here > cut ? 1u : 0u) << ch;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            st_shared16(row_s + ((j ^ (lane & 7)) << 4), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) some |= (__uint_as_float(r[j]) > cut ? 1u : 0u) << j;
-                        if (!in) some = 0u;
-                        while (__any_sync(0xffffffffu, some != 0u)) {
-                            if (some) {
-                                const int j = __ffs((int)some) - 1;
-                                some &= some - 1u;
-                                float x;
-                                asm volatile("ld.shared.f32 %0, [%1];"
-                                             : "=f"(x) : "r"(row_s + (((j >> 2) ^ (lane & 7)) << 4) + (j & 3) * 4) : "memory");
-                                best.add(x, c0 + j);
-                            }
-                        }
-                        cut = fmaxf(cut, best.value(p.top - 1));
+                        for (int j = 0; j < 32; ++j) most[K ? j : 0] = fmaxf(most[K ? j : 0], __uint_as_float(r[j]));
                     }
                 } else {
                     // 128-byte rows of the warp's buffer: 64 bf16, two chunks of 32 columns, or 32 fp32
@@ -470,6 +457,56 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
             }
             if (MODE == kLogits && in)
                 p.part[(int64_t)c.n * p.N + row] = make_float2(top == -INFINITY ? top : (isinf(top) ? 0.f : top), sum);
+            if constexpr (K > 0) {
+                // The words that may be among the row's best.  p.top of the 32 maxima are as many words, so what is below the
+                // least of those is not; this and what other tiles tell leaves some 1.2 p.top words of a row's first tile.
+                if (__any_sync(0xffffffffu, in && hot)) {
+                    if (__any_sync(0xffffffffu, in && cut == -INFINITY)) {
+                        sort32(most);
+                        float least = most[0];
+#pragma unroll
+                        for (int j = 1; j < K; ++j) least = j < p.top ? most[j] : least;
+                        if (in && least > -INFINITY) {
+                            if (p.cut) atomicMax(p.cut + row, order_of(least));
+                            cut = fmaxf(cut, below(order_of(least)));
+                        }
+                        told();
+                    }
+#pragma unroll 1
+                    for (int ch = 0; ch < chunks; ++ch) {
+                        if (!__any_sync(0xffffffffu, in && (hot >> ch & 1u))) continue;
+                        uint32_t r[32];
+                        tmem_ld32(src + ch * 32, r);
+                        tmem_wait_ld();
+                        const int c0 = col0 + ch * 32;
+                        unsigned some = 0u;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) some |= (__uint_as_float(r[j]) > cut && c0 + j < p.V ? 1u : 0u) << j;
+                        if (!in) some = 0u;
+                        if (!__any_sync(0xffffffffu, some != 0u)) continue;
+                        // They come out one at a time, each lane its own: found by their bits, then read back from the warp's
+                        // buffer, as registers have no variable index.
+                        const uint32_t row_s = buf0 + lane * 128;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            st_shared16(row_s + ((j ^ (lane & 7)) << 4), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                        while (__any_sync(0xffffffffu, some != 0u)) {
+                            if (some) {
+                                const int j = __ffs((int)some) - 1;
+                                some &= some - 1u;
+                                float x;
+                                asm volatile("ld.shared.f32 %0, [%1];"
+                                             : "=f"(x) : "r"(row_s + (((j >> 2) ^ (lane & 7)) << 4) + (j & 3) * 4) : "memory");
+                                best.add(x, c0 + j);
+                            }
+                        }
+                        cut = fmaxf(cut, best.value(p.top - 1));
+                    }
+                }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) arrive_remote(leader_empty + 8 * buf);
+            }
             if (MODE == kStats && in) {
                 const int64_t at = (int64_t)c.n * p.N + row;
                 const int count = K ? best.count(p.top) : 0;
@@ -529,70 +566,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_tc_join_kernel(const CePar
         const float lse = base + logf(sum);
         loss[row] = keep ? lse - p.at[row] : 0.f;
         if (lse_out) lse_out[row] = keep ? lse : 0.f;
-    }
-}
-
-// The same for kStats, with the entropy; K: the row's best words, a warp a row.
-template <int K>
-__global__ void __launch_bounds__(32 * kJoinWarps) logp_tc_join_kernel(const CeParams p, int words, LogProbs out)
-{
-    __shared__ float tops[kJoinWarps][32], sums[kJoinWarps][32], us[kJoinWarps][32], lses[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.x * 32 + lane;
-    wait_previous();
-    const RowStat *stat = p.stat + (row < p.N ? row : 0);
-    float top = -INFINITY, sum = 0.f, u = 0.f;
-#pragma unroll 8
-    for (int i = warp; i < words; i += kJoinWarps) top = fmaxf(top, stat[(int64_t)i * p.N].top);
-    tops[warp][lane] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, tops[i][lane]);
-    const float base = isinf(top) ? 0.f : top;   // keeps infinities and NaN in the sum
-#pragma unroll 8
-    for (int i = warp; i < words; i += kJoinWarps) {
-        const float4 v = *reinterpret_cast<const float4 *>(stat + (int64_t)i * p.N);
-        const float d = v.x - base, f = expf(d);
-        sum = fmaf(v.y, f, sum);
-        u = fmaf(f, fmaf(v.x == -INFINITY ? 0.f : d, v.y, v.z), u);
-    }
-    sums[warp][lane] = sum;
-    us[warp][lane] = u;
-    __syncthreads();
-    if (warp == 0) {
-        sum = u = 0.f;
-#pragma unroll
-        for (int i = 0; i < kJoinWarps; ++i) {
-            sum += sums[i][lane];
-            u += us[i][lane];
-        }
-        const float ls = logf(sum);
-        lses[lane] = base + ls;
-        if (row < p.N) {
-            const int t = p.targets[row];
-            const bool keep = t >= 0 && t < p.V;
-            out.logp[row] = keep ? (p.at[row] - base) - ls : 0.f;
-            out.entropy[row] = keep ? ls - u / sum : 0.f;
-            if (out.lse) out.lse[row] = keep ? base + ls : 0.f;
-        }
-    }
-    if (K == 0) return;
-    __syncthreads();
-    for (int i = warp; i < 32; i += kJoinWarps) {
-        const int r = blockIdx.x * 32 + i;
-        if (r >= p.N) break;
-        BestWords<K ? K : 1> best;
-        for (int n = lane; n < words; n += 32) {
-            const int64_t at = (int64_t)n * p.N + r;
-            const int count = p.stat[at].count;
-            for (int c = 0; c < count; ++c) {
-                const float2 v = p.best[at * p.top + c];
-                if (!(v.x > best.v[K ? K - 1 : 0])) break;   // nor do the worse ones of the tile
-                best.add(v.x, __float_as_int(v.y));
-            }
-        }
-        const int t = p.targets[r];
-        write_best(best, p.top, lses[i], t >= 0 && t < p.V, out.top_ids + (int64_t)r * p.top, out.top_logps + (int64_t)r * p.top);
     }
 }
 
@@ -763,7 +736,8 @@ static cudaError_t run_stats(const CeMaps &maps, const CeParams &p, const LogPro
 {
     const cudaError_t e = launch<kStats, K>(maps, p, st, CeStall());
     if (e != cudaSuccess) return e;
-    return launch_early(logp_tc_join_kernel<K>, ceil_div(p.N, 32), 32 * kJoinWarps, 0, st, p, p.p[0].nt, out);
+    const LogProbParts parts = {p.stat, p.best, p.at, p.targets, p.N, 1, p.N, p.V, p.p[0].nt, p.top};
+    return launch_early(logp_join_kernel<K>, ceil_div(p.N, 8), 256, 0, st, parts, out);
 }
 
 cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, const LogProbs *out, CeStall stall)
@@ -788,7 +762,7 @@ cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, cons
         p.best = (float2 *)(w + ws.best);
         p.top = out->top_k;
         // Tiles tell later ones of their rows what need not be kept, where there are rounds of them to tell.
-        if (p.top > 0 && p.tiles > 4 * kPairs) {
+        if (p.top > 0 && p.tiles > kPairs) {
             p.cut = (unsigned *)(w + ws.cut);
             const cudaError_t e = cudaMemsetAsync(p.cut, 0, (size_t)a.N * 4, st);
             if (e != cudaSuccess) return e;

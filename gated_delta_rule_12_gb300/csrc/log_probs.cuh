@@ -10,6 +10,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kernels.h"
+
 namespace gdn {
 
 constexpr int kMostTop = 20;
@@ -84,6 +86,22 @@ __device__ __forceinline__ float below(unsigned place)
     return __uint_as_float(p & 0x80000000u ? p & 0x7fffffffu : ~p);
 }
 
+// Sorts 32 values, largest first: a bitonic network, 240 exchanges.  (By recursion, as loops whose steps double are not
+// unrolled and would leave the values in memory.)
+template <int RUN = 2, int APART = 1>
+__device__ __forceinline__ void sort32(float (&v)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (!(i & APART)) {
+            const float a = v[i], b = v[i + APART], high = fmaxf(a, b), low = fminf(a, b);
+            v[i] = i & RUN ? low : high;
+            v[i + APART] = i & RUN ? high : low;
+        }
+    if constexpr (APART > 1) sort32<RUN, APART / 2>(v);
+    else if constexpr (RUN < 32) sort32<RUN * 2, RUN>(v);
+}
+
 // A warp's lists to the row's k best words.
 template <int K>
 __device__ __forceinline__ void write_best(BestWords<K> &best, int k, float lse, bool keep, int *ids, float *logps)
@@ -93,8 +111,7 @@ __device__ __forceinline__ void write_best(BestWords<K> &best, int k, float lse,
         const unsigned mine = best.id[0] >= 0 ? order_of(best.v[0]) : 0u;
         const unsigned high = __reduce_max_sync(0xffffffffu, mine);
         const unsigned word = __reduce_min_sync(0xffffffffu, high && mine == high ? (unsigned)best.id[0] : 0xffffffffu);
-        const bool won = high && mine == high && (unsigned)best.id[0] == word;
-        if (won) {
+        if (high && mine == high && (unsigned)best.id[0] == word) {
             ids[i] = keep ? best.id[0] : -1;
             logps[i] = keep ? best.v[0] - lse : 0.f;
             best.pop();
@@ -104,6 +121,67 @@ __device__ __forceinline__ void write_best(BestWords<K> &best, int k, float lse,
             logps[i] = keep ? -INFINITY : 0.f;
         }
     }
+}
+
+// The parts of the rows, part n of row r at n * part_step + r * row_step, and its best words, `top` of them, likewise.
+struct LogProbParts {
+    const RowStat *stat;
+    const float2 *best;       // a logit and its word's bits, best first
+    const float *at;          // [N] the targets' logits
+    const int32_t *targets;
+    int64_t part_step, row_step;
+    int N, V, parts, top;
+};
+
+// Joins a row's parts, a warp a row, in a fixed order; K: the best words that a lane keeps, at least p.top.
+template <int K>
+static __global__ void __launch_bounds__(256) logp_join_kernel(LogProbParts p, LogProbs out)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched beside the kernel that writes the parts
+    if (row >= p.N) return;
+    const RowStat *stat = p.stat + row * p.row_step;
+    float top = -INFINITY;
+#pragma unroll 4
+    for (int i = lane; i < p.parts; i += 32) top = fmaxf(top, stat[i * p.part_step].top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = isinf(top) ? 0.f : top;   // keeps infinities and NaN in the sum
+    float sum = 0.f, u = 0.f;
+    BestWords<K ? K : 1> best;
+    for (int i = lane; i < p.parts; i += 32) {
+        const float4 v = *reinterpret_cast<const float4 *>(stat + i * p.part_step);
+        const float d = v.x - base, f = expf(d);
+        sum = fmaf(v.y, f, sum);
+        u = fmaf(f, fmaf(v.x == -INFINITY ? 0.f : d, v.y, v.z), u);
+        if (K) {
+            const int count = __float_as_int(v.w);
+            const float2 *words = p.best + (i * p.part_step + row * p.row_step) * p.top;
+            for (int c = 0; c < count; c += 4) {   // a few at a time, on their way together
+                float2 w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = c + j < count ? words[c + j] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (w[j].x > best.v[K ? K - 1 : 0]) best.add(w[j].x, __float_as_int(w[j].y));
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        u += __shfl_xor_sync(0xffffffffu, u, o);
+    }
+    const int t = p.targets[row];
+    const bool keep = t >= 0 && t < p.V;
+    const float ls = logf(sum), lse = base + ls;
+    if (lane == 0) {
+        out.logp[row] = keep ? (p.at[row] - base) - ls : 0.f;
+        out.entropy[row] = keep ? ls - u / sum : 0.f;
+        if (out.lse) out.lse[row] = keep ? lse : 0.f;
+    }
+    if (K) write_best(best, p.top, lse, keep, out.top_ids + row * p.top, out.top_logps + row * p.top);
 }
 
 }  // namespace gdn
