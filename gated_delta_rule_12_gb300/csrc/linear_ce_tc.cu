@@ -95,8 +95,9 @@ struct CeParams {
     RowWeights weight;
     const float *scale;       // kGrads: s
     float2 *part;             // kLogits: [tiles of 256 words][N]
-    RowStat *stat;            // kStats: the same
-    float2 *best;             // kStats: [tiles of 256 words][N][top], a logit and its word's bits
+    RowStat *stat;            // kStats: [parts][N]
+    float2 *best;             // kStats: [parts][N][top], a logit and its word's bits
+    PartOrder order;          // kStats
     unsigned *cut;            // kStats: [N], order_of() of a logit that the row's best words do not fall below; or null
     int top;
     float *at;                // kLogits, kStats: [N]
@@ -120,13 +121,16 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 // Which product, tile and K range a tile index stands for.
 struct Tile {
     int which, m, n, s, k0, k1;
+    int part;                 // kStats
 };
 
 template <int MODE>
 __device__ __forceinline__ Tile tile_of(const CeParams &p, int t)
 {
-    Tile r;
-    if (MODE == kGrads) {
+    Tile r = {};
+    if (MODE == kStats) {
+        if (p.order.at(t % p.order.pairs, t / p.order.pairs, r.m, r.n, r.part)) r.k1 = p.p[0].kb;   // else nothing to do
+    } else if (MODE == kGrads) {
         r.which = t >= p.tiles0;
         const Product &q = p.p[r.which];
         int i = r.which ? t - p.tiles0 : t;
@@ -168,7 +172,7 @@ __device__ __noinline__ void spoil(const CeParams &p, int pair, int pairs, int r
             if (MODE == kLogits) {
                 p.part[(int64_t)c.n * p.N + row] = make_float2(nan, nan);
             } else if (MODE == kStats) {
-                p.stat[(int64_t)c.n * p.N + row] = {nan, nan, nan, 0};
+                p.stat[(int64_t)c.part * p.N + row] = {nan, nan, nan, 0};
             } else if (MODE == kProb || MODE == kProbEnt) {
                 static_cast<unsigned short *>(p.out[0])[row * p.pitch + col] = 0x7fff;
             } else if (c.which == 0 || p.direct) {
@@ -303,6 +307,11 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
         const uint32_t buf0 = stores + (warp - 2) * kStore;
         const uint32_t leader_empty = map_to_rank(acc_empty, 0);
         uint32_t tiles = 0;
+        float top = -INFINITY, sum = 0.f, u = 0.f;
+        // kStats: what the pair has seen of these rows so far
+        BestWords<K ? K : 1> best;
+        float cut = -INFINITY;                         // words at or below it are not among the row's best
+        bool begins = true;
         for (int t = pair; t < p.tiles; t += pairs) {
             const Tile c = tile_of<MODE>(p, t);
             if (c.k0 >= c.k1) continue;
@@ -331,16 +340,26 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
             if (!__all_sync(0xffffffffu, wait_bar(acc_full + 8 * buf, use & 1, abort_flag, p))) break;
             fence_after_sync();
             const uint32_t src = tmem + buf * 256 + (quarter << 21);   // lane field: bits 16 and up
-            float top = -INFINITY, sum = 0.f, u = 0.f;
-            BestWords<K ? K : 1> best;
-            float cut = -INFINITY;                     // words at or below it are not among the row's best
+            if (begins) {
+                top = -INFINITY;
+                sum = u = 0.f;
+                cut = -INFINITY;
+                best = BestWords<K ? K : 1>();
+            }
+            bool ends = true;
+            if (MODE == kStats && t + pairs < p.tiles) {
+                const Tile next = tile_of<MODE>(p, t + pairs);
+                ends = next.k0 >= next.k1 || next.m != c.m || next.part != c.part;
+            }
+            begins = ends;
             auto told = [&] {                          // what other tiles have found: words equal to it may be
                 const unsigned c = in && p.cut ? *(volatile const unsigned *)(p.cut + row) : 0u;
                 if (c) cut = fmaxf(cut, below(c));
             };
             if (K) told();
+            const bool fresh = K && __any_sync(0xffffffffu, in && cut == -INFINITY);
             unsigned hot = 0u;                         // chunks with words above it
-            float most[K ? 32 : 1];                    // the largest of every 32nd word
+            float most[K ? 32 : 1];                    // fresh: the largest of every 32nd word
 #pragma unroll
             for (int j = 0; j < (K ? 32 : 1); ++j) most[j] = -INFINITY;
 #pragma unroll 1
@@ -389,8 +408,9 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                     if (MODE == kStats) u += (u4[0] + u4[1]) + (u4[2] + u4[3]);
                     if (K) {
                         hot |= (here > cut ? 1u : 0u) << ch;
+                        if (fresh)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) most[K ? j : 0] = fmaxf(most[K ? j : 0], __uint_as_float(r[j]));
+                            for (int j = 0; j < 32; ++j) most[K ? j : 0] = fmaxf(most[K ? j : 0], __uint_as_float(r[j]));
                     }
                 } else {
                     // 128-byte rows of the warp's buffer: 64 bf16, two chunks of 32 columns, or 32 fp32
@@ -461,7 +481,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 // The words that may be among the row's best.  p.top of the 32 maxima are as many words, so what is below the
                 // least of those is not; this and what other tiles tell leaves some 1.2 p.top words of a row's first tile.
                 if (__any_sync(0xffffffffu, in && hot)) {
-                    if (__any_sync(0xffffffffu, in && cut == -INFINITY)) {
+                    if (fresh) {
                         sort32(most);
                         float least = most[0];
 #pragma unroll
@@ -507,8 +527,8 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 __syncwarp();
                 if (lane == 0) arrive_remote(leader_empty + 8 * buf);
             }
-            if (MODE == kStats && in) {
-                const int64_t at = (int64_t)c.n * p.N + row;
+            if (MODE == kStats && in && ends) {
+                const int64_t at = (int64_t)c.part * p.N + row;
                 const int count = K ? best.count(p.top) : 0;
                 p.stat[at] = {top == -INFINITY ? top : (isinf(top) ? 0.f : top), sum, u, count};
                 if (K) {
@@ -657,6 +677,12 @@ bool make_map(CUtensorMap *m, const void *base, int cols, int rows, int64_t pitc
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+PartOrder part_order(int N, int V)
+{
+    const int mt = ceil_div(N > 0 ? N : 1, kTile), nt = ceil_div(V, kTile);
+    return PartOrder::make(mt, nt, (int64_t)mt * nt < kPairs ? mt * nt : kPairs);
+}
+
 struct TcWorkspace {
     size_t part, at;          // forward
     size_t best, cut;         // log probabilities, forward: [tiles of words][N][top], [N]
@@ -673,7 +699,7 @@ TcWorkspace tc_layout(int N, int D, int V, bool backward, int top = -1)
     TcWorkspace w = {};
     size_t off = 256;
     if (!backward) {
-        const size_t parts = (size_t)N * ceil_div(V, kTile);
+        const size_t parts = (size_t)N * (top < 0 ? ceil_div(V, kTile) : part_order(N, V).parts);
         w.part = off; off = align256(off + parts * (top < 0 ? sizeof(float2) : sizeof(RowStat)));
         w.at = off;   off = align256(off + (size_t)N * 4);
         w.best = off; off = align256(off + (top > 0 ? parts * top * sizeof(float2) : 0));
@@ -736,7 +762,7 @@ static cudaError_t run_stats(const CeMaps &maps, const CeParams &p, const LogPro
 {
     const cudaError_t e = launch<kStats, K>(maps, p, st, CeStall());
     if (e != cudaSuccess) return e;
-    const LogProbParts parts = {p.stat, p.best, p.at, p.targets, p.N, 1, p.N, p.V, p.p[0].nt, p.top};
+    const LogProbParts parts = {p.stat, p.best, p.at, p.targets, p.cut, p.N, 1, p.N, p.V, p.order.parts, p.top, p.order};
     return launch_early(logp_join_kernel<K>, ceil_div(p.N, 8), 256, 0, st, parts, out);
 }
 
@@ -761,6 +787,8 @@ cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, cons
         p.stat = (RowStat *)(w + ws.part);
         p.best = (float2 *)(w + ws.best);
         p.top = out->top_k;
+        p.order = part_order(a.N, a.V);
+        p.tiles0 = p.tiles = p.order.pairs * p.order.rounds();
         // Tiles tell later ones of their rows what need not be kept, where there are rounds of them to tell.
         if (p.top > 0 && p.tiles > kPairs) {
             p.cut = (unsigned *)(w + ws.cut);

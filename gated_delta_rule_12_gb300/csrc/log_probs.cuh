@@ -123,14 +123,90 @@ __device__ __forceinline__ void write_best(BestWords<K> &best, int k, float lse,
     }
 }
 
+// Which part a tile of words belongs to where the tensor cores make them.  The row tiles are taken in groups of up to 32 (rows
+// whose h stays in L2; more where words are few), a group's words in windows; a window's tiles, row tile by row tile, are cut into runs of `each` for the
+// pairs of CTAs.  So a pair meets the same rows for several tiles, and their statistics and best words stay in its registers:
+// one part a run, or two where the run passes from one row tile to the next.
+struct PartOrder {
+    struct Group {
+        int rows, window, each, windows, last_window, last_each, rounds;   // rounds: tiles of a pair over the whole group
+    } full, last;
+    int pairs, size, groups;  // a group's row tiles; groups in front of the last one
+    int slots;                // parts a row may have in a window
+    int parts;                // and in all
+
+    static Group group(int rows, int nt, int pairs)
+    {
+        Group g = {};
+        g.rows = rows;
+        const int64_t tiles = (int64_t)rows * nt;
+        g.window = tiles <= 8 * (int64_t)pairs ? nt : 8 * pairs / rows > 0 ? 8 * pairs / rows : 1;
+        g.windows = (nt + g.window - 1) / g.window;
+        g.last_window = nt - (g.windows - 1) * g.window;
+        g.each = (rows * g.window + pairs - 1) / pairs;
+        g.last_each = (rows * g.last_window + pairs - 1) / pairs;
+        g.rounds = (g.windows - 1) * g.each + g.last_each;
+        return g;
+    }
+    static int slots_of(const Group &g)
+    {
+        const int a = (g.window + g.each - 1) / g.each, b = (g.last_window + g.last_each - 1) / g.last_each;
+        return (g.windows > 1 && a > b ? a : b) + 1;
+    }
+    static PartOrder make(int mt, int nt, int pairs)
+    {
+        PartOrder o = {};
+        o.pairs = pairs;
+        o.size = nt >= 19 ? 32 : (8 * pairs + nt - 1) / nt;
+        if (o.size < 32) o.size = 32;
+        o.groups = (mt - 1) / o.size;
+        o.full = group(o.size, nt, pairs);
+        o.last = group(mt - o.size * o.groups, nt, pairs);
+        o.slots = slots_of(o.last);
+        int windows = o.last.windows;
+        if (o.groups) {
+            if (slots_of(o.full) > o.slots) o.slots = slots_of(o.full);
+            if (o.full.windows > windows) windows = o.full.windows;
+        }
+        o.parts = windows * o.slots;
+        return o;
+    }
+    int rounds() const { return groups * full.rounds + last.rounds; }
+
+    // Tile `round` of a pair: its row tile, word tile and part; false where it has none.
+    __device__ __forceinline__ bool at(int pair, int round, int &m, int &n, int &part) const
+    {
+        const int g = min(round / full.rounds, groups);
+        const Group &q = g < groups ? full : last;
+        const int j = round - g * full.rounds, x = min(j / q.each, q.windows - 1);
+        const int wide = x == q.windows - 1 ? q.last_window : q.window, each = x == q.windows - 1 ? q.last_each : q.each;
+        const int i = pair * each + (j - x * q.each), row = i / wide;
+        m = size * g + row;
+        n = x * q.window + i % wide;
+        part = x * slots + pair - row * wide / each;
+        return i < q.rows * wide;
+    }
+    // Whether a row tile has this part.
+    __device__ __forceinline__ bool has(int m, int part) const
+    {
+        const int g = min(m / size, groups), row = m - size * g, x = part / slots;
+        const Group &q = g < groups ? full : last;
+        if (x >= q.windows) return false;
+        const int wide = x == q.windows - 1 ? q.last_window : q.window, each = x == q.windows - 1 ? q.last_each : q.each;
+        return (row * wide / each + part % slots) * each < (row + 1) * wide;
+    }
+};
+
 // The parts of the rows, part n of row r at n * part_step + r * row_step, and its best words, `top` of them, likewise.
 struct LogProbParts {
     const RowStat *stat;
     const float2 *best;       // a logit and its word's bits, best first
     const float *at;          // [N] the targets' logits
     const int32_t *targets;
+    const unsigned *cut;      // [N] order_of() of a logit that the row's best words do not fall below (0: none); or null
     int64_t part_step, row_step;
     int N, V, parts, top;
+    PartOrder order;          // pairs = 0: every row has all parts
 };
 
 // Joins a row's parts, a warp a row, in a fixed order; K: the best words that a lane keeps, at least p.top.
@@ -142,37 +218,51 @@ static __global__ void __launch_bounds__(256) logp_join_kernel(LogProbParts p, L
     asm volatile("griddepcontrol.wait;" ::: "memory");   // launched beside the kernel that writes the parts
     if (row >= p.N) return;
     const RowStat *stat = p.stat + row * p.row_step;
-    float top = -INFINITY;
-#pragma unroll 4
-    for (int i = lane; i < p.parts; i += 32) top = fmaxf(top, stat[i * p.part_step].top);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float base = isinf(top) ? 0.f : top;   // keeps infinities and NaN in the sum
-    float sum = 0.f, u = 0.f;
+    const int row_tile = (int)(row / 256);
+    const unsigned told = K && p.cut ? p.cut[row] : 0u;
+    const float cut = told ? below(told) : -INFINITY;   // the row's best words are above it
+    float top = -INFINITY, sum = 0.f, u = 0.f;
+    // Moves (sum, u) from `top` to a higher reference and adds another's.  A part without words has -inf and zeros (or NaN).
+    auto join = [&](float t, float s, float v) {
+        const float to = fmaxf(top, t), base = to == -INFINITY ? 0.f : to;
+        const float da = fmaxf(top - base, -1e4f), db = fmaxf(t - base, -1e4f), fa = expf(da), fb = expf(db);
+        u = fa * fmaf(da, sum, u) + fb * fmaf(db, s, v);
+        sum = fmaf(fa, sum, fb * s);
+        top = to;
+    };
     BestWords<K ? K : 1> best;
-    for (int i = lane; i < p.parts; i += 32) {
-        const float4 v = *reinterpret_cast<const float4 *>(stat + i * p.part_step);
-        const float d = v.x - base, f = expf(d);
-        sum = fmaf(v.y, f, sum);
-        u = fmaf(f, fmaf(v.x == -INFINITY ? 0.f : d, v.y, v.z), u);
-        if (K) {
-            const int count = __float_as_int(v.w);
-            const float2 *words = p.best + (i * p.part_step + row * p.row_step) * p.top;
-            for (int c = 0; c < count; c += 4) {   // a few at a time, on their way together
-                float2 w[4];
+    for (int first = lane; first < p.parts; first += 128) {   // four parts at a time, on their way together
+        float4 v[4];
+        bool in[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = c + j < count ? words[c + j] : make_float2(-INFINITY, 0.f);
+        for (int j = 0; j < 4; ++j) {
+            const int i = first + 32 * j;
+            in[j] = i < p.parts && (p.order.pairs == 0 || p.order.has(row_tile, i));
+            v[j] = in[j] ? *reinterpret_cast<const float4 *>(stat + i * p.part_step) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (w[j].x > best.v[K ? K - 1 : 0]) best.add(w[j].x, __float_as_int(w[j].y));
+        for (int j = 0; j < 4; ++j) {
+            if (!in[j]) continue;
+            join(v[j].x, v[j].y, v[j].z);
+            if (K && !(v[j].x < cut)) {   // (0 in place of an infinite maximum: the words tell)
+                const int count = __float_as_int(v[j].w);
+                const float2 *words = p.best + ((first + 32 * j) * p.part_step + row * p.row_step) * p.top;
+                for (int c = 0; c < count; c += 4) {
+                    float2 w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = c + e < count ? words[c + e] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (w[e].x > cut && w[e].x > best.v[K ? K - 1 : 0]) best.add(w[e].x, __float_as_int(w[e].y));
+                    if (!(w[3].x > cut)) break;   // nor are the worse ones
+                }
             }
         }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        u += __shfl_xor_sync(0xffffffffu, u, o);
-    }
+    for (int o = 16; o > 0; o >>= 1)
+        join(__shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, sum, o), __shfl_xor_sync(0xffffffffu, u, o));
+    const float base = top == -INFINITY ? 0.f : top;
     const int t = p.targets[row];
     const bool keep = t >= 0 && t < p.V;
     const float ls = logf(sum), lse = base + ls;

@@ -18,13 +18,15 @@ from gated_delta_rule_12_gb300 import inputs
 def main(argv=None) -> None:
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--op", choices=["fwd", "bwd", "decode", "decode_multi", "scan_fwd", "scan_bwd", "norm_fwd",
-                                     "norm_bwd", "ce_fwd", "ce_bwd"], required=True)
+                                     "norm_bwd", "rms_fwd", "rms_bwd", "rms_fp8", "quantize", "fp8_linear", "ce_fwd",
+                                     "ce_bwd", "logp_fwd", "logp_bwd"], required=True)
     ap.add_argument("--B", type=int, default=1, help="sequences (decode: N)")
     ap.add_argument("--L", type=int, default=2048, help="tokens per sequence (decode_multi: tokens per call)")
     ap.add_argument("--H", type=int, default=16)
     ap.add_argument("--dk", type=int, default=128)
     ap.add_argument("--dv", type=int, default=128)
-    ap.add_argument("--vocab", type=int, default=32768, help="words (ce_*)")
+    ap.add_argument("--vocab", type=int, default=32768, help="words (ce_*, logp_*; fp8_linear: columns)")
+    ap.add_argument("--top", type=int, default=5, help="alternatives (logp_fwd)")
     ap.add_argument("--dtype", choices=["bf16", "f32"], default="bf16")
     ap.add_argument("--calls", type=int, default=3)
     a = ap.parse_args(argv)
@@ -34,7 +36,7 @@ def main(argv=None) -> None:
     gdn.load_library()
     elem = torch.bfloat16 if a.dtype == "bf16" else torch.float32
 
-    if a.op.startswith(("scan", "norm", "ce")):
+    if a.op.startswith(("scan", "norm", "rms", "quantize", "fp8", "ce", "logp")):
         # B sequences of L tokens, H * dk channels
         gen = torch.Generator(device=dev).manual_seed(1)
         x, y = (torch.randn((a.B, a.L, a.H * a.dk), generator=gen, device=dev).to(elem) for _ in range(2))
@@ -48,13 +50,31 @@ def main(argv=None) -> None:
             _, mean, rstd = gdn.layer_norm_fwd(x, w, w)
             for _ in range(a.calls):
                 gdn.layer_norm_fwd(x, w, w) if a.op == "norm_fwd" else gdn.layer_norm_bwd(y, x, mean, rstd, w)
+        elif a.op.startswith("rms"):
+            w = torch.randn(a.H * a.dk, generator=gen, device=dev)
+            _, s, rstd = gdn.rms_norm_fwd(x, w, residual=y)
+            call = {"rms_fwd": lambda: gdn.rms_norm_fwd(x, w, residual=y), "rms_fp8": lambda: gdn.rms_norm_fp8(x, w, residual=y),
+                    "rms_bwd": lambda: gdn.rms_norm_bwd(y, s, rstd, w, dresidual=x)}[a.op]
+            for _ in range(a.calls):
+                call()
+        elif a.op in ("quantize", "fp8_linear"):
+            q, c = gdn.fp8_quantize(x)
+            w = torch.randn((a.vocab, a.H * a.dk), generator=gen, device=dev)
+            wq, wc = gdn.fp8_quantize(w, block_rows=128)
+            for _ in range(a.calls):
+                gdn.fp8_quantize(x) if a.op == "quantize" else gdn.fp8_linear(q, c, wq, wc)
         else:
             h = x.view(-1, a.H * a.dk)
             w = (torch.randn((a.vocab, h.shape[1]), generator=gen, device=dev) * h.shape[1] ** -0.5).to(elem)
             t = torch.randint(0, a.vocab, (h.shape[0],), generator=gen, device=dev, dtype=torch.int32)
             loss, lse = gdn.linear_cross_entropy_fwd(h, w, t)
+            entropy = gdn.linear_log_probs_fwd(h, w, t)[1] if a.op == "logp_bwd" else None
             for _ in range(a.calls):
-                if a.op == "ce_fwd":
+                if a.op == "logp_fwd":
+                    gdn.linear_log_probs_fwd(h, w, t, top_k=a.top)
+                elif a.op == "logp_bwd":
+                    gdn.linear_log_probs_bwd(h, w, t, lse, entropy, torch.ones_like(loss), torch.ones_like(loss))
+                elif a.op == "ce_fwd":
                     gdn.linear_cross_entropy_fwd(h, w, t)
                 else:
                     gdn.linear_cross_entropy_bwd(h, w, t, lse, torch.ones_like(loss))
