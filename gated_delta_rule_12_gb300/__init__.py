@@ -148,6 +148,8 @@ def load_library(path: str = LIB_PATH, build_if_missing: bool = False) -> ctypes
         lib.gdn_fp8_linear_workspace_size.argtypes = [_i32] * 3
         lib.gdn_fp8_linear_workspace_size.restype = _sz
         lib.gdn_fp8_linear.argtypes = [_vp] * 5 + [_i32] * 3 + [_vp, _sz, _vp]
+        lib.gdn_selftest_fp8_linear_timeout.argtypes = [ctypes.c_uint32] + [_vp] * 5 + [_i32] * 3 + [_vp, _sz, _vp]
+        lib.gdn_selftest_fp8_linear_timeout.restype = _ci
         lib.gdn_linear_cross_entropy_workspace_size.argtypes = [_i32] * 3 + [_ci, _i32]
         lib.gdn_linear_cross_entropy_workspace_size.restype = _sz
         lib.gdn_linear_cross_entropy_fwd.argtypes = [_vp] * 5 + [_i32] * 3 + [_ci, _vp, _sz, _vp]
@@ -485,6 +487,7 @@ def prologue_chunk_fwd(xq, xk, xv, wq, wk, wv, a, b, A_log, dt_bias, conv_state_
 # Calls of a few microseconds are held up by what surrounds them, so the wrappers below look torch's attributes up once
 # and take the current stream as the raw handle (0.1 us; the stream object takes 3).
 _F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+_CODES = {_F32: GDN_F32, _BF16: GDN_BF16}
 _empty, _empty_like = torch.empty, torch.empty_like
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -743,20 +746,19 @@ def _check_rms_args(x, weight, stats, same):
 
 
 def _rms_rows(x, weight, residual, residual_out, out=None):
-    """What the two forward calls check alike: (rows, D, residual_out).  Everything in order takes the short way."""
-    shape = x.shape
+    """What the two forward calls check alike: (rows, D, dtype code).  Everything in order takes the short way."""
+    shape, dtype = x.shape, x.dtype
     D = shape[-1] if shape else 0
+    if 0 < D <= _MOST and out is None and residual_out is None and dtype in _CODES and x.is_cuda and x.is_contiguous() and \
+            (weight is None or (weight.dtype is _F32 and weight.shape == shape[-1:] and weight.is_cuda
+                                and weight.is_contiguous())) and \
+            (residual is None or (residual.dtype is dtype and residual.shape == shape and residual.is_cuda
+                                  and residual.is_contiguous())):
+        return x.numel() // D, D, _CODES[dtype]
     if residual is None and residual_out is not None:
         raise ValueError("residual_out goes with a residual")
-    if 0 < D <= _MOST and out is None and residual_out is None and x.is_cuda and x.is_contiguous() and \
-            (weight is None or (_sound(weight, _F32) and weight.shape == (D,))) and \
-            (residual is None or (_sound(residual, x.dtype) and residual.shape == shape)):
-        rows = x.numel() // D
-    else:
-        rows, D = _check_rms_args(x, weight, (), (residual, residual_out, out))
-    if residual is not None and residual_out is None:
-        residual_out = _empty_like(x)
-    return rows, D, residual_out
+    rows, D = _check_rms_args(x, weight, (), (residual, residual_out, out))
+    return rows, D, _dt(x)
 
 
 def rms_norm_fwd(x, weight=None, residual=None, eps=1e-5, out=None, residual_out=None, stream=None):
@@ -768,13 +770,16 @@ def rms_norm_fwd(x, weight=None, residual=None, eps=1e-5, out=None, residual_out
     if stream is not None:
         return _elsewhere(stream, rms_norm_fwd, x, weight, residual, eps, out, residual_out)
     lib = _lib or load_library()
-    rows, D, residual_out = _rms_rows(x, weight, residual, residual_out, out)
-    dt = _dt(x)
+    rows, D, dt = _rms_rows(x, weight, residual, residual_out, out)
     if out is None:
         out = _empty_like(x)
+    if residual is not None and residual_out is None:
+        residual_out = _empty_like(x)
     rstd = _empty(x.shape[:-1], dtype=_F32, device=x.device)
-    rc = lib.gdn_rms_norm_fwd(x.data_ptr(), _ptr(residual), None if weight is None else weight.data_ptr(), out.data_ptr(),
-                              _ptr(residual_out), rstd.data_ptr(), rows, D, dt, eps, _stream_of(x))
+    rc = lib.gdn_rms_norm_fwd(x.data_ptr(), None if residual is None else residual.data_ptr(),
+                              None if weight is None else weight.data_ptr(), out.data_ptr(),
+                              None if residual is None else residual_out.data_ptr(), rstd.data_ptr(), rows, D, dt, eps,
+                              _stream_of(x))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_rms_norm_fwd")
     return out, residual_out, rstd
@@ -787,12 +792,14 @@ def rms_norm_fp8(x, weight=None, residual=None, eps=1e-5, residual_out=None, str
     if stream is not None:
         return _elsewhere(stream, rms_norm_fp8, x, weight, residual, eps, residual_out)
     lib = _lib or load_library()
-    rows, D, residual_out = _rms_rows(x, weight, residual, residual_out)
-    dt = _dt(x)
+    rows, D, dt = _rms_rows(x, weight, residual, residual_out)
+    if residual is not None and residual_out is None:
+        residual_out = _empty_like(x)
     q = _empty_like(x, dtype=_E4M3)
-    scales = _empty((*x.shape[:-1], -(-D // 128)), dtype=_F32, device=x.device)
-    rc = lib.gdn_rms_norm_fp8(x.data_ptr(), _ptr(residual), None if weight is None else weight.data_ptr(), q.data_ptr(),
-                              scales.data_ptr(), _ptr(residual_out), rows, D, dt, eps, _stream_of(x))
+    scales = _empty(x.shape[:-1] + (-(-D // 128),), dtype=_F32, device=x.device)
+    rc = lib.gdn_rms_norm_fp8(x.data_ptr(), None if residual is None else residual.data_ptr(),
+                              None if weight is None else weight.data_ptr(), q.data_ptr(), scales.data_ptr(),
+                              None if residual is None else residual_out.data_ptr(), rows, D, dt, eps, _stream_of(x))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_rms_norm_fp8")
     return q, scales, residual_out
@@ -848,7 +855,7 @@ def fp8_quantize(x, block_rows=1, stream=None):
     _need_cuda(x)
     q = _empty_like(x, dtype=_E4M3)
     lead = shape[:-1] if block_rows == 1 else (-(-rows // 128),)
-    scales = _empty((*lead, -(-D // 128)), dtype=_F32, device=x.device)
+    scales = _empty(lead + (-(-D // 128),), dtype=_F32, device=x.device)
     rc = lib.gdn_fp8_quantize(x.data_ptr(), q.data_ptr(), scales.data_ptr(), rows, D, block_rows, dt, _stream_of(x))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_fp8_quantize")
@@ -877,21 +884,20 @@ def fp8_linear(x, x_scales, weight, weight_scales, out=None, workspace=None, str
     if N < 1 or K < 1:
         raise ValueError("N and K must be 1 or more")
     M = x.numel() // K
-    if max(M, N, K) > _MOST:
+    if M > _MOST or N > _MOST or K > _MOST:
         _too_large(M=M, N=N, K=K)
-    blocks = -(-K // 128)
+    blocks, lead = -(-K // 128), xs[:-1]
     if x.dtype is not _E4M3 or weight.dtype is not _E4M3:
         raise TypeError("x and weight must be float8_e4m3fn")
     if x_scales.dtype is not _F32 or weight_scales.dtype is not _F32:
         raise TypeError("scales must be float32")
-    if x_scales.shape != (*xs[:-1], blocks) or weight_scales.shape != (-(-N // 128), blocks):
+    if x_scales.shape != lead + (blocks,) or weight_scales.shape != (-(-N // 128), blocks):
         raise ValueError("x_scales must be [..., ceil(K / 128)], weight_scales [ceil(N / 128), ceil(K / 128)]")
-    shape = (*xs[:-1], N)
     if out is None:
-        out = _empty(shape, dtype=_BF16, device=x.device)
+        out = _empty(lead + (N,), dtype=_BF16, device=x.device)
     elif out.dtype is not _BF16:
         raise TypeError("out must be bfloat16")
-    elif out.shape != shape:
+    elif out.shape != lead + (N,):
         raise ValueError("out must be [..., N]")
     _need_cuda(x, x_scales, weight, weight_scales, out)
     work, size = _workspace(workspace, 0 if workspace is not None else lib.gdn_fp8_linear_workspace_size(M, N, K), x.device)
@@ -1027,6 +1033,8 @@ def linear_log_probs_bwd(h, weight, targets, lse, entropy, dlogp, dentropy=None,
     lib = _lib or load_library()
     if dentropy is not None and entropy is None:
         raise ValueError("dentropy goes with the forward's entropy")
+    if lse is None or dlogp is None:
+        raise ValueError("the forward's lse and the gradient dlogp are needed")
     N, D, V = _check_ce_args(h, weight, targets, [t for t in (lse, dlogp, entropy, dentropy) if t is not None])
     dt = _dt(h)
     dh, dw = _empty_like(h), _empty_like(weight)
@@ -1054,6 +1062,17 @@ def selftest_wait_timeout(workspace, limit_us=20000, stream=None):
     rc = load_library().gdn_selftest_wait_timeout(_ptr(workspace), int(limit_us), _stream(stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_selftest_wait_timeout")
+
+
+def selftest_fp8_linear_timeout(x, x_scales, weight, weight_scales, out, workspace, limit_us=20000, stream=None):
+    """``gdn_selftest_fp8_linear_timeout``: a product one of whose tiles' data never comes; its kernel gives up after
+    ``limit_us`` and leaves NaN in the results that it reaches.  x [M,K], out [M,N]."""
+    _need_cuda(x, x_scales, weight, weight_scales, out, workspace)
+    rc = load_library().gdn_selftest_fp8_linear_timeout(
+        limit_us, _ptr(x), _ptr(x_scales), _ptr(weight), _ptr(weight_scales), _ptr(out), x.shape[0], weight.shape[0],
+        x.shape[1], _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_selftest_fp8_linear_timeout")
 
 
 def selftest_linear_cross_entropy_timeout(step, h, weight, targets, lse, dloss, out0, out1, workspace, limit_us=20000,

@@ -574,8 +574,8 @@ size_t gdn_fp8_linear_workspace_size(int32_t M, int32_t N, int32_t K)
     return fp8_linear_workspace_bytes(M, N, K);
 }
 
-gdn_status gdn_fp8_linear(const void *x, const float *x_scales, const void *w, const float *w_scales, void *out, int32_t M,
-                          int32_t N, int32_t K, void *workspace, size_t workspace_bytes, void *stream)
+static gdn_status fp8_args(Fp8LinearArgs &a, const void *x, const float *x_scales, const void *w, const float *w_scales,
+                           void *out, int32_t M, int32_t N, int32_t K, void *workspace, size_t workspace_bytes)
 {
     if (M < 0 || N < 1 || K < 1) return GDN_ERR_INVALID_ARG;
     if (!fp8_size_supported(M, N, K)) return GDN_ERR_UNSUPPORTED;
@@ -583,12 +583,33 @@ gdn_status gdn_fp8_linear(const void *x, const float *x_scales, const void *w, c
     if (!w || !w_scales || !aligned_to(x_scales, 4) || !aligned_to(w_scales, 4) || !aligned_to(out, 2)) return GDN_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace & 255u) != 0) return GDN_ERR_WORKSPACE;
     if (workspace_bytes < gdn_fp8_linear_workspace_size(M, N, K)) return GDN_ERR_WORKSPACE;
-    if (M == 0) return GDN_OK;
-    Fp8LinearArgs a = Fp8LinearArgs();
+    a = Fp8LinearArgs();
     a.x = (const unsigned char *)x; a.w = (const unsigned char *)w; a.xs = x_scales; a.ws = w_scales; a.out = out;
     a.M = M; a.N = N; a.K = K;
     a.workspace = workspace;
+    return GDN_OK;
+}
+
+gdn_status gdn_fp8_linear(const void *x, const float *x_scales, const void *w, const float *w_scales, void *out, int32_t M,
+                          int32_t N, int32_t K, void *workspace, size_t workspace_bytes, void *stream)
+{
+    Fp8LinearArgs a;
+    const gdn_status s = fp8_args(a, x, x_scales, w, w_scales, out, M, N, K, workspace, workspace_bytes);
+    if (s != GDN_OK || M == 0) return s;
     return launch_fp8_linear(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_selftest_fp8_linear_timeout(uint32_t limit_us, const void *x, const float *x_scales, const void *w,
+                                           const float *w_scales, void *out, int32_t M, int32_t N, int32_t K,
+                                           void *workspace, size_t workspace_bytes, void *stream)
+{
+    Fp8LinearArgs a;
+    if (limit_us < 1 || limit_us > 1000000u) return GDN_ERR_INVALID_ARG;
+    const gdn_status s = fp8_args(a, x, x_scales, w, w_scales, out, M, N, K, workspace, workspace_bytes);
+    if (s != GDN_OK) return s;
+    if (M < 1) return GDN_ERR_INVALID_ARG;
+    if (!fp8_linear_tc_supported(a)) return GDN_ERR_UNSUPPORTED;
+    return launch_fp8_linear_tc(a, (cudaStream_t)stream, (uint64_t)limit_us * 1000u) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 // launch grids and tile counts stay within 32 bits

@@ -41,6 +41,8 @@ struct Fp8Params {
     const float *xs, *ws;
     __nv_bfloat16 *out;
     unsigned *err;
+    uint64_t limit_ns;        // of a wait
+    int silent;               // the self-test: the pair or CTA whose loads never come, else -1
 };
 
 struct Fp8Maps {
@@ -74,7 +76,7 @@ __device__ __forceinline__ void mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64
 // These kernels' barriers order tensor memory, by tcgen05 fences, and what the asynchronous proxy wrote, so their waits
 // and arrivals need no wider ordering: a release to the cluster waits for the warp's loads in flight, GPU-wide latency on
 // the chain of every block.
-__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned *err)
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile int *abort_flag, const Fp8Params &p)
 {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
@@ -82,9 +84,9 @@ __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatil
         for (int i = 0; i < 64; ++i)
             if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        if (globaltimer_ns() - t0 > p.limit_ns) {
             *abort_flag = 1;
-            atomicExch(err, kDevErrTimeout);
+            atomicExch(p.err, kDevErrTimeout);
             return false;
         }
     }
@@ -155,7 +157,7 @@ pair_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Par
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + (abort_addr - base));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_here(bar, parity, abort_flag, p.err); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_here(bar, parity, abort_flag, p); };
 
     if (threadIdx.x == 32) {
         prefetch_tmap(&maps.x);
@@ -193,7 +195,7 @@ pair_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Par
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int t = pair_id; t < tiles && ok; t += pairs) {
+            for (int t = pair_id == p.silent ? tiles : pair_id; t < tiles && ok; t += pairs) {
                 int m, n;
                 pair_tile(p, t, m, n);
                 const int m0 = m * kTile + (int)rank * kHalf, n0 = n * kTile + (int)rank * kHalf;
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(few_threads<TN>(), TN == 128 ? 1 : 2) few_kern
     const int splits = p.splits, rank = (int)(blockIdx.x % (unsigned)splits), tile = (int)(blockIdx.x / (unsigned)splits);
     const int m0 = tile % p.mt * TN, n0 = tile / p.mt * kRows;
     const int k0 = (int)((int64_t)p.kb * rank / splits), k1 = (int)((int64_t)p.kb * (rank + 1) / splits);
-    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_here(bar, parity, abort_flag, p.err); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_here(bar, parity, abort_flag, p); };
 
     if (threadIdx.x == 32) {
         prefetch_tmap(&maps.x);
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(few_threads<TN>(), TN == 128 ? 1 : 2) few_kern
         if (lane == 0) {
             bool ok = true;
             int it = 0;
-            for (int k = k0; k < k1; ++k, ++it) {
+            for (int k = (int)blockIdx.x == p.silent ? k1 : k0; k < k1; ++k, ++it) {
                 const int s = it % stages;
                 if (!wait(empty + 8 * s, ((it / stages) & 1) ^ 1)) { ok = false; break; }
                 mbar_expect_tx(full + 8 * s, stage_bytes);
@@ -646,9 +648,11 @@ bool fp8_linear_tc_supported(const Fp8LinearArgs &a)
     return a.K % 16 == 0 && (((uintptr_t)a.x | (uintptr_t)a.w | (uintptr_t)a.out) & 15) == 0;
 }
 
-cudaError_t launch_fp8_linear_tc(const Fp8LinearArgs &a, cudaStream_t st)
+cudaError_t launch_fp8_linear_tc(const Fp8LinearArgs &a, cudaStream_t st, uint64_t stall_ns)
 {
     Fp8Params p = {};
+    p.silent = stall_ns ? 0 : -1;
+    p.limit_ns = stall_ns ? stall_ns : kWaitLimitNs;
     p.M = a.M; p.N = a.N; p.K = a.K;
     p.kb = ceil_div(a.K, kDepth);
     p.xs = a.xs; p.ws = a.ws;

@@ -4,6 +4,9 @@
 // Bound by memory: x read once, q and the scales written.  A block of a row lies in the registers of the 16 (bf16) or 32
 // (fp32) threads that read it in 16-byte accesses, its maximum goes by shuffles; a 128 x 128 block in those of a CTA.
 // Rows that 16-byte accesses do not fit go element by element.
+//
+// Measured (GB300, device time): 8192 x 2048 bf16 10.2 us, 5.0 TB/s (four blocks of a thread on their way instead of two 11.8,
+// eight 12.5 to 13.1; a CTA for each two instead of a grid that stays 10.5).
 #include "common.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
@@ -43,7 +46,7 @@ struct Chunk {      // 16 bytes
 template <typename T, bool EVEN>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const Fp8QuantArgs a, int64_t items, unsigned per_row)
 {
-    constexpr int VW = Chunk<T>::kSize, kLanes = kFp8Block / VW, kAhead = 4;
+    constexpr int VW = Chunk<T>::kSize, kLanes = kFp8Block / VW, kAhead = 2;
     const int lane = threadIdx.x % kLanes;
     const int64_t step = (int64_t)gridDim.x * (kThreads / kLanes);
     // the threads of a warp stay together: a block behind the last reads as zeros

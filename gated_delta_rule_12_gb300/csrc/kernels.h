@@ -158,7 +158,8 @@ cudaError_t launch_fp8_quantize(const Fp8QuantArgs &a, cudaStream_t st);
 cudaError_t launch_fp8_linear(const Fp8LinearArgs &a, cudaStream_t st);
 // K a multiple of 16, tensors on 16-byte boundaries
 bool fp8_linear_tc_supported(const Fp8LinearArgs &a);
-cudaError_t launch_fp8_linear_tc(const Fp8LinearArgs &a, cudaStream_t st);
+// stall_ns: the self-test's; the first tile's data never comes, and waits give up after it
+cudaError_t launch_fp8_linear_tc(const Fp8LinearArgs &a, cudaStream_t st, uint64_t stall_ns = 0);
 size_t fp8_linear_workspace_bytes(int M, int N, int K);
 // out, grad: the log probabilities' calls
 cudaError_t launch_linear_ce_fwd(const LinearCeArgs &a, cudaStream_t st, const LogProbs *out = nullptr);

