@@ -26,6 +26,11 @@
 // loss is off by 3.1e-7 of its size (255 x 1024 x 50257) and 7.0e-7 (8192 x 2048 x 32768), where fp32 products and expf
 // leave 5e-8 and 7e-8.
 //
+// The log probabilities are the same products: their forward pass adds the entropy's sum to a row's statistics and keeps a
+// row's best words (log_probs.cuh), their gradient is another E.  8192 x 2048 x 32768 0.50 ms without alternatives, 0.54 with
+// five and 0.70 with twenty; 255 x 1024 x 50257 30, 49 (eight) and 90 us: a row's first tile costs the epilogue some 6 us (20
+// with twenty), one word after another out of each of 32 rows, which only products of a few thousand terms cover.
+//
 // Bound by the tensor cores, or by reading w where tokens are few.  Measured on the device: loss of 8192 x 2048 x 32768
 // 0.54 ms (2.0 PFLOP/s), gradient with 65536 words 3.6 ms (1.83 PFLOP/s); both run into the power limit when repeated
 // (0.61 and 3.9 to 4.1 ms).  Loss of 255 x 1024 x 50257 29 us, half of the copy rate: three rounds of tiles and what
@@ -789,8 +794,10 @@ cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, cons
         p.top = out->top_k;
         p.order = part_order(a.N, a.V);
         p.tiles0 = p.tiles = p.order.pairs * p.order.rounds();
-        // Tiles tell later ones of their rows what need not be kept, where there are rounds of them to tell.
-        if (p.top > 0 && p.tiles > kPairs) {
+        // Tiles tell later ones of their rows what need not be kept, where there are rounds enough of them to tell: clearing
+        // the words is a launch more (255 x 1024 x 50257, three rounds, top 8: 48.7 us without, 52.6 with; 8192 x 2048 x
+        // 32768, top 5: 587 us without, 541 with; top 20: 937 and 703).
+        if (p.top > 0 && p.tiles > 4 * kPairs) {
             p.cut = (unsigned *)(w + ws.cut);
             const cudaError_t e = cudaMemsetAsync(p.cut, 0, (size_t)a.N * 4, st);
             if (e != cudaSuccess) return e;
