@@ -551,8 +551,8 @@ gdn_status gdn_linear_log_probs_fwd(const void *h, const void *weight, const int
  *   dlogp         [N] fp32;  dentropy [N] fp32 or NULL for zeros.
  *   dh, dweight, workspace (its size with backward = 1, whatever top_k is), ignored rows and errors as
  *                 gdn_linear_cross_entropy_bwd.
- * On the tensor cores G enters the products as bf16 in units of each row's max(|dlogp|, |dentropy|) (of -dlogp without
- * dentropy), and that times h as bf16 in units of the largest; sums are fp32.
+ * On the tensor cores G enters the products as bf16 in units of each row's |dlogp| (|dentropy| where that is 2^20 times
+ * larger), and that times h as bf16 in units of the largest; sums are fp32.
  */
 gdn_status gdn_linear_log_probs_bwd(const void *h, const void *weight, const int32_t *targets,
                                     const float *lse, const float *entropy, const float *dlogp, const float *dentropy,
