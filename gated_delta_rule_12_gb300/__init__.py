@@ -158,6 +158,8 @@ def load_library(path: str = LIB_PATH, build_if_missing: bool = False) -> ctypes
         lib.gdn_linear_log_probs_workspace_size.restype = _sz
         lib.gdn_linear_log_probs_fwd.argtypes = [_vp] * 8 + [_i32] * 4 + [_ci, _vp, _sz, _vp]
         lib.gdn_linear_log_probs_bwd.argtypes = [_vp] * 9 + [_i32] * 3 + [_ci, _vp, _sz, _vp]
+        lib.gdn_selftest_linear_log_probs_timeout.argtypes = [ctypes.c_uint32] + [_vp] * 7 + [_i32] * 4 + [_vp, _sz, _vp]
+        lib.gdn_selftest_linear_log_probs_timeout.restype = _ci
         lib.gdn_selftest_linear_cross_entropy_timeout.argtypes = [_i32, ctypes.c_uint32] + [_vp] * 7 + [_i32] * 3 + \
             [_vp, _sz, _vp]
         lib.gdn_selftest_linear_cross_entropy_timeout.restype = _ci
@@ -1086,6 +1088,21 @@ def selftest_linear_cross_entropy_timeout(step, h, weight, targets, lse, dloss, 
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     if rc != GDN_OK:
         raise GDNError(rc, "gdn_selftest_linear_cross_entropy_timeout")
+
+
+def selftest_linear_log_probs_timeout(h, weight, targets, logp, entropy, top_ids, top_logps, workspace, limit_us=20000,
+                                      stream=None):
+    """``gdn_selftest_linear_log_probs_timeout``: a bf16 ``linear_log_probs_fwd`` one of whose tiles' data never comes; its
+    kernel gives up after ``limit_us`` and leaves NaN in the rows that it reaches.  top_ids and top_logps None: no
+    alternatives."""
+    N, D, V = _check_ce_args(h, weight, targets, [logp, entropy])
+    _need_cuda(top_ids, top_logps, workspace)
+    rc = load_library().gdn_selftest_linear_log_probs_timeout(
+        limit_us, _ptr(h), _ptr(weight), _ptr(targets), _ptr(logp), _ptr(entropy), _ptr(top_ids), _ptr(top_logps), N, D, V,
+        0 if top_ids is None else top_ids.shape[1], _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream))
+    if rc != GDN_OK:
+        raise GDNError(rc, "gdn_selftest_linear_log_probs_timeout")
 
 
 def chunk_fwd_noalloc(q, k, v, g, beta, out, final_state=None, init_state=None, cu_seqlens=None, scale=None,

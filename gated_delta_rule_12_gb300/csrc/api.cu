@@ -723,6 +723,28 @@ gdn_status gdn_linear_log_probs_bwd(const void *h, const void *weight, const int
     return launch_linear_ce_bwd(a, (cudaStream_t)stream, {dentropy, entropy, -1.f}) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+gdn_status gdn_selftest_linear_log_probs_timeout(uint32_t limit_us, const void *h, const void *weight,
+                                                 const int32_t *targets, float *logp, float *entropy, int32_t *top_ids,
+                                                 float *top_logps, int32_t N, int32_t D, int32_t V, int32_t top_k,
+                                                 void *workspace, size_t workspace_bytes, void *stream)
+{
+    LinearCeArgs a;
+    if (limit_us < 1 || limit_us > 1000000u || top_k < 0 || top_k > GDN_MOST_TOP || top_k > V) return GDN_ERR_INVALID_ARG;
+    const gdn_status s = ce_args(a, h, weight, targets, N, D, V, GDN_BF16, false, workspace, SIZE_MAX);
+    if (s != GDN_OK) return s;
+    if (!linear_ce_tc_supported(1, D)) return GDN_ERR_UNSUPPORTED;
+    if (workspace_bytes < gdn_linear_log_probs_workspace_size(N, D, V, top_k, GDN_BF16, 0)) return GDN_ERR_WORKSPACE;
+    if (N < 1 || !logp || !entropy || (top_k > 0 && (!top_ids || !top_logps))) return GDN_ERR_INVALID_ARG;
+    const void *ptrs4[] = {logp, entropy, top_ids, top_logps};
+    for (const void *p : ptrs4)
+        if (!aligned_to(p, 4)) return GDN_ERR_INVALID_ARG;
+    const LogProbs out = {logp, entropy, nullptr, top_ids, top_logps, top_k};
+    CeStall stall;
+    stall.step = 3;
+    stall.limit_ns = (uint64_t)limit_us * 1000u;
+    return launch_linear_ce_tc_fwd(a, (cudaStream_t)stream, &out, stall) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 gdn_status gdn_selftest_linear_cross_entropy_timeout(int32_t step, uint32_t limit_us, const void *h, const void *weight,
                                                      const int32_t *targets, const float *lse, const float *dloss,
                                                      void *out0, void *out1, int32_t N, int32_t D, int32_t V,

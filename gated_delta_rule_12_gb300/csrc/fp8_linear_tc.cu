@@ -365,6 +365,7 @@ constexpr int kRows = 128;                  // words of a tile
 constexpr int kTable = 4096;                // scales kept at a time
 constexpr int kPitch = kRows + 4;           // of the partial sums [token][word]
 constexpr int kMostSplits = 8;
+constexpr int kMostSmem = 226 * 1024;
 
 template <int TN> constexpr int few_warps() { return TN == 128 ? 8 : 4; }
 template <int TN> constexpr int few_threads() { return 64 + 32 * few_warps<TN>(); }
@@ -631,7 +632,8 @@ template <int TN>
 cudaError_t launch_few(const Fp8Maps &maps, const Fp8Params &p, cudaStream_t st)
 {
     const int smem = few_smem(TN, p.stages);
-    const cudaError_t e = cudaFuncSetAttribute(few_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the same limit whatever this launch takes: another thread's launch may come between the two calls
+    const cudaError_t e = cudaFuncSetAttribute(few_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.mt * p.nt * p.splits));

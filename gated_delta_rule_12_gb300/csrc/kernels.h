@@ -167,7 +167,7 @@ cudaError_t launch_linear_ce_bwd(const LinearCeArgs &a, cudaStream_t st, LogProb
 // bf16 with D a multiple of 8 (rows that TMA can address) up to 2^24: the tensor cores
 bool linear_ce_tc_supported(int dt, int D);
 size_t linear_ce_tc_workspace_bytes(int N, int D, int V, bool backward, int top = -1);   // top: of log probabilities
-// The self-test's: in this kernel (0 the logits, 1 E, 2 the gradients) the first CTA pair's loads never come, and waits give
+// The self-test's: in this kernel (0 the logits, 1 E, 2 the gradients, 3 the log probabilities' logits) the first CTA pair's loads never come, and waits give
 // up after limit_ns.
 struct CeStall {
     int step = -1;

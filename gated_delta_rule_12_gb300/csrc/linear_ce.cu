@@ -6,6 +6,9 @@
 // A row whose target is outside [0, V) is ignored: loss, lse and its gradients are 0, and nothing that its h
 // holds (NaN included) reaches dW.
 //
+// The log probabilities' calls (log_probs.cuh) take the same kernels, with the entropy's sum and a tile's best words, and
+// with the entropy's gradient in G.
+//
 // These kernels run on the CUDA cores: fp32, and bf16 whose rows are no multiple of 16 bytes; other bf16 sizes take the
 // tensor cores (linear_ce_tc.cu).  Bound by the fp32 units.
 //

@@ -767,9 +767,9 @@ size_t linear_ce_tc_workspace_bytes(int N, int D, int V, bool backward, int top)
 }
 
 template <int K>
-static cudaError_t run_stats(const CeMaps &maps, const CeParams &p, const LogProbs &out, cudaStream_t st)
+static cudaError_t run_stats(const CeMaps &maps, const CeParams &p, const LogProbs &out, cudaStream_t st, const CeStall &stall)
 {
-    const cudaError_t e = launch<kStats, K>(maps, p, st, CeStall());
+    const cudaError_t e = launch<kStats, K>(maps, p, st, stall);
     if (e != cudaSuccess) return e;
     const LogProbParts parts = {p.stat, p.best, p.at, p.targets, p.cut, p.N, 1, p.N, p.V, p.order.parts, p.top, p.order};
     return launch_early(logp_join_kernel<K>, ceil_div(p.N, 8), 256, 0, st, parts, out);
@@ -806,8 +806,8 @@ cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, cons
             const cudaError_t e = cudaMemsetAsync(p.cut, 0, (size_t)a.N * 4, st);
             if (e != cudaSuccess) return e;
         }
-        return p.top == 0 ? run_stats<0>(maps, p, *out, st) : p.top <= 8 ? run_stats<8>(maps, p, *out, st)
-                                                                      : run_stats<kMostTop>(maps, p, *out, st);
+        return p.top == 0 ? run_stats<0>(maps, p, *out, st, stall)
+               : p.top <= 8 ? run_stats<8>(maps, p, *out, st, stall) : run_stats<kMostTop>(maps, p, *out, st, stall);
     }
     const cudaError_t e = launch<kLogits>(maps, p, st, stall);
     if (e != cudaSuccess) return e;

@@ -538,6 +538,9 @@ __global__ void __launch_bounds__(kThreads) any_dw_kernel(const RmsNormArgs a)
 // host side
 // ---------------------------------------------------------------------------
 
+// The limit that every launch of a kernel sets, whatever it takes itself: another thread's launch may come between the two.
+constexpr int kMostSmem = 226 * 1024;
+
 template <typename T, int VW, int NV, int TEAM, int MAX, int FIT, bool RES, bool Q8>
 cudaError_t run_fwd(const RmsNormArgs &a, int team, cudaStream_t st)
 {
@@ -547,7 +550,7 @@ cudaError_t run_fwd(const RmsNormArgs &a, int team, cudaStream_t st)
     const int most = kSMs * (threads > 256 ? 1 : (NV * VW <= 8 ? 4 : NV * VW <= 16 ? 3 : 2) * 256 / threads);
     if (smem > 32 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(rms_fwd_kernel<T, VW, NV, TEAM, MAX, FIT, RES, Q8>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
         if (e != cudaSuccess) return e;
     }
     rms_fwd_kernel<T, VW, NV, TEAM, MAX, FIT, RES, Q8><<<(unsigned)(ctas < most ? ctas : most), threads, smem, st>>>(a, team);
@@ -584,7 +587,7 @@ cudaError_t run_bwd(const RmsNormArgs &a, int team, cudaStream_t st)
     const int smem = joined > ring ? joined : ring;
     if (smem > 32 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(rms_bwd_kernel<T, VW, NV, TEAM, MAX, FIT, RES>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
         if (e != cudaSuccess) return e;
     }
     rms_bwd_kernel<T, VW, NV, TEAM, MAX, FIT, RES><<<grid, threads, smem, st>>>(a, team);

@@ -560,6 +560,18 @@ gdn_status gdn_linear_log_probs_bwd(const void *h, const void *weight, const int
                                     void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Self-test of the log probabilities' failure path: the bf16 forward call, the data of one of whose tiles never comes.  Its
+ * waits give up after limit_us microseconds (1 .. 1e6), nothing faults, gdn_check_device_error returns
+ * GDN_ERR_DEVICE_TIMEOUT, and logp and entropy of the rows that the tile reaches are NaN.
+ * Errors: as the call; GDN_ERR_UNSUPPORTED where it would not take the tensor cores.
+ */
+gdn_status gdn_selftest_linear_log_probs_timeout(uint32_t limit_us, const void *h, const void *weight,
+                                                 const int32_t *targets, float *logp, float *entropy,
+                                                 int32_t *top_ids, float *top_logps,
+                                                 int32_t N, int32_t D, int32_t V, int32_t top_k,
+                                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Self-test of the cross entropy's failure path: the bf16 call (step 0: forward, out0 = loss, out1 = lse; steps 1 and 2:
  * backward, out0 = dh, out1 = dweight; out1 may be NULL) in whose logits (0), softmax (1) or gradient (2) kernel the data
  * of one tile never comes.  Its waits give up after limit_us microseconds (1 .. 1e6), nothing faults,

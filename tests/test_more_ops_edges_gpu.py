@@ -121,6 +121,26 @@ def test_a_wait_that_gives_up(M, N, K):
     gdn.check_device_error(room)
 
 
+@pytest.mark.parametrize("N,V,k", [(100, 700, 0), (100, 700, 4), (2600, 9000, 9)])
+def test_log_probabilities_whose_wait_gives_up(N, V, k):
+    """The same of the log probabilities: the rows of the first pair's tiles are NaN, and the next call is right."""
+    gen = torch.Generator().manual_seed(N)
+    h, w = torch.randn(N, 64, generator=gen).bfloat16().cuda(), (torch.randn(V, 64, generator=gen) / 4).bfloat16().cuda()
+    t = torch.randint(0, V, (N,), generator=gen).int().cuda()
+    want = gdn.linear_log_probs_fwd(h, w, t, top_k=k)
+    logp, H = torch.zeros(N, device="cuda"), torch.zeros(N, device="cuda")
+    ids = torch.zeros(N, k, dtype=torch.int32, device="cuda") if k else None
+    top = torch.zeros(N, k, device="cuda") if k else None
+    room = torch.empty(gdn.linear_log_probs_workspace_size(N, 64, V, k), dtype=torch.uint8, device="cuda")
+    gdn.selftest_linear_log_probs_timeout(h, w, t, logp, H, ids, top, room, limit_us=3000)
+    with pytest.raises(gdn.GDNError, match="TIMEOUT"):
+        gdn.check_device_error(room)
+    assert torch.isnan(logp[:100]).all() and torch.isnan(H[:100]).all()
+    got = gdn.linear_log_probs_fwd(h, w, t, top_k=k, workspace=room)
+    gdn.check_device_error(room)
+    assert all(a is None or torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_products_at_once():
     """Two streams with products of both kernels and log probabilities next to one another, time and again."""
     ops = operators()

@@ -77,3 +77,15 @@ STALL = dict(limit=1000, x=FAKE, xs=FAKE, w=FAKE, ws=FAKE, out=FAKE, M=4, N=16, 
 def test_selftest_refusals(over, code):
     gbuild.build()
     assert gdn.load_library().gdn_selftest_fp8_linear_timeout(*{**STALL, **over}.values()) == code
+
+
+LOGP_STALL = dict(limit=1000, h=FAKE, w=FAKE, t=FAKE, logp=FAKE, ent=FAKE, ids=FAKE, top=FAKE, N=4, D=16, V=32, k=3,
+                  work=FAKE, size=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("over,code", [(dict(limit=0), 1), (dict(limit=1000001), 1), (dict(h=None), 1), (dict(N=0), 1),
+                                       (dict(k=33), 1), (dict(ids=None), 1), (dict(logp=FAKE + 2), 1), (dict(D=12), 2),
+                                       (dict(work=None), 3), (dict(size=256), 3)])
+def test_log_probabilities_selftest_refusals(over, code):
+    gbuild.build()
+    assert gdn.load_library().gdn_selftest_linear_log_probs_timeout(*{**LOGP_STALL, **over}.values()) == code
