@@ -198,10 +198,11 @@ template <int MODE, int K = 0>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CeParams p)
 {
+    constexpr int kWarpStore = K ? 2 * kStore : kStore;   // K: 64 words of each of a warp's rows
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t stores = base + kStages * kStageBytes;
-    const uint32_t bars = stores + kEpilogueWarps * kStore;
+    const uint32_t bars = stores + kEpilogueWarps * kWarpStore;
     const uint32_t full = bars, empty = bars + 8 * kStages, acc_full = bars + 16 * kStages, acc_empty = acc_full + 16;
     const uint32_t tmem_slot = acc_empty + 16, abort_addr = tmem_slot + 4;
     unsigned char *gen = smem_raw + (base - smem_u32(smem_raw));
@@ -313,7 +314,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
     } else {
         const uint32_t quarter = warp & 3;                     // the 32 tensor-memory lanes a warp may read
         constexpr int chunks = kTile / 32;
-        const uint32_t buf0 = stores + (warp - 2) * kStore;
+        const uint32_t buf0 = stores + (warp - 2) * kWarpStore;
         const uint32_t leader_empty = map_to_rank(acc_empty, 0);
         uint32_t tiles = 0;
         float top = -INFINITY, sum = 0.f, u = 0.f;
@@ -502,32 +503,51 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                         told();
                     }
 #pragma unroll 1
-                    for (int ch = 0; ch < chunks; ++ch) {
-                        if (!__any_sync(0xffffffffu, in && (hot >> ch & 1u))) continue;
-                        uint32_t r[32];
-                        tmem_ld32(src + ch * 32, r);
-                        tmem_wait_ld();
-                        const int c0 = col0 + ch * 32;
-                        unsigned some = 0u;
+                    for (int ch = 0; ch < chunks; ch += 2) {   // 64 words at a time
+                        unsigned some[2];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) some |= (__uint_as_float(r[j]) > cut && c0 + j < p.V ? 1u : 0u) << j;
-                        if (!in) some = 0u;
-                        if (!__any_sync(0xffffffffu, some != 0u)) continue;
+                        for (int half = 0; half < 2; ++half) {
+                            some[half] = 0u;
+                            if (!__any_sync(0xffffffffu, in && (hot >> (ch + half) & 1u))) continue;
+                            uint32_t r[32];
+                            tmem_ld32(src + (ch + half) * 32, r);
+                            tmem_wait_ld();
+                            const int c0 = col0 + (ch + half) * 32;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) some[half] |= (__uint_as_float(r[j]) > cut && c0 + j < p.V ? 1u : 0u) << j;
+                            if (!in) some[half] = 0u;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                st_shared16(buf0 + half * kStore + lane * 128 + ((j ^ (lane & 7)) << 4), r[4 * j], r[4 * j + 1],
+                                            r[4 * j + 2], r[4 * j + 3]);
+                        }
                         // They come out one at a time, each lane its own: found by their bits, then read back from the warp's
-                        // buffer, as registers have no variable index.
-                        const uint32_t row_s = buf0 + lane * 128;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            st_shared16(row_s + ((j ^ (lane & 7)) << 4), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                        while (__any_sync(0xffffffffu, some != 0u)) {
-                            if (some) {
-                                const int j = __ffs((int)some) - 1;
-                                some &= some - 1u;
-                                float x;
-                                asm volatile("ld.shared.f32 %0, [%1];"
-                                             : "=f"(x) : "r"(row_s + (((j >> 2) ^ (lane & 7)) << 4) + (j & 3) * 4) : "memory");
-                                best.add(x, c0 + j);
+                        // buffer, as registers have no variable index; the next one is on its way while one is inserted.
+                        auto take = [&](float &x, int &word) {
+                            const int half = some[0] ? 0 : 1;
+                            const unsigned m = half ? some[1] : some[0];
+                            if (!m) return false;
+                            const int j = __ffs((int)m) - 1;
+                            if (half) some[1] &= m - 1u;
+                            else some[0] &= m - 1u;
+                            asm volatile("ld.shared.f32 %0, [%1];"
+                                         : "=f"(x) : "r"(buf0 + half * kStore + lane * 128 + (((j >> 2) ^ (lane & 7)) << 4) + (j & 3) * 4)
+                                         : "memory");
+                            word = col0 + (ch + half) * 32 + j;
+                            return true;
+                        };
+                        float x = 0.f, x2 = 0.f;
+                        int word = 0, word2 = 0;
+                        bool have = take(x, word);
+                        while (__any_sync(0xffffffffu, have)) {
+                            bool more = false;
+                            if (have) {
+                                more = take(x2, word2);
+                                best.add(x, word);
                             }
+                            have = more;
+                            x = x2;
+                            word = word2;
                         }
                         cut = fmaxf(cut, best.value(p.top - 1));
                     }
@@ -743,10 +763,11 @@ cudaError_t launch(const CeMaps &maps, CeParams p, cudaStream_t st, const CeStal
 {
     p.silent = stall.step == MODE ? 0 : -1;
     p.limit_ns = stall.step == MODE ? stall.limit_ns : kWaitLimitNs;
-    const cudaError_t e = cudaFuncSetAttribute(ce_tc_kernel<MODE, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    constexpr int smem = kSmem + (K ? kEpilogueWarps * kStore : 0);
+    const cudaError_t e = cudaFuncSetAttribute(ce_tc_kernel<MODE, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int pairs = p.tiles < kPairs ? p.tiles : kPairs;
-    return launch_early(ce_tc_kernel<MODE, K>, 2 * pairs, kThreads, kSmem, st, maps, p);
+    return launch_early(ce_tc_kernel<MODE, K>, 2 * pairs, kThreads, smem, st, maps, p);
 }
 
 unsigned grid_for(int64_t items)
