@@ -28,7 +28,7 @@
 //
 // The log probabilities are the same products: their forward pass adds the entropy's sum to a row's statistics and keeps a
 // row's best words (log_probs.cuh), their gradient is another E.  8192 x 2048 x 32768 0.50 ms without alternatives, 0.54 with
-// five and 0.70 with twenty; 255 x 1024 x 50257 30, 49 (eight) and 90 us: a row's first tile costs the epilogue some 6 us (20
+// five and 0.65 with twenty; 255 x 1024 x 50257 28, 47 (eight) and 89 us: a row's first tile costs the epilogue some 6 us (16
 // with twenty), one word after another out of each of 32 rows, which only products of a few thousand terms cover.
 //
 // Bound by the tensor cores, or by reading w where tokens are few.  Measured on the device: loss of 8192 x 2048 x 32768
@@ -346,6 +346,8 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 entropy = __ldg(p.entropy + row);
             }
             if (MODE == kGrads && c.which == 0) scale = __ldg(p.scale);
+            auto told = [&] { return K && in && p.cut ? *(volatile const unsigned *)(p.cut + row) : 0u; };
+            unsigned other = told();                   // what other tiles have found: words equal to it may be among the best
             const bool keep = (MODE == kGrads && !direct) || (target >= 0 && target < p.V);
             if (!__all_sync(0xffffffffu, wait_bar(acc_full + 8 * buf, use & 1, abort_flag, p))) break;
             fence_after_sync();
@@ -362,11 +364,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 ends = next.k0 >= next.k1 || next.m != c.m || next.part != c.part;
             }
             begins = ends;
-            auto told = [&] {                          // what other tiles have found: words equal to it may be
-                const unsigned c = in && p.cut ? *(volatile const unsigned *)(p.cut + row) : 0u;
-                if (c) cut = fmaxf(cut, below(c));
-            };
-            if (K) told();
+            if (K && other) cut = fmaxf(cut, below(other));
             const bool fresh = K && __any_sync(0xffffffffu, in && cut == -INFINITY);
             unsigned hot = 0u;                         // chunks with words above it
             float most[K ? 32 : 1];                    // fresh: the largest of every 32nd word
@@ -500,7 +498,8 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                             if (p.cut) atomicMax(p.cut + row, order_of(least));
                             cut = fmaxf(cut, below(order_of(least)));
                         }
-                        told();
+                        other = told();
+                        if (other) cut = fmaxf(cut, below(other));
                     }
 #pragma unroll 1
                     for (int ch = 0; ch < chunks; ch += 2) {   // 64 words at a time
@@ -821,7 +820,7 @@ cudaError_t launch_linear_ce_tc_fwd(const LinearCeArgs &a, cudaStream_t st, cons
         p.tiles0 = p.tiles = p.order.pairs * p.order.rounds();
         // Tiles tell later ones of their rows what need not be kept, where there are rounds enough of them to tell: clearing
         // the words is a launch more (255 x 1024 x 50257, three rounds, top 8: 48.7 us without, 52.6 with; 8192 x 2048 x
-        // 32768, top 5: 587 us without, 541 with; top 20: 937 and 703).
+        // 32768, top 5: 587 us without, 541 with; top 20: 937 and 703; 32 words at a time then).
         if (p.top > 0 && p.tiles > 4 * kPairs) {
             p.cut = (unsigned *)(w + ws.cut);
             const cudaError_t e = cudaMemsetAsync(p.cut, 0, (size_t)a.N * 4, st);

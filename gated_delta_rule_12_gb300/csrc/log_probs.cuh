@@ -244,7 +244,7 @@ static __global__ void __launch_bounds__(256) logp_join_kernel(LogProbParts p, L
         for (int j = 0; j < 4; ++j) {
             if (!in[j]) continue;
             join(v[j].x, v[j].y, v[j].z);
-            if (K && !(v[j].x < cut)) {   // (0 in place of an infinite maximum: the words tell)
+            if (K && !(v[j].x < cut && v[j].y < INFINITY)) {   // (an infinite maximum, 0 here, leaves an infinite sum)
                 const int count = __float_as_int(v[j].w);
                 const float2 *words = p.best + ((first + 32 * j) * p.part_step + row * p.row_step) * p.top;
                 for (int c = 0; c < count; c += 4) {

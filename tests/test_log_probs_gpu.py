@@ -210,6 +210,18 @@ def test_words_without_a_probability(dtype):
     assert logp[2] == float("-inf") and abs(logp[0].item() - p[0].log().item()) < 1e-6
 
 
+def test_an_infinite_logit_among_many_tiles():
+    """+inf is the best word wherever it stands; its row has no finite results, and the others are as they were."""
+    h, w, t, _, _ = make(2100, 64, 9000, "bf16", seed=2, ignored=0.0)
+    h[:, 0] = 0
+    clean = gdn.linear_log_probs_fwd(h, w, t, top_k=3)
+    h[77, 0], w[5003, 0] = 1e20, 3e38
+    out = gdn.linear_log_probs_fwd(h, w, t, top_k=3)
+    assert out[3][77, 0] == 5003 and not torch.isfinite(out[0][77]) and not torch.isfinite(out[1][77])
+    rest = torch.arange(2100) != 77
+    assert all(torch.equal(x[rest], y[rest]) for x, y in zip(out, clean))
+
+
 def test_equal_logits_and_a_sure_word():
     """All words alike: entropy log V and the lowest ids.  One word far above the rest: entropy 0."""
     h, w = torch.zeros(9, 64, dtype=torch.bfloat16).cuda(), torch.randn(1000, 64).to(torch.bfloat16).cuda()
