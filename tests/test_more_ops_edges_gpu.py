@@ -172,3 +172,22 @@ def test_captured_graphs_in_turn():
             graphs[n][0].replay()
     for n in NAMES:
         assert all(same(p, q) for p, q in zip(graphs[n][1], want[n])), n
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,D", [(40001, 3), (21003, 57), (11001, 121), (5003, 249), (10001, 505), (1501, 1013),
+                                    (700, 2049), (311, 4093), (9001, 1024), (40000, 128)])
+def test_8_bit_rows_of_any_length(rows, D, dtype):
+    """More rows than a grid has teams or warps, at every place of a 16-byte chunk: the norm's output within its bound, the
+    quantised rows to the bit, and both products' inputs alike."""
+    gen = torch.Generator().manual_seed(rows)
+    x, res = (torch.randn(rows, D, generator=gen).to(dtype).cuda() for _ in range(2))
+    w = (1 + 0.1 * torch.randn(D, generator=gen)).cuda()
+    q, c, s = gdn.rms_norm_fp8(x, w, residual=res)
+    assert torch.equal(s, (x.float() + res.float()).to(dtype))
+    (y, _), (e, _) = ref.rms_fwd(s, w, 1e-5)
+    ref.check_e4m3(q, ref.spread(c, rows, D, 1), y, 2 * e, "norm")
+    q, c = gdn.fp8_quantize(x)
+    want_c = ref.scales(x, 1).float().clamp(min=ref.TINY) / 448
+    u = x.cpu().float() / ref.spread(want_c, rows, D, 1).float()
+    assert torch.equal(c.cpu(), want_c) and same(q.cpu(), u.clamp(-448, 448).to(torch.float8_e4m3fn))
