@@ -19,8 +19,7 @@
 // relaxed ones 221 us (the release waits for the scale loads in flight); waits with a suspend hint 95.6; scales one block
 // ahead 91.5; sixteen epilogue warps 98 to 104, also with registers moved to them; 128 words a multiplication in four quarters
 // of tensor memory 132 (109 with 256 there); 160 words and three accumulators 129; one forwarded arrival of the peer instead of
-// eight 94; multiplications of a CTA's own with half of the words multicast to it 95.  In timing copies the parts add up:
-// synchronisation 40 us, reading back 29, multiplying 16, loads 10, results' way out 7.  For few tokens by latency: one token takes
+// eight 94; multiplications of a CTA's own with half of the words multicast to it 95.  For few tokens by latency: one token takes
 // 5.2 us where its weights' bytes take 1.9.
 //
 // Every wait on an mbarrier is bounded (1 s); a timeout records kDevErrTimeout in the workspace's error word and leaves NaN
