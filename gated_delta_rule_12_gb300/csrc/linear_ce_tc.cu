@@ -80,7 +80,7 @@ struct RowWeights {
         const float x = __ldg(a + row);
         if (!b) return sign * x;
         const float y = fabsf(__ldg(b + row));
-        return fabsf(x) >= y * 0x1p-20f ? fabsf(x) : y;
+        return fabsf(x) * 0x1p20f >= y ? fabsf(x) : y;   // (the smallest y has no multiple by 2^-20)
     }
 };
 
@@ -340,9 +340,9 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
             }
             float ca = 0.f, cb = 0.f, entropy = 0.f;   // kProbEnt: the gradients in units of the row's weight
             if (MODE == kProbEnt && in) {
-                const float r = p.weight(row), inv = r != 0.f ? 1.f / r : 0.f;
-                ca = __ldg(p.weight.a + row) * inv;
-                cb = __ldg(p.weight.b + row) * inv;
+                const float r = p.weight(row), unit = r != 0.f ? r : 1.f;   // the least weights have no reciprocal
+                ca = __ldg(p.weight.a + row) / unit;
+                cb = __ldg(p.weight.b + row) / unit;
                 entropy = __ldg(p.entropy + row);
             }
             if (MODE == kGrads && c.which == 0) scale = __ldg(p.scale);

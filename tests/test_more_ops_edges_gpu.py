@@ -191,3 +191,35 @@ def test_8_bit_rows_of_any_length(rows, D, dtype):
     want_c = ref.scales(x, 1).float().clamp(min=ref.TINY) / 448
     u = x.cpu().float() / ref.spread(want_c, rows, D, 1).float()
     assert torch.equal(c.cpu(), want_c) and same(q.cpu(), u.clamp(-448, 448).to(torch.float8_e4m3fn))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_log_probability_gradients_below_the_normal_numbers(dtype):
+    """Rows whose gradients lie below 2^-126, where their reciprocals and their small multiples are no fp32 numbers, beside
+    ordinary ones: nothing infinite or NaN comes of them, the other rows' results stay as they are, and their own dh is the
+    formula's.  On the CUDA cores the logits' gradient itself is a multiple of 2^-149 then, three operations of up to half a
+    step each; on the tensor cores it is in units of the row's weight."""
+    gen = torch.Generator().manual_seed(8)
+    T = torch.float32 if dtype == "f32" else torch.bfloat16
+    N, D, V = 40, 32, 300
+    h, w = (0.5 * torch.randn(n, D, generator=gen) for n in (N, V))
+    h, w, t = h.to(T).cuda(), w.to(T).cuda(), torch.randint(0, V, (N,), generator=gen).to(torch.int32).cuda()
+    _, H, lse, _, _ = gdn.linear_log_probs_fwd(h, w, t)
+    small = torch.tensor([1e-39, -2e-40, 2.0 ** -149, 0.0, 0.0, 1e-39])
+    other = torch.tensor([0.0, 1e-39, 2.0 ** -149, 1e-40, 2.0 ** -140, 1e-45])
+    da, db = torch.ones(N), 0.1 * torch.ones(N)
+    da[:6], db[:6] = small, other
+    da, db = da.cuda(), db.cuda()
+    dh, dw = gdn.linear_log_probs_bwd(h, w, t, lse, H, da, db)
+    assert torch.isfinite(dh.float()).all() and torch.isfinite(dw.float()).all() and (dh[:6].float().abs() < 1e-37).all()
+    da0, db0 = da.clone(), db.clone()
+    da0[:6], db0[:6] = 0, 0
+    dh0, dw0 = gdn.linear_log_probs_bwd(h, w, t, lse, H, da0, db0)
+    assert torch.equal(dw, dw0) and torch.equal(dh[6:], dh0[6:]) and (dh0[:6] == 0).all()
+    # a weight larger by what h is smaller leaves the logits and takes dh into the normal numbers
+    up, down = (w.float() * 2.0 ** 60).to(T), (h.float() * 2.0 ** -60).to(T)
+    dh, _ = gdn.linear_log_probs_bwd(down, up, t, lse, H, da, db)
+    want, bound = ref.log_probs_bwd(down, up, t, lse, H, da, db, low_bits=dtype == "bf16")
+    room = bound[0] + (ref.BF16 * want[0].abs() * 1.01 if dtype == "bf16" else 2.0 ** -148 * ref.f64(up).abs().sum(0) + ref.U * want[0].abs())
+    err = (ref.f64(dh) - want[0]).abs()
+    assert (err[:6] <= room[:6]).all(), (err / room.clamp(min=1e-300))[:6].max(-1).values
