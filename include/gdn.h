@@ -460,7 +460,8 @@ gdn_status gdn_fp8_quantize(const void *x, void *q, float *scales, int64_t rows,
  *   cores.
  *   workspace     at least gdn_fp8_linear_workspace_size() bytes, 256-byte aligned; its first 256 bytes hold the device
  *                 error word read by gdn_check_device_error.
- * Sums are fp32, rounded once to bf16.  Results do not depend on timing.  A tensor-core kernel that gives up a wait (after
+ * Sums are fp32, rounded once to bf16.  The product of two scales is fp32 too: where it is infinite, a sum of 0 becomes
+ * NaN.  Results do not depend on timing.  A tensor-core kernel that gives up a wait (after
  * 1 s) leaves NaN in what it should have written, besides the error word.
  * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_CUDA.
  */
