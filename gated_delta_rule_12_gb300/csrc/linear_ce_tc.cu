@@ -400,8 +400,9 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                     // the base keeps infinities and NaN in the sum instead of making them NaN by themselves
                     const float was = isinf(top) ? 0.f : top, now = isinf(higher) ? 0.f : higher;
                     if (top != -INFINITY) {
-                        const float f = __expf(was - now);
-                        if (MODE == kStats) u = f * fmaf(was - now, sum, u);
+                        // words masked by the lowest number lie so far below that the distance times their sum is infinite
+                        const float d = MODE == kStats ? fmaxf(was - now, -1e4f) : was - now, f = __expf(d);
+                        if (MODE == kStats) u = f * fmaf(d, sum, u);
                         sum *= f;
                     }
                     top = higher;
