@@ -323,7 +323,7 @@ cudaError_t fwd(const LinearCeArgs &a, cudaStream_t st, const LogProbs *out)
         });
         const char *w = (const char *)a.workspace;
         const LogProbParts p = {(const RowStat *)(w + ws.part), (const float2 *)(w + ws.best), (const float *)(w + ws.at),
-                                a.targets, nullptr, 1, ws.tiles, a.N, a.V, ws.tiles, out->top_k, PartOrder()};
+                                a.targets, nullptr, a.N, a.V, out->top_k, ws.tiles, PartOrder()};
         const int blocks = ceil_div(a.N, 8);
         if (out->top_k == 0) logp_join_kernel<0><<<blocks, 256, 0, st>>>(p, *out);
         else if (out->top_k <= 8) logp_join_kernel<8><<<blocks, 256, 0, st>>>(p, *out);

@@ -104,8 +104,8 @@ struct CeParams {
     RowWeights weight;
     const float *scale;       // kGrads: s
     float2 *part;             // kLogits: [tiles of 256 words][N]
-    RowStat *stat;            // kStats: [parts][N]
-    float2 *best;             // kStats: [parts][N][top], a logit and its word's bits
+    RowStat *stat;            // kStats: [parts as `order` has them]
+    float2 *best;             // kStats: [the same][top], a logit and its word's bits
     PartOrder order;          // kStats
     unsigned *cut;            // kStats: [N], order_of() of a logit that the row's best words do not fall below; or null
     int top;
@@ -164,6 +164,12 @@ __device__ __forceinline__ Tile tile_of(const CeParams &p, int t)
     return r;
 }
 
+// Where a row's part lies.
+__device__ __forceinline__ int64_t part_of(const CeParams &p, int part, int row)
+{
+    return p.order.first(row) + part * p.order.step(row, p.N);
+}
+
 // NaN in this CTA's half of each of the pair's tiles.
 template <int MODE>
 __device__ __noinline__ void spoil(const CeParams &p, int pair, int pairs, int rank)
@@ -181,7 +187,7 @@ __device__ __noinline__ void spoil(const CeParams &p, int pair, int pairs, int r
             if (MODE == kLogits) {
                 p.part[(int64_t)c.n * p.N + row] = make_float2(nan, nan);
             } else if (MODE == kStats) {
-                p.stat[(int64_t)c.part * p.N + row] = {nan, nan, nan, 0};
+                p.stat[part_of(p, c.part, (int)row)] = {nan, nan, nan, 0};
             } else if (MODE == kProb || MODE == kProbEnt) {
                 static_cast<unsigned short *>(p.out[0])[row * p.pitch + col] = 0x7fff;
             } else if (c.which == 0 || p.direct) {
@@ -322,8 +328,10 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
         BestWords<K ? K : 1> best;
         float cut = -INFINITY;                         // words at or below it are not among the row's best
         bool begins = true;
+        Tile next = tile_of<MODE>(p, pair);
         for (int t = pair; t < p.tiles; t += pairs) {
-            const Tile c = tile_of<MODE>(p, t);
+            const Tile c = next;
+            if (t + pairs < p.tiles) next = tile_of<MODE>(p, t + pairs);
             if (c.k0 >= c.k1) continue;
             const uint32_t buf = tiles & 1, use = tiles >> 1;
             ++tiles;
@@ -358,11 +366,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 cut = -INFINITY;
                 best = BestWords<K ? K : 1>();
             }
-            bool ends = true;
-            if (MODE == kStats && t + pairs < p.tiles) {
-                const Tile next = tile_of<MODE>(p, t + pairs);
-                ends = next.k0 >= next.k1 || next.m != c.m || next.part != c.part;
-            }
+            const bool ends = MODE != kStats || t + pairs >= p.tiles || next.k0 >= next.k1 || next.m != c.m || next.part != c.part;
             begins = ends;
             if (K && other) cut = fmaxf(cut, below(other));
             const bool fresh = K && __any_sync(0xffffffffu, in && cut == -INFINITY);
@@ -557,7 +561,7 @@ ce_tc_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CePara
                 if (lane == 0) arrive_remote(leader_empty + 8 * buf);
             }
             if (MODE == kStats && in && ends) {
-                const int64_t at = (int64_t)c.part * p.N + row;
+                const int64_t at = part_of(p, c.part, row);
                 const int count = K ? best.count(p.top) : 0;
                 p.stat[at] = {top == -INFINITY ? top : (isinf(top) ? 0.f : top), sum, u, count};
                 if (K) {
@@ -713,8 +717,8 @@ PartOrder part_order(int N, int V)
 }
 
 struct TcWorkspace {
-    size_t part, at;          // forward
-    size_t best, cut;         // log probabilities, forward: [tiles of words][N][top], [N]
+    size_t part, at;          // forward: a row's statistics of each tile of words, log probabilities of each part; [N]
+    size_t best, cut;         // log probabilities, forward: the rows' parts' best words (PartOrder), [N]
     // backward: E of a piece [N][piece], h dloss / s of the kept rows [N][D], dh's slices [.][N][D], s
     size_t e, hk, acc, scale;
     size_t total;
@@ -728,7 +732,7 @@ TcWorkspace tc_layout(int N, int D, int V, bool backward, int top = -1)
     TcWorkspace w = {};
     size_t off = 256;
     if (!backward) {
-        const size_t parts = (size_t)N * (top < 0 ? ceil_div(V, kTile) : part_order(N, V).parts);
+        const size_t parts = top < 0 ? (size_t)N * ceil_div(V, kTile) : (size_t)part_order(N, V).total(N);
         w.part = off; off = align256(off + parts * (top < 0 ? sizeof(float2) : sizeof(RowStat)));
         w.at = off;   off = align256(off + (size_t)N * 4);
         w.best = off; off = align256(off + (top > 0 ? parts * top * sizeof(float2) : 0));
@@ -792,7 +796,7 @@ static cudaError_t run_stats(const CeMaps &maps, const CeParams &p, const LogPro
 {
     const cudaError_t e = launch<kStats, K>(maps, p, st, stall);
     if (e != cudaSuccess) return e;
-    const LogProbParts parts = {p.stat, p.best, p.at, p.targets, p.cut, p.N, 1, p.N, p.V, p.order.parts, p.top, p.order};
+    const LogProbParts parts = {p.stat, p.best, p.at, p.targets, p.cut, p.N, p.V, p.top, 0, p.order};
     return launch_early(logp_join_kernel<K>, ceil_div(p.N, 8), 256, 0, st, parts, out);
 }
 

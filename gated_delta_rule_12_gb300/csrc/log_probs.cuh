@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "kernels.h"
+#include "part_order.h"
 
 namespace gdn {
 
@@ -123,90 +124,16 @@ __device__ __forceinline__ void write_best(BestWords<K> &best, int k, float lse,
     }
 }
 
-// Which part a tile of words belongs to where the tensor cores make them.  The row tiles are taken in groups of up to 32 (rows
-// whose h stays in L2; more where words are few), a group's words in windows; a window's tiles, row tile by row tile, are cut into runs of `each` for the
-// pairs of CTAs.  So a pair meets the same rows for several tiles, and their statistics and best words stay in its registers:
-// one part a run, or two where the run passes from one row tile to the next.
-struct PartOrder {
-    struct Group {
-        int rows, window, each, windows, last_window, last_each, rounds;   // rounds: tiles of a pair over the whole group
-    } full, last;
-    int pairs, size, groups;  // a group's row tiles; groups in front of the last one
-    int slots;                // parts a row may have in a window
-    int parts;                // and in all
-
-    static Group group(int rows, int nt, int pairs)
-    {
-        Group g = {};
-        g.rows = rows;
-        const int64_t tiles = (int64_t)rows * nt;
-        g.window = tiles <= 8 * (int64_t)pairs ? nt : 8 * pairs / rows > 0 ? 8 * pairs / rows : 1;
-        g.windows = (nt + g.window - 1) / g.window;
-        g.last_window = nt - (g.windows - 1) * g.window;
-        g.each = (rows * g.window + pairs - 1) / pairs;
-        g.last_each = (rows * g.last_window + pairs - 1) / pairs;
-        g.rounds = (g.windows - 1) * g.each + g.last_each;
-        return g;
-    }
-    static int slots_of(const Group &g)
-    {
-        const int a = (g.window + g.each - 1) / g.each, b = (g.last_window + g.last_each - 1) / g.last_each;
-        return (g.windows > 1 && a > b ? a : b) + 1;
-    }
-    static PartOrder make(int mt, int nt, int pairs)
-    {
-        PartOrder o = {};
-        o.pairs = pairs;
-        o.size = nt >= 19 ? 32 : (8 * pairs + nt - 1) / nt;
-        if (o.size < 32) o.size = 32;
-        o.groups = (mt - 1) / o.size;
-        o.full = group(o.size, nt, pairs);
-        o.last = group(mt - o.size * o.groups, nt, pairs);
-        o.slots = slots_of(o.last);
-        int windows = o.last.windows;
-        if (o.groups) {
-            if (slots_of(o.full) > o.slots) o.slots = slots_of(o.full);
-            if (o.full.windows > windows) windows = o.full.windows;
-        }
-        o.parts = windows * o.slots;
-        return o;
-    }
-    int rounds() const { return groups * full.rounds + last.rounds; }
-
-    // Tile `round` of a pair: its row tile, word tile and part; false where it has none.
-    __device__ __forceinline__ bool at(int pair, int round, int &m, int &n, int &part) const
-    {
-        const int g = min(round / full.rounds, groups);
-        const Group &q = g < groups ? full : last;
-        const int j = round - g * full.rounds, x = min(j / q.each, q.windows - 1);
-        const int wide = x == q.windows - 1 ? q.last_window : q.window, each = x == q.windows - 1 ? q.last_each : q.each;
-        const int i = pair * each + (j - x * q.each), row = i / wide;
-        m = size * g + row;
-        n = x * q.window + i % wide;
-        part = x * slots + pair - row * wide / each;
-        return i < q.rows * wide;
-    }
-    // Whether a row tile has this part.
-    __device__ __forceinline__ bool has(int m, int part) const
-    {
-        const int g = min(m / size, groups), row = m - size * g, x = part / slots;
-        const Group &q = g < groups ? full : last;
-        if (x >= q.windows) return false;
-        const int wide = x == q.windows - 1 ? q.last_window : q.window, each = x == q.windows - 1 ? q.last_each : q.each;
-        return (row * wide / each + part % slots) * each < (row + 1) * wide;
-    }
-};
-
-// The parts of the rows, part n of row r at n * part_step + r * row_step, and its best words, `top` of them, likewise.
+// The parts of the rows, and of each its best words, `top` of them.
 struct LogProbParts {
     const RowStat *stat;
     const float2 *best;       // a logit and its word's bits, best first
     const float *at;          // [N] the targets' logits
     const int32_t *targets;
     const unsigned *cut;      // [N] order_of() of a logit that the row's best words do not fall below (0: none); or null
-    int64_t part_step, row_step;
-    int N, V, parts, top;
-    PartOrder order;          // pairs = 0: every row has all parts
+    int N, V, top;
+    int parts;                // [N][parts] where order.pairs = 0: every row has all of them
+    PartOrder order;          // else as this has them
 };
 
 // Joins a row's parts, a warp a row, in a fixed order; K: the best words that a lane keeps, at least p.top.
@@ -217,8 +144,10 @@ static __global__ void __launch_bounds__(256) logp_join_kernel(LogProbParts p, L
     const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");   // launched beside the kernel that writes the parts
     if (row >= p.N) return;
-    const RowStat *stat = p.stat + row * p.row_step;
-    const int row_tile = (int)(row / 256);
+    const bool ordered = p.order.pairs > 0;
+    const int row_tile = (int)(row / PartOrder::kRows), parts = ordered ? p.order.of(row_tile).parts : p.parts;
+    const int64_t start = ordered ? p.order.first((int)row) : row * p.parts, step = ordered ? p.order.step((int)row, p.N) : 1;
+    const RowStat *stat = p.stat + start;
     const unsigned told = K && p.cut ? p.cut[row] : 0u;
     const float cut = told ? below(told) : -INFINITY;   // the row's best words are above it
     float top = -INFINITY, sum = 0.f, u = 0.f;
@@ -231,14 +160,14 @@ static __global__ void __launch_bounds__(256) logp_join_kernel(LogProbParts p, L
         top = to;
     };
     BestWords<K ? K : 1> best;
-    for (int first = lane; first < p.parts; first += 128) {   // four parts at a time, on their way together
+    for (int first = lane; first < parts; first += 128) {   // four parts at a time, on their way together
         float4 v[4];
         bool in[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int i = first + 32 * j;
-            in[j] = i < p.parts && (p.order.pairs == 0 || p.order.has(row_tile, i));
-            v[j] = in[j] ? *reinterpret_cast<const float4 *>(stat + i * p.part_step) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            in[j] = i < parts && (!ordered || p.order.has(row_tile, i));
+            v[j] = in[j] ? *reinterpret_cast<const float4 *>(stat + i * step) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -246,7 +175,7 @@ static __global__ void __launch_bounds__(256) logp_join_kernel(LogProbParts p, L
             join(v[j].x, v[j].y, v[j].z);
             if (K && !(v[j].x < cut && v[j].y < INFINITY)) {   // (an infinite maximum, 0 here, leaves an infinite sum)
                 const int count = __float_as_int(v[j].w);
-                const float2 *words = p.best + ((first + 32 * j) * p.part_step + row * p.row_step) * p.top;
+                const float2 *words = p.best + (start + (first + 32 * j) * step) * p.top;
                 for (int c = 0; c < count; c += 4) {
                     float2 w[4];
 #pragma unroll

@@ -531,8 +531,8 @@ gdn_status gdn_linear_cross_entropy_bwd(const void *h, const void *weight, const
  *                 logits by the lower index.  0 <= top_k <= GDN_MOST_TOP, top_k <= V; NULL with top_k = 0.  Words whose
  *                 logit is -inf or NaN are none; where too few others are left, ids are -1 and log probabilities -inf.
  *   workspace     at least gdn_linear_log_probs_workspace_size(..., backward = 0) bytes, 256-byte aligned (at
- *                 most about N V (2 + top_k) / 32 bytes, on the CUDA cores twice that); its first 256 bytes as those of the cross
- *                 entropy's.
+ *                 most N (V / 256 + 2) (16 + 8 top_k) + 8 N bytes and 2 KB, on the CUDA cores with V / 128; some 40 MB for 8192
+ *                 tokens, 32768 words and twenty alternatives); its first 256 bytes as those of the cross entropy's.
  * Sizes, types, precision, waits and errors as gdn_linear_cross_entropy_fwd.
  */
 #define GDN_MOST_TOP 20
