@@ -9,7 +9,7 @@
 // The last group may have fewer row tiles than the others, down to one.  Its windows are wider then and its rows' runs are of
 // more pairs, so each of the two kinds has its own number of parts a row (32 row tiles and 32768 words: 28), those of the last
 // group's rows behind the others'.  One number for all rows, the most windows times the most slots, took 455 for 8193 tokens,
-// 16 times the memory of 8192, and the join 5 to 26 % of the call.  A row has at most one part more than there are tiles of words.
+// 16 times the memory of 8192, and calls 5 to 26 % longer.  A row has at most one part more than there are tiles of words.
 #pragma once
 
 #include <stdint.h>

@@ -363,7 +363,8 @@ gdn_status gdn_gated_scan_step(float *state, const void *x, const void *g, void 
  *   weight, bias  [D] fp32, or NULL for 1 and 0.
  *   mean, rstd    [rows] fp32, or NULL to skip; the backward pass needs them.
  *   rows >= 0, D >= 1, rows * D <= 2^48, eps >= 0; pointers aligned to their element size (x and out that start on
- *   16-byte boundaries take the fast path up to D = 16384, whatever D is).
+ *   16-byte boundaries take the fast path up to D = 16384 where rows are whole 16-byte units, else up to 16377 (bf16) or
+ *   16381 (fp32)).
  * Statistics are fp32, the variance from the deviations from the mean.
  * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
  */
@@ -397,7 +398,8 @@ gdn_status gdn_layer_norm_bwd(const void *dout, const void *x, const float *mean
  *   weight        [D] fp32, or NULL for 1.
  *   rstd          [rows] fp32, or NULL to skip; the backward pass needs it.
  *   rows >= 0, D >= 1, rows * D <= 2^48, eps >= 0; pointers aligned to their element size (tensors that start on
- *   16-byte boundaries take the fast path up to D = 16384, whatever D is).
+ *   16-byte boundaries take the fast path up to D = 16384 where rows are whole 16-byte units, else up to 16377 (bf16) or
+ *   16381 (fp32)).
  * Statistics are fp32.
  * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_CUDA.
  */
