@@ -6,7 +6,8 @@
 // Rows that 16-byte accesses do not fit go element by element.
 //
 // Measured (GB300, device time): 8192 x 2048 bf16 10.2 us, 5.0 TB/s (four blocks of a thread on their way instead of two 11.8,
-// eight 12.5 to 13.1; a CTA for each two instead of a grid that stays 10.5).
+// eight 12.5 to 13.1; a CTA for each two instead of a grid that stays 10.5); fp32 17.1 us, 4.9 TB/s.  Weights of 6144 x 2048, a
+// CTA a block: bf16 12.8 us, 3.0 TB/s, fp32 12.4, 5.1.
 #include "common.cuh"
 #include "fp8.cuh"
 #include "kernels.h"

@@ -10,7 +10,9 @@
 // with the entropy's gradient in G.
 //
 // These kernels run on the CUDA cores: fp32, and bf16 whose rows are no multiple of 16 bytes; other bf16 sizes take the
-// tensor cores (linear_ce_tc.cu).  Bound by the fp32 units.
+// tensor cores (linear_ce_tc.cu).  Bound by the fp32 units where there are tiles for all SMs.  Measured (GB300, device time, fp32):
+// 512 x 512 x 4096 loss 72 us (30 TFLOP/s), log probabilities 74, with five alternatives 84; 255 x 1024 x 50257 with eight 794 us
+// (33).  Gradients 0.68 ms and 8.8 ms (9 TFLOP/s): dh of a piece has 16 tiles at these sizes.
 //
 // Forward: each 128 x 128 tile of logits leaves one (max, sum of exponentials) pair a row, joined by a second
 // kernel in the order of the tiles.  Backward: the vocabulary is taken in pieces; a piece's G is recomputed into

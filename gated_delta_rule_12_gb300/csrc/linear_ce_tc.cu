@@ -28,8 +28,10 @@
 //
 // The log probabilities are the same products: their forward pass adds the entropy's sum to a row's statistics and keeps a
 // row's best words (log_probs.cuh), their gradient is another E.  8192 x 2048 x 32768 0.50 ms without alternatives, 0.54 with
-// five and 0.65 with twenty; 255 x 1024 x 50257 28, 47 (eight) and 89 us: a row's first tile costs the epilogue some 6 us (16
-// with twenty), one word after another out of each of 32 rows, which only products of a few thousand terms cover.
+// five and 0.64 with twenty; 255 x 1024 x 50257 28, 46 (eight) and 88 us: a row's first tile costs the epilogue some 6 us (16
+// with twenty), one word after another out of each of 32 rows, which only products of a few thousand terms cover.  Over short
+// rows of h the epilogue is all that counts: 8192 x 256 x 32768 0.22 ms without alternatives, 0.39 with five, 0.56 with twenty,
+// where the products take 0.072.
 //
 // Bound by the tensor cores, or by reading w where tokens are few.  Measured on the device: loss of 8192 x 2048 x 32768
 // 0.54 ms (2.0 PFLOP/s), gradient with 65536 words 3.6 ms (1.83 PFLOP/s); both run into the power limit when repeated
